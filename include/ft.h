@@ -179,6 +179,97 @@ int ft_kv_unpack_int4(const ft_block_cfg *cfg, const void *cache, int max_batch,
                       int len, uint8_t *k_codes, uint8_t *v_codes, uint16_t *k_scales,
                       uint16_t *v_scales, ft_stream stream);
 
+/* ---- paged KV cache -----------------------------------------------------
+ * One layer's cache as a pool of pages that requests share: page i holds
+ * page_size positions (16, 32, 64 or 128) of every KV head, and a request's
+ * block table names its pages in order.  A slot is page * page_size + offset.
+ * Rotation and quantiser are those of ft_kv_append_int4 (codes -7..7; -8 never
+ * occurs), so a row has the same codes and scales in either cache.  Layout of a
+ * page (P = page_size, d = head_dim): n_kv head blocks of P (d + 4) bytes, each
+ *   P K entries of d/2 bytes, P/2 V entries of d bytes (positions 2i, 2i + 1),
+ *   P pairs of BF16 (K scale, V scale).
+ * Values are sign and magnitude, four to a 16-bit word; word (g, j) of a
+ * position, g < 8, j < d/32, holds channels 32 j + g + 8 e, e = 0..3, with
+ * magnitudes at bits 0, 3, 8, 11 and signs at bits 15, 14, 7, 6.  Its byte is
+ *   K, offset p:  p d/2 + (g / 2) d/8 + 4 j + 2 (g % 2)
+ *   V, pair i:    i d + (g XOR turn(i)) d/8 + 4 j + 2 (offset % 2),
+ *                 turn(i) = 2 (i % 4) for d = 128, 4 ((i / 2) % 2) for d = 64.
+ * The pool is 16-byte aligned; all offsets are 64-bit. */
+
+/* Bytes of a pool of n_pages pages; 0 for an invalid configuration. */
+size_t ft_kv_pages_bytes(const ft_block_cfg *cfg, int n_pages, int page_size);
+
+/* Block tables, slot map and prefix sums of one step, built on the device from
+ * the requests' lengths (no host round trip; can be captured and replayed).
+ *   ctx_len, new_len: int32 [B], tokens that request b has in the cache and
+ *     tokens that it adds.
+ *   block_table: int32 [B, table_stride]; entries of pages that already hold
+ *     tokens (ceil(ctx_len / page_size) of them) are read, those of the pages
+ *     added are written, the others are left as they are.
+ *   free_pages: int32 [n_free]; the pages added are free_pages[head], head + 1,
+ *     ... in request order, with head = *free_head (NULL: 0).
+ *   free_head_out: int32, head + pages taken (NULL: not written).
+ *   cu_seqlens: int32 [B + 1], prefix sums of new_len.  kv_len: int32 [B],
+ *     ctx_len + new_len.
+ *   slots: int32 [n_slots]; slot of row i (request b, position ctx_len[b] + i -
+ *     cu_seqlens[b]); -1 for rows behind the last one.
+ * kv_len may be ctx_len and free_head_out may be free_head (advanced in place);
+ * no other arguments may overlap.  A request with a negative length, more
+ * positions than its table row holds, or whose new pages end behind the free
+ * list sets FT_DEV_CAPACITY and is not served: its rows get slot -1, its kv_len
+ * is 0 and its table row is left alone (pages are counted in request order, also
+ * those of requests that did not get them).  More rows than n_slots, a head
+ * outside [0, n_free] or a page outside [0, n_pages) set FT_DEV_RANGE; such rows
+ * are dropped (slot -1).  B <= 8192, else FT_ERR_UNSUPPORTED. */
+int ft_kv_page_map(int page_size, int n_pages, const int32_t *ctx_len, const int32_t *new_len, int B,
+                   int32_t *block_table, int table_stride, const int32_t *free_pages, int n_free,
+                   const int32_t *free_head, int32_t *free_head_out, int32_t *cu_seqlens, int32_t *kv_len,
+                   int32_t *slots, int n_slots, int32_t *dev_status, ft_stream stream);
+
+/* Rotate, quantise and place `total` rows at their slots.  k_bf16, v_bf16: BF16
+ * bits, row t at t * stride (strides in elements, >= n_kv d; a view of the fused
+ * projection's output works), [n_kv, d] inside a row, post-RoPE.  slots: int32
+ * [total]; -1 skips the row, any other slot outside the pool sets FT_DEV_RANGE
+ * and skips it.  The slots of one call must be distinct.  A row whose rotated
+ * values are not finite sets FT_DEV_RANGE; what it stores is not defined. */
+int ft_kv_append_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pages, int page_size, const uint16_t *k_bf16,
+                            int64_t k_stride, const uint16_t *v_bf16, int64_t v_stride, const int32_t *slots, int total,
+                            int32_t *dev_status, ft_stream stream);
+
+/* Reads rows back as values in the model basis (decoded, the rotation undone,
+ * rounded to BF16): k_out, v_out BF16 bits [total, n_kv, d].  Slot -1 gives zeros;
+ * any other slot outside the pool gives zeros and sets FT_DEV_RANGE. */
+int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, int page_size, const int32_t *slots,
+                          int total, uint16_t *k_out, uint16_t *v_out, int32_t *dev_status, ft_stream stream);
+
+/* Attention of the new tokens of B requests over the paged cache (their own K/V
+ * appended before): prompts, chunks of prompts, drafts of a few tokens and single
+ * tokens, in any mixture.  Token i of request b (row cu_seqlens[b] + i) is at
+ * position kv_len[b] - n_b + i, n_b = cu_seqlens[b + 1] - cu_seqlens[b], and
+ * attends to positions 0 .. its own:
+ *   o = H softmax(scale * (H q) . K^) V^,   query head h reads KV head h / G.
+ * q_bf16, o_bf16: BF16 bits, row t at t * stride (elements, >= n_q d), [n_q, d]
+ * inside a row, q post-RoPE; o may be q where the strides are equal.  A token at
+ * a negative position (kv_len < n_b) sees nothing and gets zeros.  Rows behind
+ * cu_seqlens[B] are left as they are.  max_q: an upper bound of n_b; it picks the
+ * kernel and sizes the launch.
+ * Arithmetic: q rounded to FP16 after the rotation (|q scale log2(e)| < 1023, else
+ * FT_DEV_RANGE), codes exact, softmax weights rounded to FP16 below the products,
+ * sums and statistics in FP32.  V scales below 2^-100 count as 2^-100.  Entries
+ * behind a token's position may hold anything.  What a request's rows are does not
+ * depend on the other requests of the call, up to the order of FP32 sums.
+ * Device conditions: cu_seqlens not ascending within [0, total_q], or n_b > max_q:
+ * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative or
+ * longer than table_stride pages: FT_DEV_CAPACITY, zeros; a page outside the pool:
+ * FT_DEV_RANGE, its positions count as masked.
+ * The workspace (16-byte aligned) holds partial results during the call only; calls
+ * that may run at the same time need one each. */
+size_t ft_attn_paged_workspace_bytes(const ft_block_cfg *cfg, int B, int total_q, int max_q);
+int ft_attn_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, int page_size, const uint16_t *q_bf16,
+                       int64_t q_stride, const int32_t *cu_seqlens, const int32_t *kv_len, const int32_t *block_table,
+                       int table_stride, int B, int total_q, int max_q, float scale, uint16_t *o_bf16, int64_t o_stride,
+                       void *workspace, size_t ws_bytes, int32_t *dev_status, ft_stream stream);
+
 /* ---- the decode block ---------------------------------------------------
  * One token per request b < B at position pos[b] (= L_b, its history length):
  *   rho1 = (mean x^2 + eps)^-1/2;  [q;k;v] = rho1 * W'_qkv x      (row factor
@@ -291,6 +382,21 @@ int ft_read_device_status(const int32_t *dev_status, int32_t *host_out, ft_strea
  * chunk).  z enters the tensor cores as a BF16 (hi, lo) pair. */
 int ft_lm_head_bf16(const float *x, const float *gamma, const uint16_t *W, float *logits, int B, int V, int H,
                     float eps, ft_stream stream);
+
+/* Log probabilities of given tokens from logits [N, V] (FT_F32 or FT_BF16, row i at
+ * i * row_stride elements, e.g. those of ft_lm_head_bf16):
+ *   logprob[i] = x[target] - log sum exp x;   entropy[i] = - sum p log p (nats);
+ *   rank[i] = number of tokens before the target, by value and then lower index;
+ *   top_ids, top_logprobs [N, top_k]: the top_k first ones in that order.
+ * Any output pointer may be NULL (top_k = 0: no alternatives); targets may be NULL
+ * where neither logprob nor rank is asked for.  Masked logits are -infinity.  A
+ * target of -1 means none: logprob 0, rank -1; any other outside [0, V) gives NaN
+ * and -1 and sets FT_DEV_RANGE.  A row with a NaN or +infinity, or with nothing above
+ * -infinity, gives NaN (ids and rank -1) and sets FT_DEV_RANGE.  All sums in FP32.
+ * top_k <= min(32, V), else FT_ERR_UNSUPPORTED. */
+int ft_logprobs(const void *logits, int dtype, int64_t row_stride, int N, int V, const int32_t *targets, int top_k,
+                float *logprob, float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
+                int32_t *dev_status, ft_stream stream);
 
 /* ft_decode_block without a caller-provided workspace.  The FuTransformer paper
  * has no counterpart to this call; it exists for callers that cannot allocate
