@@ -628,7 +628,7 @@ def test_two_streams_with_their_own_workspaces():
 
 def test_binding_refuses_what_it_cannot_pass():
     a = Attn(8, 2, 128, 64, [3], [10])
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ft.ft_attn_paged_workspace_bytes(a.cfg, 1, 3, 3), dtype=torch.uint8, device="cuda")
     o = torch.empty((3, 8, 128), dtype=torch.bfloat16, device="cuda")
     call = lambda q=a.q, kv=_i32([10]), pool=a.pool, out=o: ft.ft_attn_paged_int4(  # noqa: E731
         a.cfg, pool, a.n_pages, 64, q, _i32([0, 3]), kv, _i32(a.table), 1, 3, 3, 0.1, out, ws)
