@@ -4,16 +4,29 @@
 //   m = max x, z = sum 2^((x - m) log2 e):  log z + m is the normaliser,
 //   entropy = log z - sum e (x - m) / z.
 //
-// One CTA per row.  Alternatives are ordered by a 64-bit key (the value as an ordered
-// integer, then the lower index), so ties have one answer whatever order the row is
-// read in.
+// A cluster of CTAs per row, each streaming a slice once with 16-byte loads, the next
+// round's in flight while one is used: running maximum, sum and weighted sum per thread
+// (a moved maximum rescales them), the target's rank counted by comparison, and the
+// alternatives filtered through a threshold: only elements above the k-th best so far
+// reach a shared list, which is cut back to k when it passes kKeep.  The first threshold
+// is the k-th largest of the threads' first maxima, so few elements pass even then.
+// CTA 0 joins the slices through distributed shared memory: one launch, no workspace.
+// Bound by HBM for many rows; a single row by its latency, hence up to 16 CTAs for it.
+//
+// Alternatives are ordered by a 64-bit key (the value as an ordered integer, then the
+// lower index), so ties have one answer whatever order the row is read in.
 #include <algorithm>
 
 #include "ft_internal.cuh"
 
 namespace ft {
 
-constexpr int kLpThreads = 512, kLpMaxTop = 32;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpMaxTop = 32, kLpMaxCluster = 16;
+constexpr int kLpElems = 16;                              // elements of one thread in one round
+constexpr int kLpKeep = 256;                              // listed alternatives before a cut
+constexpr int kLpList = kLpThreads * kLpElems + kLpKeep;  // all of a round may pass
+constexpr int kLpSel = kLpMaxTop * (kLpList / kLpThreads + 1);
+constexpr float kLog2e = 1.44269504088896341f;
 
 struct LogprobParams {
   const void* x;
@@ -24,85 +37,384 @@ struct LogprobParams {
   int V, top;
 };
 
-template <bool BF16>
-__device__ __forceinline__ float lp_load(const void* x, int64_t i) {
-  if (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(x)[i]);
-  return static_cast<const float*>(x)[i];
-}
-// Larger key: larger value (-0 = +0), then lower index.
-__device__ __forceinline__ unsigned long long lp_key(float v, int i) {
+typedef unsigned long long lp_key_t;
+
+__device__ __forceinline__ uint32_t lp_order(float v) {  // -0 = +0
   const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return ((unsigned long long)o << 32) | (uint32_t)~i;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float lp_key_value(unsigned long long k) {
+// Larger key: larger value, then lower index.
+__device__ __forceinline__ lp_key_t lp_key(float v, int i) { return ((lp_key_t)lp_order(v) << 32) | (uint32_t)~i; }
+__device__ __forceinline__ float lp_key_value(lp_key_t k) {
   const uint32_t o = (uint32_t)(k >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
+__device__ __forceinline__ float lp_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-template <typename T, typename F>
-__device__ __forceinline__ T lp_block_reduce(T v, F op, T* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (lane == 0) sh[warp] = v;
+// Running statistics: maximum m, z = sum e^d, u = sum e^d d, d = x - m (m itself is not scaled by
+// log2 e, which would overflow for logits near FP32's largest).
+struct LpStat {
+  float m, z, u;
+  __device__ __forceinline__ void move(float to) {  // to >= m
+    if (m == -INFINITY) {
+      m = to;  // z = u = 0
+    } else if (to != m) {
+      const float f = lp_ex2((m - to) * kLog2e);
+      u = f == 0.0f ? 0.0f : f * fmaf(m - to, z, u);
+      z *= f;
+      m = to;
+    }
+  }
+  __device__ __forceinline__ void join(LpStat o) {
+    const float to = fmaxf(m, o.m);
+    move(to);
+    o.move(to);
+    z += o.z;
+    u += o.u;
+  }
+};
+
+struct LpShared {
+  lp_key_t list[kLpList], sel[kLpSel], best[kLpMaxTop];
+  lp_key_t inbox[kLpMaxCluster * kLpMaxTop];  // CTA 0: the slices' best
+  float4 stat[kLpMaxCluster];                 // CTA 0: the slices' (m, z, u, rank)
+  __align__(16) float first[kLpThreads];
+  float4 wstat[kLpWarps];
+  lp_key_t tau;
+  int count, nsel;
+};
+
+// The k largest of list[0 .. n), in order, to best[]; the list then holds them.  All threads.
+__device__ __forceinline__ void lp_cut(LpShared& s, lp_key_t* list, int n, int k) {
+  const int tid = threadIdx.x;
+  const lp_key_t* from = list;
+  if (n > kLpSel) {
+    // the k-th largest of the threads' maxima bounds the k-th largest from below; only the
+    // k threads at or above it hold keys that pass
+    lp_key_t mx = 0;
+    for (int i = tid; i < n; i += kLpThreads) mx = max(mx, list[i]);
+    s.sel[tid] = mx;
+    if (tid == 0) s.nsel = 0;
+    __syncthreads();
+    int above = 0;
+    for (int i = 0; i < kLpThreads; ++i) above += s.sel[i] > mx;
+    if (above == k - 1) s.tau = mx;
+    __syncthreads();
+    const lp_key_t t = s.tau;
+    for (int i = tid; i < n; i += kLpThreads)
+      if (list[i] >= t) s.sel[atomicAdd(&s.nsel, 1)] = list[i];
+    __syncthreads();
+    n = s.nsel;
+    from = s.sel;
+  }
+  for (int i = tid; i < n; i += kLpThreads) {
+    const lp_key_t mine = from[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += from[j] > mine;
+    if (above < k) s.best[above] = mine;
+  }
   __syncthreads();
-  v = sh[0];
-  for (int w = 1; w < kLpThreads / 32; ++w) v = op(v, sh[w]);
+  for (int i = tid; i < min(n, k); i += kLpThreads) list[i] = s.best[i];
+  if (tid == 0) {
+    s.count = min(n, k);
+    s.tau = n >= k ? s.best[k - 1] : 0;
+  }
   __syncthreads();
-  return v;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobParams p) {
-  __shared__ float shf[kLpThreads / 32];
-  __shared__ unsigned long long shk[kLpThreads / 32];
-  const int tid = threadIdx.x, V = p.V;
-  const int64_t row = blockIdx.x, at = row * p.stride;
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobParams p) {
+  constexpr int E = BF16 ? 8 : 4, U = kLpElems / E;  // elements of a 16-byte vector, vectors of a round
+  extern __shared__ __align__(16) uint8_t lp_smem[];
+  LpShared& s = *reinterpret_cast<LpShared*>(lp_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = p.V, top = p.top;
+  uint32_t rank_in, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_in));
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
+  const int64_t row = blockIdx.x / ctas;
+  if (ctas > 1) cluster_arrive();  // paired with the wait before the first store to CTA 0
+  const uint8_t* base = static_cast<const uint8_t*>(p.x) + row * p.stride * (BF16 ? 2 : 4);
+  auto at = [&](int i) {
+    return BF16 ? bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i))
+                : __ldg(reinterpret_cast<const float*>(base) + i);
+  };
   const int t = p.target ? p.target[row] : -1;
   const bool has = t >= 0 && t < V;
-  const float xt = has ? lp_load<BF16>(p.x, at + t) : 0.0f;
-  const auto fadd = [](float a, float b) { return a + b; };
-  float m = -INFINITY, nan = 0.0f;
-  for (int i = tid; i < V; i += kLpThreads) {
-    const float v = lp_load<BF16>(p.x, at + i);
-    m = fmaxf(m, v);
-    if (!(v < INFINITY)) nan = 1.0f;
+  const float xt = has ? at(t) : INFINITY;  // without a target nothing is before it
+  // vector v holds elements v E - lead .. + E - 1, 16-byte aligned; the first and the last may be partial
+  const int lead = (int)((reinterpret_cast<uintptr_t>(base) & 15u) / (BF16 ? 2 : 4));
+  const uint8_t* vec0 = base - lead * (BF16 ? 2 : 4);
+  const int nvec = (lead + V + E - 1) / E;
+  const int v0 = (int)((int64_t)nvec * rank_in / ctas), v1 = (int)((int64_t)nvec * (rank_in + 1) / ctas);
+  LpStat st = {-INFINITY, 0.0f, 0.0f};
+  int above = 0;
+  if (tid == 0) {
+    s.count = 0;
+    s.tau = 0;
   }
-  m = lp_block_reduce(m, [](float a, float b) { return fmaxf(a, b); }, shf);
-  nan = lp_block_reduce(nan, fadd, shf);
-  const bool bad = nan > 0.0f || m == -INFINITY;  // a NaN or +infinity, or nothing that is possible
-  float z = 0.0f, u = 0.0f, above = 0.0f;
-  for (int i = tid; i < V && !bad; i += kLpThreads) {
-    const float v = lp_load<BF16>(p.x, at + i), d = fmaxf(v - m, -1e4f), e = expf(d);
-    z += e;
-    u = fmaf(e, d, u);
-    above += (v > xt || (v == xt && i < t)) ? 1.0f : 0.0f;
+
+  // 16-byte vectors, or their elements inside the row at its ends; the others -infinity
+  auto fetch = [&](int r, uint4 (&q)[U]) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = r + i * kLpThreads + tid;
+      const int e0 = v * E - lead;
+      if (v < v1 && e0 >= 0 && e0 + E <= V) {
+        q[i] = ld_stream_v4(vec0 + (size_t)v * 16);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = BF16 ? 0xFF80FF80u : 0xFF800000u;
+        if (v < v1) {
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            if (e0 + k < 0 || e0 + k >= V) continue;
+            if (BF16) {
+              const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(base) + e0 + k);
+              w[k / 2] = (k & 1) ? (w[k / 2] & 0xFFFFu) | (h << 16) : (w[k / 2] & 0xFFFF0000u) | h;
+            } else {
+              w[k % 4] = __ldg(reinterpret_cast<const uint32_t*>(base) + e0 + k);
+            }
+          }
+        }
+        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+  float tau = -INFINITY;      // value of the threshold: nothing below it can be an alternative
+  lp_key_t tau_key = 0;       // keys must be above this
+  bool full = false;          // this thread saw the list past kLpKeep
+  auto use = [&](int r, const uint4 (&q)[U], bool filter) {
+    float x[kLpElems];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        x[i * E + k] = BF16 ? __uint_as_float((k & 1) ? (w[k / 2] & 0xFFFF0000u) : (w[k / 2] << 16))
+                            : __uint_as_float(w[k % 4]);
+    }
+    float bm = x[0];
+#pragma unroll
+    for (int k = 1; k < kLpElems; ++k) bm = fmaxf(bm, x[k]);
+    if (bm > st.m) st.move(bm);
+    const float m = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+    for (int k = 0; k < kLpElems; ++k) {
+      const float d = x[k] - m, e = lp_ex2(d * kLog2e);
+      st.z += e;                                // a NaN or +infinity stays in z
+      st.u = fmaf(e, fmaxf(d, -1000.0f), st.u);  // 0 x -infinity of a masked logit is 0
+    }
+    if (has) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int e0 = (r + i * kLpThreads + tid) * E - lead;
+        if (e0 > t) {
+#pragma unroll
+          for (int k = 0; k < E; ++k) above += x[i * E + k] > xt;
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const float v = x[i * E + k];
+            above += (v > xt || (v == xt && e0 + k < t)) && e0 + k >= 0 && r + i * kLpThreads + tid < v1;
+          }
+        }
+      }
+    }
+    if (filter && bm >= tau) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int v = r + i * kLpThreads + tid;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const int e = v * E - lead + k;
+          if (x[i * E + k] >= tau && v < v1 && e >= 0 && e < V) {
+            const lp_key_t key = lp_key(x[i * E + k], e);
+            if (key > tau_key) {
+              const int n = atomicAdd(&s.count, 1);
+              if (n < kLpList) s.list[n] = key;
+              full |= n >= kLpKeep;
+            }
+          }
+        }
+      }
+    }
+    return bm;
+  };
+
+  uint4 cur[U], nxt[U];
+  constexpr int kStep = U * kLpThreads;
+  fetch(v0, cur);
+  if (top > 0) {
+    if (v0 + kStep < v1) fetch(v0 + kStep, nxt);
+    s.first[tid] = use(v0, cur, false);
+    __syncthreads();
+    int over = 0, ties = 0;
+    const float mine = s.first[tid];
+#pragma unroll 4
+    for (int i = 0; i < kLpThreads; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(s.first + i);
+      over += (f.x > mine) + (f.y > mine) + (f.z > mine) + (f.w > mine);
+      ties += (f.x == mine && i < tid) + (f.y == mine && i + 1 < tid) + (f.z == mine && i + 2 < tid) +
+              (f.w == mine && i + 3 < tid);
+    }
+    if (over + ties == top - 1) s.tau = (lp_key_t)lp_order(mine) << 32;  // below every key of this value
+    __syncthreads();
+    tau_key = s.tau;
+    tau = tau_key ? lp_key_value(tau_key) : -INFINITY;
+    // the first round again, for the list only
+    {
+      float x[kLpElems];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+        const int v = v0 + i * kLpThreads + tid;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          x[k] = BF16 ? __uint_as_float((k & 1) ? (w[k / 2] & 0xFFFF0000u) : (w[k / 2] << 16)) : __uint_as_float(w[k % 4]);
+          const int e = v * E - lead + k;
+          if (x[k] >= tau && v < v1 && e >= 0 && e < V) {
+            const int n = atomicAdd(&s.count, 1);
+            s.list[n] = lp_key(x[k], e);
+            full |= n >= kLpKeep;
+          }
+        }
+      }
+    }
+    for (int r = v0 + kStep; r < v1; r += kStep) {
+      if (__syncthreads_or(full)) {
+        lp_cut(s, s.list, s.count, top);
+        tau_key = s.tau;
+        tau = tau_key ? lp_key_value(tau_key) : -INFINITY;
+        full = false;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) cur[i] = nxt[i];
+      if (r + kStep < v1) fetch(r + kStep, nxt);
+      use(r, cur, true);
+    }
+    __syncthreads();
+    lp_cut(s, s.list, s.count, top);
+  } else {
+    for (int r = v0; r < v1; r += kStep) {
+      if (r + kStep < v1) fetch(r + kStep, nxt);
+      use(r, cur, false);
+#pragma unroll
+      for (int i = 0; i < U; ++i) cur[i] = nxt[i];
+    }
   }
-  z = lp_block_reduce(z, fadd, shf);
-  u = lp_block_reduce(u, fadd, shf);
-  above = lp_block_reduce(above, fadd, shf);
-  const float lz = logf(z), lse = m + lz, nanv = __int_as_float(0x7FC00000);
+
+  // ---- the CTA's statistics, in warp order
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpStat b;
+    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    b.z = __shfl_xor_sync(0xffffffffu, st.z, o);
+    b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
+    st.join(b);
+    above += __shfl_xor_sync(0xffffffffu, above, o);
+  }
+  if (lane == 0) s.wstat[warp] = make_float4(st.m, st.z, st.u, __int_as_float(above));
+  __syncthreads();
+  const int n_best = top > 0 ? s.count : 0;
+  if (ctas > 1) cluster_wait();
+  if (tid == 0) {
+    LpStat all = {-INFINITY, 0.0f, 0.0f};
+    int cnt = 0;
+    for (int w = 0; w < kLpWarps; ++w) {
+      const float4 q = s.wstat[w];
+      LpStat b = {q.x, q.y, q.z};
+      all.join(b);
+      cnt += __float_as_int(q.w);
+    }
+    const float4 q = make_float4(all.m, all.z, all.u, __int_as_float(cnt));
+    uint32_t dst;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&s.stat[rank_in])));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(q.x), "f"(q.y), "f"(q.z), "f"(q.w)
+                 : "memory");
+  }
+  if (tid < top) {
+    uint32_t dst;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&s.inbox[rank_in * top + tid])));
+    const lp_key_t key = tid < n_best ? s.best[tid] : 0ull;
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(key) : "memory");
+  }
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (rank_in != 0) return;
+
+  // ---- CTA 0: the slices joined in order
+  LpStat all = {-INFINITY, 0.0f, 0.0f};
+  int cnt = 0;
+  for (uint32_t c = 0; c < ctas; ++c) {
+    const float4 q = s.stat[c];
+    LpStat b = {q.x, q.y, q.z};
+    all.join(b);
+    cnt += __float_as_int(q.w);
+  }
+  const bool bad = !(all.z > 0.0f && all.z < INFINITY);  // a NaN or +infinity, or nothing that is possible
+  const float lz = logf(all.z), mx = all.m, nanv = __int_as_float(0x7FC00000);
+  auto logp = [&](float v) { return (v - mx) - lz; };
   if (tid == 0) {
     if (bad || (t != -1 && !has)) set_status(p.status, FT_DEV_RANGE);
-    if (p.logprob) p.logprob[row] = t == -1 ? 0.0f : (bad || !has) ? nanv : xt - lse;
-    if (p.entropy) p.entropy[row] = bad ? nanv : lz - u / z;
-    if (p.rank) p.rank[row] = (bad || !has) ? -1 : (int)above;
+    if (p.logprob) p.logprob[row] = t == -1 ? 0.0f : (bad || !has) ? nanv : logp(xt);
+    if (p.entropy) p.entropy[row] = bad ? nanv : lz - all.u / all.z;
+    if (p.rank) p.rank[row] = (bad || !has) ? -1 : cnt;
   }
-  unsigned long long prev = ~0ull;
-  for (int k = 0; k < p.top; ++k) {
-    unsigned long long best = 0ull;
-    for (int i = tid; i < V && !bad; i += kLpThreads) {
-      const unsigned long long key = lp_key(lp_load<BF16>(p.x, at + i), i);
-      if (key < prev && key > best) best = key;
+  if (top > 0) {
+    if (ctas > 1) lp_cut(s, s.inbox, (int)ctas * top, top);
+    if (tid < top) {
+      const lp_key_t key = s.best[tid];
+      p.top_id[row * top + tid] = bad ? -1 : (int)~(uint32_t)key;
+      p.top_val[row * top + tid] = bad ? nanv : logp(lp_key_value(key));
     }
-    best = lp_block_reduce(best, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; }, shk);
-    if (tid == 0) {
-      p.top_id[row * p.top + k] = bad ? -1 : (int)~(uint32_t)best;
-      p.top_val[row * p.top + k] = bad ? nanv : lp_key_value(best) - lse;
-    }
-    prev = best;
   }
+}
+
+// CTAs per row: enough for four on every SM, of at least one round each.
+static int lp_cluster(int N, int V) {
+  int sms = ft_host::num_sms();
+  if (sms <= 0) sms = 152;
+  const int rounds = (V + kLpThreads * kLpElems - 1) / (kLpThreads * kLpElems);
+  int c = 1;
+  while (c < kLpMaxCluster && 2 * c <= rounds && (int64_t)N * c < (int64_t)4 * sms) c *= 2;
+  return c;
+}
+
+template <bool BF16>
+static cudaError_t launch_logprobs(const LogprobParams& p, int N, cudaStream_t st) {
+  static int allowed[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!allowed[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(LpShared));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(logprobs_kernel<BF16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    allowed[dev] = 1;
+  }
+  const int ctas = lp_cluster(N, p.V);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)N * ctas));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = sizeof(LpShared);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<BF16>, p);
 }
 
 }  // namespace ft
@@ -130,11 +442,9 @@ int ft_logprobs(const void* logits, int dtype, int64_t row_stride, int N, int V,
   p.status = dev_status;
   p.V = V;
   p.top = top_k;
-  if (dtype == FT_BF16)
-    ft::logprobs_kernel<true><<<N, ft::kLpThreads, 0, (cudaStream_t)stream>>>(p);
-  else
-    ft::logprobs_kernel<false><<<N, ft::kLpThreads, 0, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  const cudaError_t e = dtype == FT_BF16 ? ft::launch_logprobs<true>(p, N, (cudaStream_t)stream)
+                                         : ft::launch_logprobs<false>(p, N, (cudaStream_t)stream);
+  return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
 }  // extern "C"
