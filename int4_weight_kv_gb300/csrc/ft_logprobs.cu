@@ -55,6 +55,29 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
+// Pairs of FP32 values: one instruction for two elements.
+struct lp2 {
+  unsigned long long v;
+  __device__ __forceinline__ lp2() {}
+  __device__ __forceinline__ lp2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ lp2 add2(lp2 a, lp2 b) {
+  lp2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ lp2 mul2(lp2 a, lp2 b) {
+  lp2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ lp2 fma2(lp2 a, lp2 b, lp2 c) {
+  lp2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // Running statistics: maximum m, z = sum e^d, u = sum e^d d, d = x - m (m itself is not scaled by
 // log2 e, which would overflow for logits near FP32's largest).
 struct LpStat {
@@ -150,7 +173,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
   const uint8_t* vec0 = base - lead * (BF16 ? 2 : 4);
   const int nvec = (lead + V + E - 1) / E;
   const int v0 = (int)((int64_t)nvec * rank_in / ctas), v1 = (int)((int64_t)nvec * (rank_in + 1) / ctas);
-  LpStat st = {-INFINITY, 0.0f, 0.0f};
+  float run_m = -INFINITY;                      // this thread's statistics, the sums in pairs
+  lp2 run_z(0.0f, 0.0f), run_u(0.0f, 0.0f);
   int above = 0;
   if (tid == 0) {
     s.count = 0;
@@ -163,7 +187,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     for (int i = 0; i < U; ++i) {
       const int v = r + i * kLpThreads + tid;
       const int e0 = v * E - lead;
-      if (v < v1 && e0 >= 0 && e0 + E <= V) {
+      if (r > 0 && r + U * kLpThreads < v1) {  // a round inside the row and the slice
+        q[i] = ld_stream_v4(vec0 + (size_t)v * 16);
+      } else if (v < v1 && e0 >= 0 && e0 + E <= V) {
         q[i] = ld_stream_v4(vec0 + (size_t)v * 16);
       } else {
         uint32_t w[4];
@@ -201,27 +227,34 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     float bm = x[0];
 #pragma unroll
     for (int k = 1; k < kLpElems; ++k) bm = fmaxf(bm, x[k]);
-    if (bm > st.m) st.move(bm);
-    const float m = st.m == -INFINITY ? 0.0f : st.m;
-#pragma unroll
-    for (int k = 0; k < kLpElems; ++k) {
-      const float d = x[k] - m, e = lp_ex2(d * kLog2e);
-      st.z += e;                                // a NaN or +infinity stays in z
-      st.u = fmaf(e, fmaxf(d, -1000.0f), st.u);  // 0 x -infinity of a masked logit is 0
+    if (bm > run_m) {
+      const float f = run_m == -INFINITY ? 0.0f : lp_ex2((run_m - bm) * kLog2e);
+      const float d = f == 0.0f ? 0.0f : run_m - bm;
+      const lp2 f2(f, f);
+      run_u = mul2(f2, fma2(lp2(d, d), run_z, run_u));
+      run_z = mul2(f2, run_z);
+      run_m = bm;
     }
-    if (has) {
+    const float m = run_m == -INFINITY ? 0.0f : run_m;
+    const lp2 m2(-m, -m), l2(kLog2e, kLog2e);
+#pragma unroll
+    for (int k = 0; k < kLpElems; k += 2) {
+      const lp2 d2 = add2(lp2(x[k], x[k + 1]), m2);
+      float d0, d1, s0, s1;
+      mul2(d2, l2).get(s0, s1);
+      d2.get(d0, d1);
+      const lp2 e2(lp_ex2(s0), lp_ex2(s1));
+      run_z = add2(run_z, e2);                                                // a NaN or +infinity stays in z
+      run_u = fma2(e2, lp2(fmaxf(d0, -1000.0f), fmaxf(d1, -1000.0f)), run_u);  // 0 x -infinity of a masked logit is 0
+    }
+    if (has && bm >= xt) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int e0 = (r + i * kLpThreads + tid) * E - lead;
-        if (e0 > t) {
+        const int v = r + i * kLpThreads + tid, e0 = v * E - lead;
 #pragma unroll
-          for (int k = 0; k < E; ++k) above += x[i * E + k] > xt;
-        } else {
-#pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const float v = x[i * E + k];
-            above += (v > xt || (v == xt && e0 + k < t)) && e0 + k >= 0 && r + i * kLpThreads + tid < v1;
-          }
+        for (int k = 0; k < E; ++k) {
+          const float y = x[i * E + k];
+          above += (y > xt || (y == xt && e0 + k < t)) && e0 + k >= 0 && v < v1;
         }
       }
     }
@@ -309,6 +342,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
   }
 
   // ---- the CTA's statistics, in warp order
+  LpStat st;
+  {
+    float a, b;
+    st.m = run_m;
+    run_z.get(a, b);
+    st.z = a + b;
+    run_u.get(a, b);
+    st.u = a + b;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     LpStat b;
