@@ -8,8 +8,10 @@
 // round's in flight while one is used: running maximum, sum and weighted sum per thread
 // (a moved maximum rescales them), the target's rank counted by comparison, and the
 // alternatives filtered through a threshold: only elements above the k-th best so far
-// reach a shared list, which is cut back to k when it passes kKeep.  The first threshold
-// is the k-th largest of the threads' first maxima, so few elements pass even then.
+// reach the warp's list, which is cut back to k when it passes kLpKeep.  The first
+// threshold is the k-th largest of the lanes' first maxima, so few elements pass even
+// then; the best threshold of any warp serves all of the CTA.  Warps meet only at the
+// end: a barrier in every round cost a third of the time.
 // CTA 0 joins the slices through distributed shared memory: one launch, no workspace.
 // Bound by HBM for many rows; a single row by its latency, hence up to 16 CTAs for it.
 //
@@ -23,9 +25,8 @@ namespace ft {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpMaxTop = 32, kLpMaxCluster = 16;
 constexpr int kLpElems = 16;                              // elements of one thread in one round
-constexpr int kLpKeep = 256;                              // listed alternatives before a cut
-constexpr int kLpList = kLpThreads * kLpElems + kLpKeep;  // all of a round may pass
-constexpr int kLpSel = kLpMaxTop * (kLpList / kLpThreads + 1);
+constexpr int kLpKeep = 2 * kLpMaxTop + 4;                // listed alternatives of a warp before a cut, at most
+constexpr int kLpList = 32 * kLpElems + kLpKeep;          // all of a warp's round may pass
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct LogprobParams {
@@ -102,56 +103,93 @@ struct LpStat {
 };
 
 struct LpShared {
-  lp_key_t list[kLpList], sel[kLpSel], best[kLpMaxTop];
+  lp_key_t list[kLpWarps][kLpList];
+  lp_key_t cut[kLpWarps][kLpMaxTop];          // scratch
+  lp_key_t best[kLpWarps * kLpMaxTop];        // each warp's best, then the CTA's
   lp_key_t inbox[kLpMaxCluster * kLpMaxTop];  // CTA 0: the slices' best
   float4 stat[kLpMaxCluster];                 // CTA 0: the slices' (m, z, u, rank)
-  __align__(16) float first[kLpThreads];
   float4 wstat[kLpWarps];
-  lp_key_t tau;
-  int count, nsel;
+  uint32_t tau;                               // largest threshold of any warp (lp_order)
 };
 
-// The k largest of list[0 .. n), in order, to best[]; the list then holds them.  All threads.
-__device__ __forceinline__ void lp_cut(LpShared& s, lp_key_t* list, int n, int k) {
-  const int tid = threadIdx.x;
-  const lp_key_t* from = list;
-  if (n > kLpSel) {
-    // the k-th largest of the threads' maxima bounds the k-th largest from below; only the
-    // k threads at or above it hold keys that pass
-    lp_key_t mx = 0;
-    for (int i = tid; i < n; i += kLpThreads) mx = max(mx, list[i]);
-    s.sel[tid] = mx;
-    if (tid == 0) s.nsel = 0;
-    __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kLpThreads; ++i) above += s.sel[i] > mx;
-    if (above == k - 1) s.tau = mx;
-    __syncthreads();
-    const lp_key_t t = s.tau;
-    for (int i = tid; i < n; i += kLpThreads)
-      if (list[i] >= t) s.sel[atomicAdd(&s.nsel, 1)] = list[i];
-    __syncthreads();
-    n = s.nsel;
-    from = s.sel;
+// The k-th largest of one value per lane (the lowest where fewer lanes hold one).
+template <typename T>
+__device__ __forceinline__ T lp_kth(T mine, int k) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const T o = __shfl_sync(0xffffffffu, mine, i);
+    before += o > mine || (o == mine && i < lane);
   }
-  for (int i = tid; i < n; i += kLpThreads) {
-    const lp_key_t mine = from[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += from[j] > mine;
-    if (above < k) s.best[above] = mine;
-  }
-  __syncthreads();
-  for (int i = tid; i < min(n, k); i += kLpThreads) list[i] = s.best[i];
-  if (tid == 0) {
-    s.count = min(n, k);
-    s.tau = n >= k ? s.best[k - 1] : 0;
-  }
-  __syncthreads();
+  const int src = __ffs(__ballot_sync(0xffffffffu, before == k - 1)) - 1;
+  return __shfl_sync(0xffffffffu, mine, max(src, 0));
 }
 
+// Cuts a warp's list of n keys to its k largest, in order, at the front of the list; returns how many.
+// `out` is scratch of k keys.
+__device__ __noinline__ int lp_cut(lp_key_t* list, lp_key_t* out, int n, int k) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (n > 4 * kLpMaxTop) {
+    // the k-th largest of the lanes' maxima bounds the k-th largest from below, and only the
+    // k lanes at or above it hold keys that pass: at most k n / 32 are left
+    lp_key_t mx = 0;
+    for (int i = lane; i < n; i += 32) mx = max(mx, list[i]);
+    const lp_key_t t = lp_kth(mx, k);
+    int kept = 0;
+    for (int i = lane; i - lane < n; i += 32) {
+      const lp_key_t key = i < n ? list[i] : 0;
+      const bool in = i < n && key >= t;
+      const uint32_t votes = __ballot_sync(0xffffffffu, in);  // every lane has read its key
+      if (in) list[kept + __popc(votes & ((1u << lane) - 1))] = key;
+      kept += __popc(votes);
+      __syncwarp();
+    }
+    n = kept;
+  }
+  for (int i0 = 0; i0 < n; i0 += 128) {  // every key's place among the others, four keys a lane
+    lp_key_t mine[4];
+    int before[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mine[q] = i0 + 32 * q + lane < n ? list[i0 + 32 * q + lane] : ~0ull;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const lp_key_t o = list[j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) before[q] += o > mine[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i0 + 32 * q + lane < n && before[q] < k) out[before[q]] = mine[q];
+  }
+  __syncwarp();
+  if (lane < min(n, k)) list[lane] = out[lane];
+  __syncwarp();
+  return min(n, k);
+}
+
+// The k largest of n <= 2 kLpThreads keys (0: none), in order, to out; all threads of the CTA.
+__device__ __forceinline__ void lp_merge(const lp_key_t* list, lp_key_t* out, int n, int k) {
+  const int tid = threadIdx.x;
+  const lp_key_t a = tid < n ? list[tid] : 0, b = tid + kLpThreads < n ? list[tid + kLpThreads] : 0;
+  int before_a = 0, before_b = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) {
+    const lp_key_t o = list[j];
+    before_a += o > a;
+    before_b += o > b;
+  }
+  if (a && before_a < k) out[before_a] = a;
+  if (b && before_b < k) out[before_b] = b;
+  __syncthreads();
+}
+static_assert(kLpMaxCluster * kLpMaxTop <= 2 * kLpThreads && kLpWarps * kLpMaxTop <= 2 * kLpThreads, "lp_merge");
+
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobParams p) {
-  constexpr int E = BF16 ? 8 : 4, U = kLpElems / E;  // elements of a 16-byte vector, vectors of a round
+__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobParams p) {
+  constexpr int E = BF16 ? 8 : 4, U = kLpElems / E;  // elements of a 16-byte vector, vectors of a thread's round
+  constexpr int kStep = U * kLpThreads;              // vectors of the CTA's round
   extern __shared__ __align__(16) uint8_t lp_smem[];
   LpShared& s = *reinterpret_cast<LpShared*>(lp_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = p.V, top = p.top;
@@ -176,10 +214,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
   float run_m = -INFINITY;                      // this thread's statistics, the sums in pairs
   lp2 run_z(0.0f, 0.0f), run_u(0.0f, 0.0f);
   int above = 0;
-  if (tid == 0) {
-    s.count = 0;
-    s.tau = 0;
-  }
+  if (tid == 0) s.tau = 0;
+  __syncthreads();
 
   // 16-byte vectors, or their elements inside the row at its ends; the others -infinity
   auto fetch = [&](int r, uint4 (&q)[U]) {
@@ -211,10 +247,37 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
       }
     }
   };
-  float tau = -INFINITY;      // value of the threshold: nothing below it can be an alternative
-  lp_key_t tau_key = 0;       // keys must be above this
-  bool full = false;          // this thread saw the list past kLpKeep
-  auto use = [&](int r, const uint4 (&q)[U], bool filter) {
+  uint4 cur[U], nxt[U];
+  fetch(v0, cur);
+  float tau = -INFINITY;  // nothing below it can be an alternative
+  int listed = 0;         // keys in the warp's list
+  lp_key_t tau_key = 0;   // the warp's own k-th best: keys must be above it
+  const int keep = 2 * top + 4 < kLpKeep ? 2 * top + 4 : kLpKeep;  // a late cut leaves the threshold low
+  // the elements of a round at or above tau, to the warp's list
+  auto filter = [&](int r, const float (&x)[kLpElems]) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = r + i * kLpThreads + tid;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const int e = v * E - lead + k;
+        const lp_key_t key = lp_key(x[i * E + k], e);
+        const bool in = x[i * E + k] >= tau && key > tau_key && v < v1 && e >= 0 && e < V;
+        const uint32_t votes = __ballot_sync(0xffffffffu, in);
+        if (in) s.list[warp][listed + __popc(votes & ((1u << lane) - 1))] = key;
+        listed += __popc(votes);
+      }
+    }
+    __syncwarp();
+    if (listed > keep) {
+      listed = lp_cut(s.list[warp], s.cut[warp], listed, top);
+      if (listed == top) {
+        tau_key = s.list[warp][top - 1];
+        if (lane == 0) atomicMax(&s.tau, (uint32_t)(tau_key >> 32));
+      }
+    }
+  };
+  auto use = [&](int r, const uint4 (&q)[U], bool first) {
     float x[kLpElems];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -247,98 +310,52 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
       run_z = add2(run_z, e2);                                                // a NaN or +infinity stays in z
       run_u = fma2(e2, lp2(fmaxf(d0, -1000.0f), fmaxf(d1, -1000.0f)), run_u);  // 0 x -infinity of a masked logit is 0
     }
-    if (has && bm >= xt) {
+    if (bm >= xt) {  // without a target xt is +infinity: a row that reaches it has no rank anyway
+      const int lo = r * E - lead;
+      if (r > 0 && r + kStep < v1 && (lo > t || lo + kStep * E <= t)) {  // all of the round behind the target, or before it
+        if (lo > t) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int v = r + i * kLpThreads + tid, e0 = v * E - lead;
+          for (int k = 0; k < kLpElems; ++k) above += x[k] > xt;
+        } else {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float y = x[i * E + k];
-          above += (y > xt || (y == xt && e0 + k < t)) && e0 + k >= 0 && v < v1;
+          for (int k = 0; k < kLpElems; ++k) above += x[k] >= xt;
         }
-      }
-    }
-    if (filter && bm >= tau) {
+      } else {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int v = r + i * kLpThreads + tid;
+        for (int i = 0; i < U; ++i) {
+          const int v = r + i * kLpThreads + tid, e0 = v * E - lead;
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const int e = v * E - lead + k;
-          if (x[i * E + k] >= tau && v < v1 && e >= 0 && e < V) {
-            const lp_key_t key = lp_key(x[i * E + k], e);
-            if (key > tau_key) {
-              const int n = atomicAdd(&s.count, 1);
-              if (n < kLpList) s.list[n] = key;
-              full |= n >= kLpKeep;
-            }
+          for (int k = 0; k < E; ++k) {
+            const float y = x[i * E + k];
+            above += (y > xt || (y == xt && e0 + k < t)) && e0 + k >= 0 && v < v1;
           }
         }
       }
     }
-    return bm;
+    if (top > 0) {
+      if (first) {
+        tau = lp_kth(bm, top);
+        if (lane == 0 && tau > -INFINITY) atomicMax(&s.tau, lp_order(tau));
+      } else {
+        const uint32_t o = *reinterpret_cast<volatile uint32_t*>(&s.tau);
+        if (o) tau = fmaxf(tau, lp_key_value((lp_key_t)o << 32));
+      }
+      if (__any_sync(0xffffffffu, bm >= tau)) filter(r, x);
+    }
   };
 
-  uint4 cur[U], nxt[U];
-  constexpr int kStep = U * kLpThreads;
-  fetch(v0, cur);
-  if (top > 0) {
-    if (v0 + kStep < v1) fetch(v0 + kStep, nxt);
-    s.first[tid] = use(v0, cur, false);
+  for (int r = v0; r < v1; r += kStep) {
+    if (r + kStep < v1) fetch(r + kStep, nxt);
+    use(r, cur, r == v0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) cur[i] = nxt[i];
+  }
+  if (top > 0) {  // the warps' best, joined by the first warp
+    const int n = lp_cut(s.list[warp], s.cut[warp], listed, top);
+    if (lane < top) s.best[warp * top + lane] = lane < n ? s.list[warp][lane] : 0;
+    if (tid < top) s.cut[0][tid] = 0;  // (lp_cut is done with it) a slice may hold fewer than k
     __syncthreads();
-    int over = 0, ties = 0;
-    const float mine = s.first[tid];
-#pragma unroll 4
-    for (int i = 0; i < kLpThreads; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(s.first + i);
-      over += (f.x > mine) + (f.y > mine) + (f.z > mine) + (f.w > mine);
-      ties += (f.x == mine && i < tid) + (f.y == mine && i + 1 < tid) + (f.z == mine && i + 2 < tid) +
-              (f.w == mine && i + 3 < tid);
-    }
-    if (over + ties == top - 1) s.tau = (lp_key_t)lp_order(mine) << 32;  // below every key of this value
-    __syncthreads();
-    tau_key = s.tau;
-    tau = tau_key ? lp_key_value(tau_key) : -INFINITY;
-    // the first round again, for the list only
-    {
-      float x[kLpElems];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-        const int v = v0 + i * kLpThreads + tid;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          x[k] = BF16 ? __uint_as_float((k & 1) ? (w[k / 2] & 0xFFFF0000u) : (w[k / 2] << 16)) : __uint_as_float(w[k % 4]);
-          const int e = v * E - lead + k;
-          if (x[k] >= tau && v < v1 && e >= 0 && e < V) {
-            const int n = atomicAdd(&s.count, 1);
-            s.list[n] = lp_key(x[k], e);
-            full |= n >= kLpKeep;
-          }
-        }
-      }
-    }
-    for (int r = v0 + kStep; r < v1; r += kStep) {
-      if (__syncthreads_or(full)) {
-        lp_cut(s, s.list, s.count, top);
-        tau_key = s.tau;
-        tau = tau_key ? lp_key_value(tau_key) : -INFINITY;
-        full = false;
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) cur[i] = nxt[i];
-      if (r + kStep < v1) fetch(r + kStep, nxt);
-      use(r, cur, true);
-    }
-    __syncthreads();
-    lp_cut(s, s.list, s.count, top);
-  } else {
-    for (int r = v0; r < v1; r += kStep) {
-      if (r + kStep < v1) fetch(r + kStep, nxt);
-      use(r, cur, false);
-#pragma unroll
-      for (int i = 0; i < U; ++i) cur[i] = nxt[i];
-    }
+    lp_merge(s.best, s.cut[0], kLpWarps * top, top);
   }
 
   // ---- the CTA's statistics, in warp order
@@ -362,7 +379,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
   }
   if (lane == 0) s.wstat[warp] = make_float4(st.m, st.z, st.u, __int_as_float(above));
   __syncthreads();
-  const int n_best = top > 0 ? s.count : 0;
   if (ctas > 1) cluster_wait();
   if (tid == 0) {
     LpStat all = {-INFINITY, 0.0f, 0.0f};
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
   if (tid < top) {
     uint32_t dst;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&s.inbox[rank_in * top + tid])));
-    const lp_key_t key = tid < n_best ? s.best[tid] : 0ull;
+    const lp_key_t key = s.cut[0][tid];
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(key) : "memory");
   }
   if (ctas > 1) {
@@ -412,9 +428,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     if (p.rank) p.rank[row] = (bad || !has) ? -1 : cnt;
   }
   if (top > 0) {
-    if (ctas > 1) lp_cut(s, s.inbox, (int)ctas * top, top);
+    if (ctas > 1) lp_merge(s.inbox, s.cut[0], (int)ctas * top, top);
     if (tid < top) {
-      const lp_key_t key = s.best[tid];
+      const lp_key_t key = s.cut[0][tid];
       p.top_id[row * top + tid] = bad ? -1 : (int)~(uint32_t)key;
       p.top_val[row * top + tid] = bad ? nanv : logp(lp_key_value(key));
     }
