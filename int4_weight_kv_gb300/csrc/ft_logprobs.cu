@@ -6,12 +6,13 @@
 //
 // A cluster of CTAs per row, each streaming a slice once with 16-byte loads, the next
 // round's in flight while one is used: running maximum, sum and weighted sum per thread
-// (a moved maximum rescales them), the target's rank counted by comparison, and the
-// alternatives filtered through a threshold: only elements above the k-th best so far
-// reach the warp's list, which is cut back to k when it passes kLpKeep.  The first
-// threshold is the k-th largest of the lanes' first maxima, so few elements pass even
-// then; the best threshold of any warp serves all of the CTA.  Warps meet only at the
-// end: a barrier in every round cost a third of the time.
+// (a moved maximum rescales them), and the target's rank counted by comparison.  The
+// alternatives cost the stream nothing: with t the k-th largest of the 256 threads'
+// maxima, only elements >= t can be among the k largest, and only the threads whose
+// maximum reaches t (k of them, more with ties) hold such elements.  The CTA reads those
+// threads' vectors once more, lists what reaches t, and ranks the list.  (Filtering every
+// round through a running threshold instead cost 36 us of 213 for k = 1 and 53 of 88 for
+// k = 20, 256 rows of 128256.)
 // CTA 0 joins the slices through distributed shared memory: one launch, no workspace.
 // Bound by HBM for many rows; a single row by its latency, hence up to 16 CTAs for it.
 //
@@ -25,8 +26,9 @@ namespace ft {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpMaxTop = 32, kLpMaxCluster = 16;
 constexpr int kLpElems = 16;                              // elements of one thread in one round
-constexpr int kLpKeep = 2 * kLpMaxTop + 4;                // listed alternatives of a warp before a cut, at most
-constexpr int kLpList = 32 * kLpElems + kLpKeep;          // all of a warp's round may pass
+constexpr int kLpKeep = 256;                              // listed alternatives before a cut
+constexpr int kLpScan = 8;                                // elements a thread reads again in one round
+constexpr int kLpList = kLpThreads * kLpScan + kLpKeep;   // all of a round may pass
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct LogprobParams {
@@ -103,77 +105,26 @@ struct LpStat {
 };
 
 struct LpShared {
-  lp_key_t list[kLpWarps][kLpList];
-  lp_key_t cut[kLpWarps][kLpMaxTop];          // scratch
-  lp_key_t best[kLpWarps * kLpMaxTop];        // each warp's best, then the CTA's
+  lp_key_t list[kLpList];
+  lp_key_t best[kLpMaxTop];
   lp_key_t inbox[kLpMaxCluster * kLpMaxTop];  // CTA 0: the slices' best
+  lp_key_t high[kLpThreads];
   float4 stat[kLpMaxCluster];                 // CTA 0: the slices' (m, z, u, rank)
   float4 wstat[kLpWarps];
-  uint32_t tau;                               // largest threshold of any warp (lp_order)
+  __align__(16) float top[kLpThreads];        // the threads' maxima
+  uint8_t cand[kLpThreads];
+  uint32_t tau;
+  lp_key_t tau_key;
+  int count, n_cand;
 };
-
-// The k-th largest of one value per lane (the lowest where fewer lanes hold one).
-template <typename T>
-__device__ __forceinline__ T lp_kth(T mine, int k) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const T o = __shfl_sync(0xffffffffu, mine, i);
-    before += o > mine || (o == mine && i < lane);
-  }
-  const int src = __ffs(__ballot_sync(0xffffffffu, before == k - 1)) - 1;
-  return __shfl_sync(0xffffffffu, mine, max(src, 0));
-}
-
-// Cuts a warp's list of n keys to its k largest, in order, at the front of the list; returns how many.
-// `out` is scratch of k keys.
-__device__ __noinline__ int lp_cut(lp_key_t* list, lp_key_t* out, int n, int k) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-  if (n > 4 * kLpMaxTop) {
-    // the k-th largest of the lanes' maxima bounds the k-th largest from below, and only the
-    // k lanes at or above it hold keys that pass: at most k n / 32 are left
-    lp_key_t mx = 0;
-    for (int i = lane; i < n; i += 32) mx = max(mx, list[i]);
-    const lp_key_t t = lp_kth(mx, k);
-    int kept = 0;
-    for (int i = lane; i - lane < n; i += 32) {
-      const lp_key_t key = i < n ? list[i] : 0;
-      const bool in = i < n && key >= t;
-      const uint32_t votes = __ballot_sync(0xffffffffu, in);  // every lane has read its key
-      if (in) list[kept + __popc(votes & ((1u << lane) - 1))] = key;
-      kept += __popc(votes);
-      __syncwarp();
-    }
-    n = kept;
-  }
-  for (int i0 = 0; i0 < n; i0 += 128) {  // every key's place among the others, four keys a lane
-    lp_key_t mine[4];
-    int before[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) mine[q] = i0 + 32 * q + lane < n ? list[i0 + 32 * q + lane] : ~0ull;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const lp_key_t o = list[j];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) before[q] += o > mine[q];
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (i0 + 32 * q + lane < n && before[q] < k) out[before[q]] = mine[q];
-  }
-  __syncwarp();
-  if (lane < min(n, k)) list[lane] = out[lane];
-  __syncwarp();
-  return min(n, k);
-}
 
 // The k largest of n <= 2 kLpThreads keys (0: none), in order, to out; all threads of the CTA.
 __device__ __forceinline__ void lp_merge(const lp_key_t* list, lp_key_t* out, int n, int k) {
   const int tid = threadIdx.x;
   const lp_key_t a = tid < n ? list[tid] : 0, b = tid + kLpThreads < n ? list[tid + kLpThreads] : 0;
   int before_a = 0, before_b = 0;
+  if (tid < k) out[tid] = 0;
+  __syncthreads();
 #pragma unroll 8
   for (int j = 0; j < n; ++j) {
     const lp_key_t o = list[j];
@@ -184,7 +135,39 @@ __device__ __forceinline__ void lp_merge(const lp_key_t* list, lp_key_t* out, in
   if (b && before_b < k) out[before_b] = b;
   __syncthreads();
 }
-static_assert(kLpMaxCluster * kLpMaxTop <= 2 * kLpThreads && kLpWarps * kLpMaxTop <= 2 * kLpThreads, "lp_merge");
+static_assert(kLpMaxCluster * kLpMaxTop <= 2 * kLpThreads, "lp_merge");
+
+// The list's k largest, in order, to best.  A longer list than lp_merge takes is first cut the
+// way the row is: the k-th largest of the threads' maxima bounds what can matter.
+__device__ __forceinline__ void lp_rank(LpShared& s, int k) {
+  const int tid = threadIdx.x;
+  int n = s.count;
+  while (n > 2 * kLpThreads) {  // leaves at most k ceil(n / kLpThreads) keys, under half of them
+    lp_key_t mine = 0;
+    for (int i = tid; i < n; i += kLpThreads) mine = max(mine, s.list[i]);
+    s.high[tid] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < kLpThreads; ++j) before += s.high[j] > mine;
+    if (before == k - 1) s.tau_key = mine;
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    const lp_key_t t = s.tau_key;
+    lp_key_t held[(kLpList + kLpThreads - 1) / kLpThreads];
+#pragma unroll
+    for (int q = 0; q < (kLpList + kLpThreads - 1) / kLpThreads; ++q) {
+      const int i = q * kLpThreads + tid;
+      held[q] = i < n ? s.list[i] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < (kLpList + kLpThreads - 1) / kLpThreads; ++q)
+      if (held[q] >= t && held[q]) s.list[atomicAdd(&s.count, 1)] = held[q];
+    __syncthreads();
+    n = s.count;
+  }
+  lp_merge(s.list, s.best, n, k);
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobParams p) {
@@ -214,9 +197,6 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
   float run_m = -INFINITY;                      // this thread's statistics, the sums in pairs
   lp2 run_z(0.0f, 0.0f), run_u(0.0f, 0.0f);
   int above = 0;
-  if (tid == 0) s.tau = 0;
-  __syncthreads();
-
   // 16-byte vectors, or their elements inside the row at its ends; the others -infinity
   auto fetch = [&](int r, uint4 (&q)[U]) {
 #pragma unroll
@@ -247,37 +227,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
       }
     }
   };
-  uint4 cur[U], nxt[U];
-  fetch(v0, cur);
-  float tau = -INFINITY;  // nothing below it can be an alternative
-  int listed = 0;         // keys in the warp's list
-  lp_key_t tau_key = 0;   // the warp's own k-th best: keys must be above it
-  const int keep = 2 * top + 4 < kLpKeep ? 2 * top + 4 : kLpKeep;  // a late cut leaves the threshold low
-  // the elements of a round at or above tau, to the warp's list
-  auto filter = [&](int r, const float (&x)[kLpElems]) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int v = r + i * kLpThreads + tid;
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const int e = v * E - lead + k;
-        const lp_key_t key = lp_key(x[i * E + k], e);
-        const bool in = x[i * E + k] >= tau && key > tau_key && v < v1 && e >= 0 && e < V;
-        const uint32_t votes = __ballot_sync(0xffffffffu, in);
-        if (in) s.list[warp][listed + __popc(votes & ((1u << lane) - 1))] = key;
-        listed += __popc(votes);
-      }
-    }
-    __syncwarp();
-    if (listed > keep) {
-      listed = lp_cut(s.list[warp], s.cut[warp], listed, top);
-      if (listed == top) {
-        tau_key = s.list[warp][top - 1];
-        if (lane == 0) atomicMax(&s.tau, (uint32_t)(tau_key >> 32));
-      }
-    }
-  };
-  auto use = [&](int r, const uint4 (&q)[U], bool first) {
+  auto use = [&](int r, const uint4 (&q)[U]) {
     float x[kLpElems];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -332,30 +282,69 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
         }
       }
     }
-    if (top > 0) {
-      if (first) {
-        tau = lp_kth(bm, top);
-        if (lane == 0 && tau > -INFINITY) atomicMax(&s.tau, lp_order(tau));
-      } else {
-        const uint32_t o = *reinterpret_cast<volatile uint32_t*>(&s.tau);
-        if (o) tau = fmaxf(tau, lp_key_value((lp_key_t)o << 32));
-      }
-      if (__any_sync(0xffffffffu, bm >= tau)) filter(r, x);
-    }
   };
 
+  uint4 cur[U], nxt[U];
+  fetch(v0, cur);
   for (int r = v0; r < v1; r += kStep) {
     if (r + kStep < v1) fetch(r + kStep, nxt);
-    use(r, cur, r == v0);
+    use(r, cur);
 #pragma unroll
     for (int i = 0; i < U; ++i) cur[i] = nxt[i];
   }
-  if (top > 0) {  // the warps' best, joined by the first warp
-    const int n = lp_cut(s.list[warp], s.cut[warp], listed, top);
-    if (lane < top) s.best[warp * top + lane] = lane < n ? s.list[warp][lane] : 0;
-    if (tid < top) s.cut[0][tid] = 0;  // (lp_cut is done with it) a slice may hold fewer than k
+  if (top > 0) {
+    s.top[tid] = run_m;
+    if (tid == 0) s.count = s.n_cand = 0, s.tau = 0xFFFFFFFFu, s.tau_key = 0;
     __syncthreads();
-    lp_merge(s.best, s.cut[0], kLpWarps * top, top);
+    int before = 0;
+#pragma unroll 4
+    for (int i = 0; i < kLpThreads; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(s.top + i);
+      before += (f.x > run_m) + (f.y > run_m) + (f.z > run_m) + (f.w > run_m);
+    }
+    if (before < top) atomicMin(&s.tau, lp_order(run_m));  // the lowest of the k largest maxima
+    __syncthreads();
+    const uint32_t tau_o = s.tau;
+    const float tau = lp_key_value((lp_key_t)tau_o << 32);
+    if (run_m >= tau) s.cand[atomicAdd(&s.n_cand, 1)] = (uint8_t)tid;  // order does not matter
+    __syncthreads();
+    // the candidates' vectors again: item w is vector w % nv of thread cand[w / nv]
+    const int nv = (v1 - v0 + kLpThreads - 1) / kLpThreads, items = s.n_cand * nv;
+    constexpr int kPer = kLpScan / E;
+    lp_key_t floor_key = 0;  // once cut, keys must be above the k-th best
+    for (int w0 = 0; w0 < items; w0 += kPer * kLpThreads) {
+      bool full = false;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int w = w0 + i * kLpThreads + tid;
+        if (w < items) {
+          const int c = w / nv, v = v0 + (w - c * nv) * kLpThreads + s.cand[c], e0 = v * E - lead;
+          if (v < v1) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+              if (e0 + k < 0 || e0 + k >= V) continue;
+              const float x = at(e0 + k);
+              if (x >= tau) {
+                const lp_key_t key = lp_key(x, e0 + k);
+                if (key > floor_key) {
+                  const int n = atomicAdd(&s.count, 1);
+                  s.list[n] = key;
+                  full |= n >= kLpKeep;
+                }
+              }
+            }
+          }
+        }
+      }
+      if (__syncthreads_or(full) && w0 + kPer * kLpThreads < items) {
+        lp_rank(s, top);
+        floor_key = s.best[top - 1];
+        if (tid < top) s.list[tid] = s.best[tid];
+        if (tid == 0) s.count = top;
+        __syncthreads();
+      }
+    }
+    lp_rank(s, top);
   }
 
   // ---- the CTA's statistics, in warp order
@@ -398,7 +387,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
   if (tid < top) {
     uint32_t dst;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&s.inbox[rank_in * top + tid])));
-    const lp_key_t key = s.cut[0][tid];
+    const lp_key_t key = s.best[tid];
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(key) : "memory");
   }
   if (ctas > 1) {
@@ -428,9 +417,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
     if (p.rank) p.rank[row] = (bad || !has) ? -1 : cnt;
   }
   if (top > 0) {
-    if (ctas > 1) lp_merge(s.inbox, s.cut[0], (int)ctas * top, top);
+    if (ctas > 1) lp_merge(s.inbox, s.best, (int)ctas * top, top);
     if (tid < top) {
-      const lp_key_t key = s.cut[0][tid];
+      const lp_key_t key = s.best[tid];
       p.top_id[row * top + tid] = bad ? -1 : (int)~(uint32_t)key;
       p.top_val[row * top + tid] = bad ? nanv : logp(lp_key_value(key));
     }
