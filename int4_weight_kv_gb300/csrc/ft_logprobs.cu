@@ -14,7 +14,7 @@
 // round through a running threshold instead cost 36 us of 213 for k = 1 and 53 of 88 for
 // k = 20, 256 rows of 128256.)
 // CTA 0 joins the slices through distributed shared memory: one launch, no workspace.
-// Bound by HBM for many rows; a single row by its latency, hence up to 16 CTAs for it.
+// Bound by HBM for many rows; a single row by its latency, hence up to 8 CTAs for it.
 //
 // Alternatives are ordered by a 64-bit key (the value as an ordered integer, then the
 // lower index), so ties have one answer whatever order the row is read in.
@@ -24,7 +24,7 @@
 
 namespace ft {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpMaxTop = 32, kLpMaxCluster = 16;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kLpMaxTop = 32, kLpMaxCluster = 8;
 constexpr int kLpElems = 16;                              // elements of one thread in one round
 constexpr int kLpKeep = 256;                              // listed alternatives before a cut
 constexpr int kLpScan = 8;                                // elements a thread reads again in one round
@@ -320,10 +320,16 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
         if (w < items) {
           const int c = w / nv, v = v0 + (w - c * nv) * kLpThreads + s.cand[c], e0 = v * E - lead;
           if (v < v1) {
+            const bool inside = e0 >= 0 && e0 + E <= V;
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (inside) q = ld_stream_v4(vec0 + (size_t)v * 16);
+            const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < E; ++k) {
-              if (e0 + k < 0 || e0 + k >= V) continue;
-              const float x = at(e0 + k);
+              if (!inside && (e0 + k < 0 || e0 + k >= V)) continue;
+              const float x = !inside ? at(e0 + k)
+                              : BF16  ? __uint_as_float((k & 1) ? (wd[k / 2] & 0xFFFF0000u) : (wd[k / 2] << 16))
+                                      : __uint_as_float(wd[k % 4]);
               if (x >= tau) {
                 const lp_key_t key = lp_key(x, e0 + k);
                 if (key > floor_key) {
@@ -426,13 +432,16 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
   }
 }
 
-// CTAs per row: enough for four on every SM, of at least one round each.
+// CTAs per row: as many as keep the grid within one and a half CTAs a SM, with two rounds
+// each.  Every further CTA pays the alternatives' fixed cost again.  Measured (FP32, V = 128256,
+// k = 1; us): one row 16.7 / 12.9 / 10.4 / 9.2 / 8.8 for 1 / 2 / 4 / 8 / 16 CTAs, 32 rows 17.0 / 12.8
+// / 10.7 / 11.3 / 18.3, 256 rows 33 / 41 / 44 / 58 / 108.
 static int lp_cluster(int N, int V) {
   int sms = ft_host::num_sms();
   if (sms <= 0) sms = 152;
   const int rounds = (V + kLpThreads * kLpElems - 1) / (kLpThreads * kLpElems);
   int c = 1;
-  while (c < kLpMaxCluster && 2 * c <= rounds && (int64_t)N * c < (int64_t)4 * sms) c *= 2;
+  while (c < kLpMaxCluster && 4 * c <= rounds && (int64_t)N * 4 * c <= (int64_t)3 * sms) c *= 2;
   return c;
 }
 
@@ -442,9 +451,8 @@ static cudaError_t launch_logprobs(const LogprobParams& p, int N, cudaStream_t s
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!allowed[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(LpShared));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(logprobs_kernel<BF16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(LpShared));
     if (e != cudaSuccess) return e;
     allowed[dev] = 1;
   }
