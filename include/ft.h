@@ -237,7 +237,7 @@ int ft_kv_append_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pages, i
                             int32_t *dev_status, ft_stream stream);
 
 /* Reads rows back as values in the model basis (decoded, the rotation undone,
- * rounded to BF16): k_out, v_out BF16 bits [total, n_kv, d].  Slot -1 gives zeros;
+ * rounded to BF16): k_out, v_out BF16 bits [total, n_kv, d], 16-byte aligned.  Slot -1 gives zeros;
  * any other slot outside the pool gives zeros and sets FT_DEV_RANGE. */
 int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, int page_size, const int32_t *slots,
                           int total, uint16_t *k_out, uint16_t *v_out, int32_t *dev_status, ft_stream stream);

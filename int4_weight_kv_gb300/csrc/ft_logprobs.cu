@@ -58,29 +58,6 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
-// Pairs of FP32 values: one instruction for two elements.
-struct lp2 {
-  unsigned long long v;
-  __device__ __forceinline__ lp2() {}
-  __device__ __forceinline__ lp2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ lp2 add2(lp2 a, lp2 b) {
-  lp2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ lp2 mul2(lp2 a, lp2 b) {
-  lp2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ lp2 fma2(lp2 a, lp2 b, lp2 c) {
-  lp2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 // Running statistics: maximum m, z = sum e^d, u = sum e^d d, d = x - m (m itself is not scaled by
 // log2 e, which would overflow for logits near FP32's largest).
 struct LpStat {
@@ -195,7 +172,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
   const int nvec = (lead + V + E - 1) / E;
   const int v0 = (int)((int64_t)nvec * rank_in / ctas), v1 = (int)((int64_t)nvec * (rank_in + 1) / ctas);
   float run_m = -INFINITY;                      // this thread's statistics, the sums in pairs
-  lp2 run_z(0.0f, 0.0f), run_u(0.0f, 0.0f);
+  f32x2 run_z(0.0f, 0.0f), run_u(0.0f, 0.0f);
   int above = 0;
   // 16-byte vectors, or their elements inside the row at its ends; the others -infinity
   auto fetch = [&](int r, uint4 (&q)[U]) {
@@ -243,22 +220,22 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
     if (bm > run_m) {
       const float f = run_m == -INFINITY ? 0.0f : lp_ex2((run_m - bm) * kLog2e);
       const float d = f == 0.0f ? 0.0f : run_m - bm;
-      const lp2 f2(f, f);
-      run_u = mul2(f2, fma2(lp2(d, d), run_z, run_u));
+      const f32x2 f2(f, f);
+      run_u = mul2(f2, fma2(f32x2(d, d), run_z, run_u));
       run_z = mul2(f2, run_z);
       run_m = bm;
     }
     const float m = run_m == -INFINITY ? 0.0f : run_m;
-    const lp2 m2(-m, -m), l2(kLog2e, kLog2e);
+    const f32x2 m2(-m, -m), l2(kLog2e, kLog2e);
 #pragma unroll
     for (int k = 0; k < kLpElems; k += 2) {
-      const lp2 d2 = add2(lp2(x[k], x[k + 1]), m2);
+      const f32x2 d2 = add2(f32x2(x[k], x[k + 1]), m2);
       float d0, d1, s0, s1;
       mul2(d2, l2).get(s0, s1);
       d2.get(d0, d1);
-      const lp2 e2(lp_ex2(s0), lp_ex2(s1));
+      const f32x2 e2(lp_ex2(s0), lp_ex2(s1));
       run_z = add2(run_z, e2);                                                // a NaN or +infinity stays in z
-      run_u = fma2(e2, lp2(fmaxf(d0, -1000.0f), fmaxf(d1, -1000.0f)), run_u);  // 0 x -infinity of a masked logit is 0
+      run_u = fma2(e2, f32x2(fmaxf(d0, -1000.0f), fmaxf(d1, -1000.0f)), run_u);  // 0 x -infinity of a masked logit is 0
     }
     if (bm >= xt) {  // without a target xt is +infinity: a row that reaches it has no rank anyway
       const int lo = r * E - lead;

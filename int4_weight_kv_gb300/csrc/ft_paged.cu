@@ -158,93 +158,263 @@ __global__ void __launch_bounds__(kMapThreads, 1) page_map_kernel(const MapParam
 }
 
 // ------------------------------------------------------------------ placement
-// D / 4 lanes per (row, head, K or V): each lane owns the four channels of one
-// 16-bit word of the entry (paged_fwht's ownership), so the rotated row is
-// quantised and stored without passing through shared memory.
+// D / 32 lanes per row of one head, K (blockIdx.y 0) or V; a warp holds 32 / (D / 32)
+// consecutive rows of one head, so that a prompt's entries leave it as contiguous pieces
+// and the two positions of a V pair meet in neighbouring groups of lanes.  The rotated row
+// is quantised in the registers where it was formed: no shared memory.
+constexpr int kRowThreads = 128;
+
+struct PagedRows {
+  const uint16_t *k, *v;
+  uint16_t *k_out, *v_out;
+  int64_t k_stride, v_stride;
+  const int32_t* slots;
+  uint8_t* pages;
+  PagedLayout L;
+  int total, hb;
+  float norm;
+  int32_t* status;
+};
+
+// This thread's row: t (total: none), head, lane of the row and its slot as given.
 template <int D>
-__global__ void __launch_bounds__(256) append_paged_kernel(const uint16_t* __restrict__ k, int64_t k_stride,
-                                                           const uint16_t* __restrict__ v, int64_t v_stride,
-                                                           const int32_t* __restrict__ slots,
-                                                           uint8_t* __restrict__ pages, PagedLayout L, int64_t nvec,
-                                                           int hb, float norm, int32_t* status) {
-  constexpr int LV = D / 4;
-  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t vec = gid / LV;
-  const int lane = (int)(gid % LV), g = lane & 7, j = lane >> 3;
-  const bool live = vec < nvec;
-  const int which = (int)(vec & 1);
-  const int64_t th = vec >> 1;
-  const int h = (int)(th % L.nkv);
-  const int64_t t = th / L.nkv;
-  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  int slot = -1;
-  if (live) {
-    slot = slots[t];
-    const uint16_t* src = which ? v + t * v_stride : k + t * k_stride;
-    src += h * D + 32 * j + g;
+__device__ __forceinline__ void paged_row(const PagedRows& p, int& t, int& h, int& j, int& slot) {
+  constexpr int LV = D / 32, R = 32 / LV;  // lanes of a row, rows of a warp
+  const int64_t warp = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  h = (int)(warp % p.L.nkv);
+  const int64_t row = (warp / p.L.nkv) * R + lane / LV;
+  t = (int)min(row, (int64_t)p.total);
+  j = lane % LV;
+  slot = t < p.total ? __ldg(p.slots + t) : -1;
+}
+// The slot, or -1 (and a flag) where it is none.
+__device__ __forceinline__ int paged_slot(const PagedRows& p, int slot, int j) {
+  if (slot == -1 || (slot >= 0 && (slot >> p.L.pshift) < p.L.npages)) return slot;
+  if (j == 0) set_status(p.status, FT_DEV_RANGE);
+  return -1;
+}
+
+// NaN where either is, else the larger.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kMagic = 12582912.0f;  // 1.5 2^23: |x| r + kMagic rounds to the nearest integer, ties to even
+
+// Codes of words g and g + 1 (values u[e][0] and u[e][1], as kMagic + magnitude; x the signed
+// values) as one register: magnitudes at bits 0, 3, 8, 11, signs at bits 15, 14, 7, 6 of each half.
+__device__ __forceinline__ uint32_t paged_pack(const f32x2 (&x)[4], const f32x2 (&u)[4]) {
+  constexpr uint32_t kTop = 0x4B400000u, kAll = (1u + (1u << 3) + (1u << 8) + (1u << 11)) * kTop;
+  uint32_t xs[4][2], w = 0u - kAll - (kAll << 16);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = bf16_bits_to_f32(src[8 * e]);
+  for (int e = 0; e < 4; ++e) {
+    float a, b;
+    u[e].get(a, b);
+    const int at = (e & 1) * 3 + (e >> 1) * 8;
+    w += (__float_as_uint(a) << at) + (__float_as_uint(b) << (at + 16));
+    x[e].get(a, b);
+    xs[e][0] = __float_as_uint(a), xs[e][1] = __float_as_uint(b);
   }
-  paged_fwht<D>(x, hb, norm);
-  float am = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-  bool bad = !(fabsf(x[0]) <= 3e38f && fabsf(x[1]) <= 3e38f && fabsf(x[2]) <= 3e38f && fabsf(x[3]) <= 3e38f);
+  // sign bytes: (value 0, value 2) and (value 1, value 3) as the halves' high and low bytes
+  const uint32_t s02 = prmt(prmt(xs[2][0], xs[0][0], 0x0073u), prmt(xs[2][1], xs[0][1], 0x0073u), 0x5410u);
+  const uint32_t s13 = prmt(prmt(xs[3][0], xs[1][0], 0x0073u), prmt(xs[3][1], xs[1][1], 0x0073u), 0x5410u);
+  return w | (s02 & 0x80808080u) | ((s13 >> 1) & 0x40404040u);
+}
+
+// Magnitude of the code of y = fl(|x| norm) by scale s, min(rne(fl(y / s)), 7), decided without a
+// division where c = rne(y / s) is right but perhaps for the side of a boundary.  With t the
+// nearest boundary, y - t s is exact; the FP32 quotient is t itself (and the even neighbour its
+// code) while that is within half a step of t, else its sign decides.
+__device__ __noinline__ float paged_edge(float y, float s, float c) {
+  if (!(s >= 1e-30f)) return s > 0.0f ? fminf(rintf(__fdiv_rn(y, s)), 7.0f) : 0.0f;
+  const float t = fmaf(-c, s, y) > 0.0f ? c + 0.5f : c - 0.5f, rem = fmaf(-t, s, y);
+  const float step = __uint_as_float((__float_as_uint(t) & 0x7F800000u) - (24u << 23));  // half a step above t
+  const float half = (rem < 0.0f && t == 0.5f) ? 0.5f * step : step;                     // below a power of two: half of it
+  const float lo = t - 0.5f, hi = t + 0.5f;
+  if (fabsf(rem) <= s * half) return ((int)lo & 1) ? hi : lo;
+  return fminf(rem > 0.0f ? hi : lo, 7.0f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) append_paged_kernel(const PagedRows p) {
+  constexpr int LV = D / 32;
+  int t, h, j, slot;
+  paged_row<D>(p, t, h, j, slot);
+  const bool is_v = blockIdx.y != 0;
+  f32x2 x[16];
+  if (t < p.total) {
+    const uint16_t* src = (is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) + h * D + 32 * j;
+    if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
 #pragma unroll
-  for (int o = LV / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  const uint16_t sb = quant_scale_bits(am);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = f32x2(bf16_bits_to_f32(__ldg(src + 2 * i)), bf16_bits_to_f32(__ldg(src + 2 * i + 1)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = f32x2(0.0f, 0.0f);
+  }
+  slot = paged_slot(p, slot, j);  // after the row's loads: its own load is under way beside them
+  paged_fwht<D>(x, p.hb);
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    x[i].get(a, b);
+    am = max_nan(am, max_nan(fabsf(a), fabsf(b)));
+  }
+#pragma unroll
+  for (int o = 1; o < LV; o <<= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+  const bool finite = am < INFINITY;
+  const uint16_t sb = quant_scale_bits(am * p.norm);
   const float s = bf16_bits_to_f32(sb);
-  int c[4];
+  // Codes by a reciprocal: |x| (norm r) is within 2^-22 (relative) of the quotient fl(x norm) / s
+  // rounded to FP32 that the quantiser takes its decision from, so the two agree unless it lies
+  // within 7 x 2^-21 of a rounding boundary; those few values are decided exactly.
+  const float r = s >= 1e-30f ? p.norm * __frcp_rn(s) : 0.0f;
+  const f32x2 r2(r, r), magic2(kMagic, kMagic), minus(-1.0f, -1.0f);
+  const float far = r > 0.0f || s == 0.0f ? 0.5f - 7.0f * 4.76837158203125e-07f : -1.0f;  // 7 x 2^-21
+  uint32_t hw[4];  // words 2 q and 2 q + 1 of this lane's 32 channels
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = max((int)quant_code(x[e], s) - 8, -7);
-  const uint32_t w = paged_pack(c[0], c[1], c[2], c[3]);
-  if (!live || slot == -1) return;
-  if (slot < 0 || (slot >> L.pshift) >= L.npages) {
-    if (lane == 0) set_status(status, FT_DEV_RANGE);
-    return;
+  for (int q = 0; q < 4; ++q) {
+    f32x2 xe[4], u[4];
+    float near = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, b;
+      xe[e] = x[4 * e + q];
+      xe[e].get(a, b);
+      const f32x2 mag(fabsf(a), fabsf(b));
+      u[e] = fma2(mag, r2, magic2);
+      fma2(mag, r2, fma2(u[e], minus, magic2)).get(a, b);
+      near = fmaxf(near, fmaxf(fabsf(a), fabsf(b)));
+    }
+    if (near >= far) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[2], m[2];
+        xe[e].get(v[0], v[1]);
+        u[e].get(m[0], m[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float a = fabsf(v[i]), c = m[i] - kMagic;
+          if (fabsf(fmaf(a, r, -c)) >= far) m[i] = kMagic + paged_edge(a * p.norm, s, c);
+        }
+        u[e] = f32x2(m[0], m[1]);
+      }
+    }
+    hw[q] = paged_pack(xe, u);
   }
-  if (bad) set_status(status, FT_DEV_RANGE);
-  const int p = slot & (L.psize - 1);
-  uint8_t* blk = pages + paged_block(L, slot >> L.pshift, h);
-  const uint32_t off = which ? L.voff + paged_v_word<D>(p, g, j) : paged_k_word<D>(p, g, j);
-  *reinterpret_cast<uint16_t*>(blk + off) = (uint16_t)w;
-  if (lane == 0) *reinterpret_cast<uint16_t*>(blk + L.soff + 4 * p + 2 * which) = sb;
+  // a NaN's "code" may spill over its neighbours' bits: such a row is not defined, only flagged
+  if (!finite && slot >= 0) set_status(p.status, FT_DEV_RANGE);
+  const int pos = max(slot, 0) & (p.L.psize - 1);
+  uint8_t* blk = p.pages + paged_block(p.L, max(slot, 0) >> p.L.pshift, h);
+  if (!is_v) {
+    if (slot >= 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint32_t*>(blk + paged_k_word<D>(pos, 2 * q, j)) = hw[q];
+    }
+  } else {
+    // the pair's other position in the neighbouring lanes: each side stores four whole words
+    const int other = __shfl_xor_sync(0xffffffffu, slot, LV);
+    const bool pair = slot >= 0 && other == (slot ^ 1);
+    const bool odd = (slot & 1) != 0;
+    uint32_t got[2], keep[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      got[q] = __shfl_xor_sync(0xffffffffu, odd ? hw[q] : hw[2 + q], LV);
+      keep[q] = odd ? hw[2 + q] : hw[q];
+    }
+    uint8_t* dst = blk + p.L.voff;
+    if (pair) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t even_w = odd ? got[q] : keep[q], odd_w = odd ? keep[q] : got[q];
+        const int g = (odd ? 4 : 0) + 2 * q;
+        *reinterpret_cast<uint32_t*>(dst + paged_v_word<D>(pos & ~1, g, j)) = prmt(even_w, odd_w, 0x5410u);
+        *reinterpret_cast<uint32_t*>(dst + paged_v_word<D>(pos & ~1, g + 1, j)) = prmt(even_w, odd_w, 0x7632u);
+      }
+    } else if (slot >= 0) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        *reinterpret_cast<uint16_t*>(dst + paged_v_word<D>(pos, g, j)) = (uint16_t)(hw[g / 2] >> (16 * (g & 1)));
+    }
+  }
+  if (slot >= 0 && j == 0) *reinterpret_cast<uint16_t*>(blk + p.L.soff + 4 * pos + (is_v ? 2 : 0)) = sb;
 }
 
 // Rows of the given slots as values in the model basis: decoded, rotated back,
 // rounded to BF16.
 template <int D>
-__global__ void __launch_bounds__(256) read_paged_kernel(const uint8_t* __restrict__ pages, PagedLayout L,
-                                                         const int32_t* __restrict__ slots,
-                                                         uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                                                         int64_t nvec, int hb, float norm, int32_t* status) {
-  constexpr int LV = D / 4;
-  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t vec = gid / LV;
-  const int lane = (int)(gid % LV), g = lane & 7, j = lane >> 3;
-  const bool live = vec < nvec;
-  const int which = (int)(vec & 1);
-  const int64_t th = vec >> 1;
-  const int h = (int)(th % L.nkv);
-  const int64_t t = th / L.nkv;
-  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (live) {
-    const int slot = slots[t];
-    if (slot >= 0 && (slot >> L.pshift) < L.npages) {
-      const int p = slot & (L.psize - 1);
-      const uint8_t* blk = pages + paged_block(L, slot >> L.pshift, h);
-      const uint32_t off = which ? L.voff + paged_v_word<D>(p, g, j) : paged_k_word<D>(p, g, j);
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(blk + off);
-      const float s = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(blk + L.soff + 4 * p + 2 * which));
+__global__ void __launch_bounds__(kRowThreads) read_paged_kernel(const PagedRows p) {
+  int t, h, j, slot;
+  paged_row<D>(p, t, h, j, slot);
+  slot = paged_slot(p, slot, j);
+  const bool is_v = blockIdx.y != 0;
+  const int pos = max(slot, 0) & (p.L.psize - 1);
+  const uint8_t* blk = p.pages + paged_block(p.L, max(slot, 0) >> p.L.pshift, h);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};  // words 2 q, 2 q + 1
+  float s = 0.0f;
+  if (slot >= 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = paged_value(w, e) * s;
-    } else if (slot != -1 && lane == 0) {
-      set_status(status, FT_DEV_RANGE);
+    for (int q = 0; q < 4; ++q) {
+      if (is_v) {
+        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q, j)));
+        const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q + 1, j)));
+        w[q] = prmt(a, b, (pos & 1) ? 0x7632u : 0x5410u);
+      } else {
+        w[q] = __ldg(reinterpret_cast<const uint32_t*>(blk + paged_k_word<D>(pos, 2 * q, j)));
+      }
+    }
+    const uint32_t both = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.soff + 4 * pos));
+    s = __uint_as_float(is_v ? both & 0xFFFF0000u : both << 16);
+  }
+  // the decoded halves are x 2^-24 (e even) and x 2^-20
+  const f32x2 s0(s * 16777216.0f, s * 16777216.0f), s1(s * 1048576.0f, s * 1048576.0f), norm2(p.norm, p.norm);
+  f32x2 x[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[4];
+    paged_word(w[q], r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[e]));
+      x[4 * e + q] = mul2(f32x2(f.x, f.y), (e & 1) ? s1 : s0);
     }
   }
-  paged_fwht<D>(x, hb, norm);
-  if (!live) return;
-  uint16_t* dst = (which ? v_out : k_out) + th * D + 32 * j + g;
+  paged_fwht<D>(x, p.hb);
+  if (t >= p.total) return;
+  uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)t * p.L.nkv + h) * D + 32 * j);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) dst[8 * e] = __bfloat16_as_ushort(__float2bfloat16_rn(x[e]));
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a, b;
+      mul2(x[4 * i + k], norm2).get(a, b);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+      o[k] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// Grid over (rows, heads) x (K, V); 0 blocks: too many.
+static dim3 row_grid(int total, int nkv, int d) {
+  const int per = 32 / (d / 32);
+  const int64_t warps = ((int64_t)total + per - 1) / per * nkv, blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  return dim3(blocks > INT32_MAX ? 0u : (unsigned)blocks, 2);
 }
 
 }  // namespace ft
@@ -321,13 +491,22 @@ int ft_kv_append_paged_int4(const ft_block_cfg* c, void* pages, int n_pages, int
   if (total == 0) return FT_OK;
   const int64_t row = (int64_t)c->n_kv * c->head_dim;
   if (!k_bf16 || !v_bf16 || !slots || k_stride < row || v_stride < row) return FT_ERR_INVALID_ARG;
-  const ft::PagedLayout L = ft::paged_layout(*c, n_pages, page_size);
-  const int64_t nvec = (int64_t)total * c->n_kv * 2, blocks = (nvec * (c->head_dim / 4) + 255) / 256;
-  if (blocks > (int64_t)INT32_MAX) return FT_ERR_UNSUPPORTED;
+  ft::PagedRows p = {};
+  p.k = k_bf16;
+  p.v = v_bf16;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.L = ft::paged_layout(*c, n_pages, page_size);
+  p.total = total;
+  p.hb = c->had_block;
+  p.norm = ft::paged_norm(c->had_block);
+  p.status = dev_status;
+  const dim3 grid = ft::row_grid(total, c->n_kv, c->head_dim);
+  if (grid.x == 0) return FT_ERR_UNSUPPORTED;
   const auto kernel = c->head_dim == 128 ? ft::append_paged_kernel<128> : ft::append_paged_kernel<64>;
-  kernel<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(k_bf16, k_stride, v_bf16, v_stride, slots,
-                                                             static_cast<uint8_t*>(pages), L, nvec, c->had_block,
-                                                             ft::paged_norm(c->had_block), dev_status);
+  kernel<<<grid, ft::kRowThreads, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
@@ -337,14 +516,21 @@ int ft_kv_read_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages,
   if (st != FT_OK) return st;
   if (total < 0) return FT_ERR_INVALID_ARG;
   if (total == 0) return FT_OK;
-  if (!slots || !k_out || !v_out) return FT_ERR_INVALID_ARG;
-  const ft::PagedLayout L = ft::paged_layout(*c, n_pages, page_size);
-  const int64_t nvec = (int64_t)total * c->n_kv * 2, blocks = (nvec * (c->head_dim / 4) + 255) / 256;
-  if (blocks > (int64_t)INT32_MAX) return FT_ERR_UNSUPPORTED;
+  if (!slots || !k_out || !v_out || !ft_host::aligned16(k_out) || !ft_host::aligned16(v_out)) return FT_ERR_INVALID_ARG;
+  ft::PagedRows p = {};
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.slots = slots;
+  p.pages = static_cast<uint8_t*>(const_cast<void*>(pages));
+  p.L = ft::paged_layout(*c, n_pages, page_size);
+  p.total = total;
+  p.hb = c->had_block;
+  p.norm = ft::paged_norm(c->had_block);
+  p.status = dev_status;
+  const dim3 grid = ft::row_grid(total, c->n_kv, c->head_dim);
+  if (grid.x == 0) return FT_ERR_UNSUPPORTED;
   const auto kernel = c->head_dim == 128 ? ft::read_paged_kernel<128> : ft::read_paged_kernel<64>;
-  kernel<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(static_cast<const uint8_t*>(pages), L, slots, k_out, v_out,
-                                                             nvec, c->had_block, ft::paged_norm(c->had_block),
-                                                             dev_status);
+  kernel<<<grid, ft::kRowThreads, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 

@@ -80,48 +80,47 @@ __device__ __forceinline__ void paged_word(uint32_t w, uint32_t (&r)[4]) {
   r[2] = sw & 0x80078007u;
   r[3] = (sw << 1) & 0x80708070u;
 }
-// Value e of a 16-bit word as a float (an integer in -7..7).
-__device__ __forceinline__ float paged_value(uint32_t w, int e) {
-  const int mag = (w >> ((e & 1) * 3 + (e >> 1) * 8)) & 7;
-  const int neg = (w >> (e == 0 ? 15 : e == 1 ? 14 : e == 2 ? 7 : 6)) & 1;
-  return (float)(neg ? -mag : mag);
-}
-// 16-bit word of four codes in -7..7.
-__device__ __forceinline__ uint32_t paged_pack(int c0, int c1, int c2, int c3) {
-  uint32_t w = (uint32_t)abs(c0) | ((uint32_t)abs(c1) << 3) | ((uint32_t)abs(c2) << 8) | ((uint32_t)abs(c3) << 11);
-  w |= (c0 < 0 ? 0x8000u : 0u) | (c1 < 0 ? 0x4000u : 0u) | (c2 < 0 ? 0x80u : 0u) | (c3 < 0 ? 0x40u : 0u);
-  return w;
-}
-
-// Normalised Walsh-Hadamard transform (order hb, natural order) of a d-vector held
-// by D / 4 neighbouring lanes: lane (g = channel bits 0-2, j = bits 5 and up) owns
-// the four channels 32 j + g + 8 e.  Strides 1, 2, 4, ... in this order, FP32, so
-// every lane layout and the plain form round alike.
+// Walsh-Hadamard transform (order hb, natural order, not yet normalised) of a d-vector
+// held by D / 32 neighbouring lanes, lane j owning channels 32 j .. 32 j + 31: five
+// strides inside a lane, the last two (one for d = 64) across lanes, so a vector costs 8
+// shuffles of a warp where four channels a lane would cost 20.  Strides 1, 2, 4, ... in
+// this order, FP32, so every lane layout and the plain form round alike.
+// Channels 2 i and 2 i + 1 are pair i: one instruction adds two.
 template <int D>
-__device__ __forceinline__ void paged_fwht(float (&v)[4], int hb, float norm) {
-  const int lane = threadIdx.x & 31;
-  auto across = [&](int s) {
+__device__ __forceinline__ void paged_fwht(f32x2 (&v)[16], int hb) {
+  const f32x2 minus(-1.0f, -1.0f);
+  if (hb > 1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float o = __shfl_xor_sync(0xffffffffu, v[e], s);
-      v[e] = (lane & s) ? (o - v[e]) : (v[e] + o);
+    for (int i = 0; i < 16; ++i) {
+      float a, b;
+      v[i].get(a, b);
+      v[i] = f32x2(a + b, a - b);
     }
-  };
-  if (hb > 1) across(1);
-  if (hb > 2) across(2);
-  if (hb > 4) across(4);
-  if (hb > 8) {
-    const float a = v[0], b = v[1], c = v[2], d = v[3];
-    v[0] = a + b, v[1] = a - b, v[2] = c + d, v[3] = c - d;
   }
-  if (hb > 16) {
-    const float a = v[0], b = v[1], c = v[2], d = v[3];
-    v[0] = a + c, v[2] = a - c, v[1] = b + d, v[3] = b - d;
-  }
-  if (hb > 32) across(8);
-  if (D == 128 && hb > 64) across(16);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] *= norm;
+  for (int s = 1; s < 16; s <<= 1) {
+    if (2 * s >= hb) break;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i & s) continue;
+      const f32x2 a = v[i], b = v[i + s];
+      v[i] = add2(a, b);
+      v[i + s] = fma2(b, minus, a);
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < D / 32; s <<= 1) {
+    if (32 * s >= hb) break;
+    const float sign = (threadIdx.x & s) ? -1.0f : 1.0f;
+    const f32x2 sign2(sign, sign);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a, b;
+      v[i].get(a, b);
+      const f32x2 o(__shfl_xor_sync(0xffffffffu, a, s), __shfl_xor_sync(0xffffffffu, b, s));
+      v[i] = fma2(sign2, v[i], o);
+    }
+  }
 }
 
 inline float paged_norm(int hb) { return (float)(1.0 / std::sqrt((double)hb)); }
