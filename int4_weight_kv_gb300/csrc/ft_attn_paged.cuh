@@ -1,0 +1,71 @@
+// What the kernels of attention over the paged 4-bit cache share.
+//
+//   o = H sum_j softmax_j(scale (H q) . K^_j) V^_j   over positions j <= the token's
+//
+// with K^_j = ks_j x codes and V^_j = vs_j x codes.  In log2 units, with lv_j =
+// log2(vs_j) and t_j = scale log2(e) (H q) . K^_j + lv_j:
+//   p_j = 2^(t_j - m),   o = (sum_j p_j codes_j) / (sum_j p_j / vs_j),
+// so the V scales never multiply the matrix product's operand P: it stays within
+// FP16 whatever the scales are, and one FMA applies both scales to a score.
+#pragma once
+
+#include "ft_paged.cuh"
+
+namespace ft {
+
+constexpr float kQUp = 64.0f;                 // query operand: q scale log2(e) x 64 (keeps q / 16 out of FP16's subnormals)
+constexpr float kKsUp = 262144.0f;            // 2^24 (codes are x 2^-24) / 64
+constexpr float kOUp = 16777216.0f;           // 2^24
+constexpr float kPBias = 10.0f;               // P = 2^(t - m + 10): FP16 normals down to 2^-24 of the largest weight
+constexpr float kPLazy = 4.0f;                // the running max moves when a score passes it by 2^4 (P < 2^14 + rounding)
+constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: smaller V scales count as this (their values are ~0)
+
+struct AttnPagedParams {
+  const uint8_t* pages;
+  PagedLayout L;
+  const uint16_t* q;
+  uint16_t* o;
+  int64_t q_stride, o_stride;
+  const int32_t *cu, *kv_len, *table;
+  int32_t* status;
+  int table_stride, B, total_q, max_q, G, hb;
+  float qscale, norm;  // scale log2(e) kQUp; 1 / sqrt(hb)
+};
+
+// One request's rows and length, checked (conditions to status, which may be NULL); false:
+// nothing of it is computed.
+__device__ __forceinline__ bool attn_request(const AttnPagedParams& p, int b, int32_t* status, int& row0, int& n, int& kv) {
+  row0 = p.cu[b];
+  n = p.cu[b + 1] - row0;
+  kv = p.kv_len[b];
+  if (row0 < 0 || n < 0 || row0 > p.total_q - n || n > p.max_q) {
+    set_status(status, FT_DEV_RANGE);
+    return false;
+  }
+  if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) {
+    set_status(status, FT_DEV_CAPACITY);
+    kv = 0;  // every row empty: zeros
+  }
+  return true;
+}
+
+// MUFU operations without the denormal handling of the library functions.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Requests with many rows (ft_attn_tiles.cu).
+cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, cudaStream_t st);
+
+}  // namespace ft
