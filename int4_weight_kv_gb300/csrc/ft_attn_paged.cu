@@ -22,13 +22,16 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 //
 // The work is the list of (request, head, 64 positions) units in this order; each CTA takes
 // an equal, contiguous share of it whatever the lengths are, and a warp of its four one
-// 16-position tile of each unit.  A share's segment that is a whole (request, head) is
-// finished in place; the others (at most the first and the last of a share) leave (max,
-// sum, accumulator) partials, which a second kernel adds in the order of the shares.
+// 16-position tile of each unit.  A share's segment (its part of one request and head) costs
+// about as much beside its tiles as kSegUnits units do, so each (request, head) counts that
+// many more, ahead of its first: without them the shares that hold many short requests took
+// twice as long as the others (32 requests of 1 to 4096 positions: 38 us, 54% of the SMs' time).
+// A segment that is a whole (request, head) is finished in place; the others leave (max, sum,
+// accumulator) partials, which a second kernel adds in the order of the shares.
 //   S = K q:     A = K codes (rows positions), B = q (columns the rows)
 //   O^T = V^T P: A = V codes (rows channels), B = P transposed in registers
 // Tiles come through a ring of kApStages per warp by 16-byte asynchronous copies.
-constexpr int kUnit = 16 * kApWarps;
+constexpr int kUnit = 16 * kApWarps, kSegUnits = 3;
 constexpr int kApStages = 4;
 constexpr int kApMaxB = 8192;
 
@@ -44,7 +47,7 @@ struct SplitWs {
 __device__ __forceinline__ int attn_units(const AttnPagedParams& p, int b, bool flag) {
   int row0, n, kv;
   if (!attn_request(p, b, flag ? p.status : nullptr, row0, n, kv) || n == 0) return 0;
-  return p.L.nkv * max(1, (kv + kUnit - 1) / kUnit);
+  return p.L.nkv * (kSegUnits + max(1, (kv + kUnit - 1) / kUnit));
 }
 // First unit of CTA c's share, and the CTA that holds unit u (shares of per or per + 1).
 __device__ __forceinline__ int share_begin(int units, int ctas, int c) {
@@ -83,7 +86,10 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
   {
     const int per = (p.B + kApWarps * 32 - 1) / (kApWarps * 32), b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += attn_units(p, b, blockIdx.x == 0);
+    for (int b = b0; b < b1; ++b) {
+      pref[b] = sum;  // within the thread's requests, for now
+      sum += attn_units(p, b, blockIdx.x == 0);
+    }
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -94,10 +100,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     __syncthreads();
     int at = inc - sum;
     for (int w = 0; w < warp; ++w) at += warp_tot[w];
-    for (int b = b0; b < b1; ++b) {
-      pref[b] = at;
-      at += attn_units(p, b, false);
-    }
+    for (int b = b0; b < b1; ++b) pref[b] += at;
+    at += sum;
     if (b1 == p.B && b0 < b1) pref[p.B] = at;
     __syncthreads();
     if (blockIdx.x == 0)
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
   }
   const int units = pref[p.B], ctas = gridDim.x;
   int u = share_begin(units, ctas, blockIdx.x);
-  const int u_begin = u, u_end = share_begin(units, ctas, blockIdx.x + 1);
+  const int u_end = share_begin(units, ctas, blockIdx.x + 1);
   if (u == u_end) return;
   int b;
   {
@@ -120,8 +124,11 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
 
   while (u < u_end) {
     while (pref[b + 1] <= u) ++b;
-    const int nu = (pref[b + 1] - pref[b]) / p.L.nkv, h = (u - pref[b]) / nu;
-    const int k0 = u - pref[b] - h * nu, k1 = min(nu, k0 + (u_end - u));
+    const int nv = (pref[b + 1] - pref[b]) / p.L.nkv, nu = nv - kSegUnits, h = (u - pref[b]) / nv;
+    const int at = u - pref[b] - h * nv, step = min(nv - at, u_end - u);
+    const int k0 = max(at - kSegUnits, 0), k1 = max(at + step - kSegUnits, 0);
+    u += step;
+    if (k0 == k1) continue;  // the share ends in what the segment costs beside its units
     const int row0 = p.cu[b], n = p.cu[b + 1] - row0, nrow = n * p.G;
     int kv = p.kv_len[b];
     if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) kv = 0;
@@ -130,26 +137,29 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     const int t0 = k0 * kApWarps + warp, t1 = min(k1 * kApWarps, (kv + 15) / 16);
 
     // asynchronous copy of one tile into its ring slot; a page outside the pool is left out
-    // (its scales are set so that every position is masked)
+    // (its scales are set so that every position is masked).  The page of the tile after it is
+    // looked up ahead, so that no copy waits for its address.
+    const uint32_t page_bytes = (uint32_t)p.L.nkv * p.L.block, ring0 = smem_u32(ring) + lane * 16;
+    const uint8_t* lane_base = p.pages + (size_t)h * p.L.block + lane * 16;
+    auto page_at = [&](int t) { return t < t1 ? __ldg(table + ((16 * t) >> p.L.pshift)) : 0; };
+    int page_ahead = page_at(t0);
     auto load = [&](int t, int slot) {
+      const int page = page_ahead;
+      page_ahead = page_at(t + kApWarps);
       if (t < t1) {
-        const int p0 = 16 * t, pin = p0 & (p.L.psize - 1);
-        const int page = __ldg(table + (p0 >> p.L.pshift));
-        uint8_t* dst = ring + slot * T::kTile;
-        if (page >= 0 && page < p.L.npages) {
-          const uint8_t* blk = p.pages + paged_block(p.L, page, h);
-          const uint8_t* ksrc = blk + pin * (D / 2) + lane * 16;
-          const uint8_t* vsrc = blk + p.L.voff + pin * (D / 2) + lane * 16;
-          const uint32_t d0 = smem_u32(dst) + lane * 16;
+        const uint32_t pin = (16 * t) & (p.L.psize - 1), d0 = ring0 + slot * T::kTile;
+        if ((uint32_t)page < (uint32_t)p.L.npages) {
+          const uint8_t* ksrc = lane_base + (uint64_t)(uint32_t)page * page_bytes + pin * (D / 2);
+          const uint8_t* vsrc = ksrc + p.L.voff;
 #pragma unroll
           for (int i = 0; i < 8 * D; i += 512) {
             cp_async16(d0 + i, ksrc + i);
             cp_async16(d0 + 8 * D + i, vsrc + i);
           }
-          if (lane < 4) cp_async16(d0 + 16 * D, blk + p.L.soff + 4 * pin + lane * 16);
+          if (lane < 4) cp_async16(d0 + 16 * D, ksrc + p.L.soff - pin * (D / 2 - 4));
         } else {
           if (lane == 0) set_status(p.status, FT_DEV_RANGE);
-          if (lane < 16) reinterpret_cast<uint32_t*>(dst + 16 * D)[lane] = 0xFFFFFFFFu;  // NaN scales: see below
+          if (lane < 16) reinterpret_cast<uint32_t*>(ring + slot * T::kTile + 16 * D)[lane] = 0xFFFFFFFFu;  // NaN scales: see below
         }
       }
       cp_async_commit();
@@ -194,10 +204,11 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     const int all = kv - n;  // positions up to this are visible to every row
 
     float acc[NT][KT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], u0[NT][2];  // running max, sum, and max - kPBias (0 for none yet)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t][0] = m[t][1] = -INFINITY;
+      u0[t][0] = u0[t][1] = -kPBias;
       l[t][0] = l[t][1] = 0.0f;
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) acc[t][mt][0] = acc[t][mt][1] = acc[t][mt][2] = acc[t][mt][3] = 0.0f;
@@ -289,6 +300,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
           x0 = fmaxf(x0, m[c][0]), x1 = fmaxf(x1, m[c][1]);
           const float f0 = m[c][0] == x0 ? 1.0f : ex2(m[c][0] - x0), f1 = m[c][1] == x1 ? 1.0f : ex2(m[c][1] - x1);
           m[c][0] = x0, m[c][1] = x1;
+          u0[c][0] = (x0 == -INFINITY ? 0.0f : x0) - kPBias;
+          u0[c][1] = (x1 == -INFINITY ? 0.0f : x1) - kPBias;
           l[c][0] *= f0, l[c][1] *= f1;
 #pragma unroll
           for (int mt = 0; mt < KT; ++mt)
@@ -298,9 +311,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
       uint32_t pb[NT][2];
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        const float u0 = (m[c][0] == -INFINITY ? 0.0f : m[c][0]) - kPBias;
-        const float u1 = (m[c][1] == -INFINITY ? 0.0f : m[c][1]) - kPBias;
-        const float e0 = ex2(s[c][0] - u0), e1 = ex2(s[c][1] - u1), e2 = ex2(s[c][2] - u0), e3 = ex2(s[c][3] - u1);
+        const float e0 = ex2(s[c][0] - u0[c][0]), e1 = ex2(s[c][1] - u0[c][1]);
+        const float e2 = ex2(s[c][2] - u0[c][0]), e3 = ex2(s[c][3] - u0[c][1]);
         l[c][0] = fmaf(e0, rs0, fmaf(e2, rs1, l[c][0]));
         l[c][1] = fmaf(e1, rs0, fmaf(e3, rs1, l[c][1]));
         const __half2 pa2 = __floats2half2_rn(e0, e1), pb2 = __floats2half2_rn(e2, e3);
@@ -341,7 +353,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nu;
-    float* out = ws.part + (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * (8 * NT * PW);
+    // at most one segment of a share continues another share's (slot 0), one other is continued (slot 1)
+    float* out = ws.part + (size_t)(2 * blockIdx.x + (k0 == 0 ? 1 : 0)) * (8 * NT * PW);
     for (int r = warp; r < min(8 * NT, nrow); r += kApWarps) {
       float M = -INFINITY;
 #pragma unroll
@@ -372,48 +385,79 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
       }
     }
     __syncthreads();  // part and qs are free again
-    u += k1 - k0;
   }
 }
 
 // Joins the partials of the (request, head) pairs that several CTAs shared, one warp
-// per row, in the order of the shares.
+// per row, in the order of the shares; eight partials' loads in flight.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnPagedParams p, const SplitWs ws, int ctas) {
-  constexpr int NPL = D / 32, PW = D + 4;
-  const int lane = threadIdx.x & 31, rb = (8 * NT + 3) / 4;
+  constexpr int PW = D + 4, CH = D / 32, kBatch = 8;  // channels CH lane .. + CH - 1 of each lane
+  const int lane = threadIdx.x & 31, rb = 2 * NT;
   const int r = 4 * (blockIdx.x % rb) + (threadIdx.x >> 5), bh = blockIdx.x / rb, h = bh % p.L.nkv, b = bh / p.L.nkv;
+  const int row0 = p.cu[b], n = p.cu[b + 1] - row0;  // (not the few-rows kernel's: no need to wait)
   griddep_wait();
-  const int first = __ldcg(ws.pref + b), nu = (__ldcg(ws.pref + b + 1) - first) / p.L.nkv, units = __ldcg(ws.pref + p.B);
-  if (nu == 0) return;
-  const int row0 = p.cu[b], n = p.cu[b + 1] - row0;
-  if (r >= n * p.G) return;
-  const int u0 = first + h * nu, u1 = u0 + nu;
-  const int c0 = share_of(units, ctas, u0), c1 = share_of(units, ctas, u1 - 1);
+  const int first = __ldcg(ws.pref + b), next = __ldcg(ws.pref + b + 1), units = __ldcg(ws.pref + p.B);
+  if (next == first || r >= n * p.G) return;
+  const int nv = (next - first) / p.L.nkv, v0 = first + h * nv;
+  const int c0 = share_of(units, ctas, v0 + kSegUnits), c1 = share_of(units, ctas, v0 + nv - 1);
   if (c0 == c1) return;
-  auto row = [&](int c) {
-    return ws.part + ((size_t)(2 * c + (share_begin(units, ctas, c) < u0 ? 1 : 0)) * (8 * NT) + r) * PW;
-  };
+  // the first share's partial in its slot 1, the others' in their slot 0
+  const float* base = ws.part + (size_t)r * PW;
+  auto row = [&](int c) { return base + (size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT * PW); };
   float M = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(row(c)));
   M = warp_max(M);
-  float lt = 0.0f, o[NPL] = {};
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float* q = row(c);
-    const float mc = __ldcg(q), f = mc == M ? 1.0f : ex2(mc - M);
-    lt = fmaf(f, __ldcg(q + 1), lt);
+  float lt = 0.0f, o[CH] = {};
+  for (int c = c0; c <= c1; c += kBatch) {
+    float2 ml[kBatch];
+    float x[kBatch][CH];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) o[i] = fmaf(f, __ldcg(q + 4 + lane + 32 * i), o[i]);
+    for (int i = 0; i < kBatch; ++i) {
+      if (c + i > c1) continue;
+      const float* q = row(c + i);
+      ml[i] = __ldcg(reinterpret_cast<const float2*>(q));
+      if constexpr (D == 128) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(q + 4) + lane);
+        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(q + 4) + lane);
+        x[i][0] = f.x, x[i][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (c + i > c1) continue;
+      const float f = ml[i].x == M ? 1.0f : ex2(ml[i].x - M);
+      lt = fmaf(f, ml[i].y, lt);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) o[k] = fmaf(f, x[i][k], o[k]);
+    }
   }
   const float inv = lt == 0.0f ? 0.0f : kOUp / lt;
+  // the rotation of neighbouring channels, strides 1 (and 2) in the lane, the others across lanes
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) o[i] *= inv;
-  warp_fwht<NPL>(o, p.hb);
+  for (int k = 0; k < CH; ++k) o[k] *= inv;
+#pragma unroll
+  for (int s = 1; s < CH; s <<= 1) {
+    if (s >= p.hb) break;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      if (k & s) continue;
+      const float a = o[k], c = o[k + s];
+      o[k] = a + c;
+      o[k + s] = a - c;
+    }
+  }
+  for (int s = 1; CH * s < p.hb; s <<= 1) {
+    const float sign = (lane & s) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) o[k] = fmaf(sign, o[k], __shfl_xor_sync(0xffffffffu, o[k], s));
+  }
   const int tok = r / p.G, hh = r - tok * p.G;
-  uint16_t* dst = p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D;
+  uint16_t* dst = p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D + CH * lane;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) dst[lane + 32 * i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
+  for (int k = 0; k < CH; ++k) dst[k] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k] * p.norm));
 }
 
 // CTAs of the few-rows kernel: every SM filled (its occupancy by registers and ring).
@@ -448,7 +492,7 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.L.nkv * ((8 * NT + 3) / 4)));
+  cfg.gridDim = dim3((unsigned)(p.B * p.L.nkv * 2 * NT));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -486,7 +530,7 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
   if (!ft_host::aligned16(workspace)) return FT_ERR_INVALID_ARG;
   if (B > ft::kApMaxB) return FT_ERR_UNSUPPORTED;
   // units of work are counted in 32 bits
-  if (((int64_t)table_stride * page_size / ft::kUnit + 1) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
+  if (((int64_t)table_stride * page_size / ft::kUnit + 1 + ft::kSegUnits) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
   if (ws_bytes < ft_attn_paged_workspace_bytes(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;
   ft::AttnPagedParams p = {};
   p.pages = static_cast<const uint8_t*>(pages);
