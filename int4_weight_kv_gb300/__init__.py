@@ -128,41 +128,62 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _current():
+    """(current CUDA device, its current stream's handle).  The stream object that
+    torch.cuda.current_stream() builds costs 3 us a call, its handle alone 0.1."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.init()
+        _raw_stream = (torch.cuda.current_device, get or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    dev = _raw_stream[0]()
+    return dev, _raw_stream[1](dev)
+
+
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current()[1]
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _on_device(*tensors) -> None:
-    """Every tensor (None and raw pointers aside) lives on the current CUDA device."""
-    import torch
-    here = torch.cuda.current_device()
+def _check_device(*tensors) -> int:
+    """Every tensor (None and raw pointers aside) lives on the current CUDA device; returns its current stream."""
+    here, stream = _current()
     for t in tensors:
-        if t is not None and not isinstance(t, int) and (not t.is_cuda or t.get_device() != here):
+        if t is not None and not isinstance(t, int) and t.get_device() != here:
             raise ValueError(f"tensor on {t.device}, the current device is cuda:{here}")
+    return stream
 
 
 def _plain(t, nbytes: int):
     """A contiguous tensor of nbytes-wide elements (or None, or a raw pointer)."""
-    if t is not None and not isinstance(t, int) and (t.element_size() != nbytes or not t.is_contiguous()):
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != nbytes or not t.is_contiguous():
         raise ValueError(f"need a contiguous tensor of {nbytes}-byte elements, got {t.dtype} with strides {t.stride()}")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _rows(t, inner: int, nbytes: int) -> tuple[int, int]:
     """(pointer, elements between rows) of a tensor whose rows are `inner` contiguous nbytes-wide elements."""
-    want, good = 1, t.element_size() == nbytes and t.dim() >= 2
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        good = good and (step == want or size == 1)
-        want *= size
+    shape = t.shape
+    if t.is_contiguous() and t.element_size() == nbytes and len(shape) >= 2 and t.numel() == shape[0] * inner:
+        return t.data_ptr(), inner
+    step = t.stride()
+    want, good = 1, t.element_size() == nbytes and len(shape) >= 2
+    for i in range(len(shape) - 1, 0, -1):
+        good = good and (step[i] == want or shape[i] == 1)
+        want *= shape[i]
     if not good or want != inner:
-        raise ValueError(f"need rows of {inner} contiguous {nbytes}-byte elements, got {t.dtype} {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    return t.data_ptr(), max(t.stride(0), inner) if t.shape[0] <= 1 else t.stride(0)
+        raise ValueError(f"need rows of {inner} contiguous {nbytes}-byte elements, got {t.dtype} {tuple(shape)} "
+                         f"with strides {step}")
+    return t.data_ptr(), step[0] if shape[0] > 1 else max(step[0], inner)
 
 
 def make_cfg(hidden, n_q, n_kv, head_dim, inter, had_block=0, kv_group=0, rms_eps=1e-5, rope_base=500000.0,
@@ -253,24 +274,24 @@ def ft_kv_pages_bytes(cfg, n_pages: int, page_size: int) -> int:
 def ft_kv_page_map(page_size, n_pages, ctx_len, new_len, B, block_table, free_pages, free_head, free_head_out,
                    cu_seqlens, kv_len, slots, dev_status=None, stream=None) -> int:
     """block_table: int32 [B, >= pages of a request]; the other tensors int32, one-dimensional."""
-    _on_device(ctx_len, new_len, block_table, free_pages, free_head, free_head_out, cu_seqlens, kv_len, slots, dev_status)
+    here = _check_device(ctx_len, new_len, block_table, free_pages, free_head, free_head_out, cu_seqlens, kv_len, slots, dev_status)
     if min(ctx_len.numel(), new_len.numel(), kv_len.numel(), cu_seqlens.numel() - 1, block_table.shape[0]) < B:
         raise ValueError(f"lengths, prefix sums or block tables of fewer than {B} requests")
     table, stride = _rows(block_table, block_table.shape[1], 4)
     return lib().ft_kv_page_map(page_size, n_pages, _plain(ctx_len, 4), _plain(new_len, 4), B, table, stride,
                                 _plain(free_pages, 4), free_pages.numel(), _plain(free_head, 4),
                                 _plain(free_head_out, 4), _plain(cu_seqlens, 4), _plain(kv_len, 4), _plain(slots, 4),
-                                slots.numel(), _ptr(dev_status), _stream(stream))
+                                slots.numel(), _ptr(dev_status), here if stream is None else _stream(stream))
 
 
 def _check_pool(cfg, pages, n_pages, page_size) -> None:
-    if not isinstance(pages, int) and pages.numel() * pages.element_size() < ft_kv_pages_bytes(cfg, n_pages, page_size):
-        raise ValueError(f"a pool of {pages.numel() * pages.element_size()} bytes does not hold {n_pages} pages")
+    if not isinstance(pages, int) and pages.numel() < n_pages * cfg.n_kv * page_size * (cfg.head_dim + 4):
+        raise ValueError(f"a pool of {pages.numel()} bytes does not hold {n_pages} pages")
 
 
 def ft_kv_append_paged_int4(cfg, pages, n_pages, page_size, k, v, slots, total, dev_status=None, stream=None) -> int:
     """k, v: BF16 [>= total, n_kv, d], rows at any stride; slots: int32 [>= total]."""
-    _on_device(pages, k, v, slots, dev_status)
+    here = _check_device(pages, k, v, slots, dev_status)
     _check_pool(cfg, pages, n_pages, page_size)
     if min(k.shape[0], v.shape[0], slots.numel()) < total:
         raise ValueError(f"fewer than {total} rows or slots")
@@ -278,18 +299,18 @@ def ft_kv_append_paged_int4(cfg, pages, n_pages, page_size, k, v, slots, total, 
     kp, ks = _rows(k, row, 2)
     vp, vs = _rows(v, row, 2)
     return lib().ft_kv_append_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, kp, ks, vp, vs,
-                                         _plain(slots, 4), total, _ptr(dev_status), _stream(stream))
+                                         _plain(slots, 4), total, _ptr(dev_status), here if stream is None else _stream(stream))
 
 
 def ft_kv_read_paged_int4(cfg, pages, n_pages, page_size, slots, total, k_out, v_out, dev_status=None,
                           stream=None) -> int:
     """k_out, v_out: BF16 [>= total, n_kv, d], contiguous; slots: int32 [>= total]."""
-    _on_device(pages, slots, k_out, v_out, dev_status)
+    here = _check_device(pages, slots, k_out, v_out, dev_status)
     _check_pool(cfg, pages, n_pages, page_size)
     if min(k_out.numel(), v_out.numel()) < total * cfg.n_kv * cfg.head_dim or slots.numel() < total:
         raise ValueError(f"fewer than {total} rows or slots")
     return lib().ft_kv_read_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, _plain(slots, 4), total,
-                                       _plain(k_out, 2), _plain(v_out, 2), _ptr(dev_status), _stream(stream))
+                                       _plain(k_out, 2), _plain(v_out, 2), _ptr(dev_status), here if stream is None else _stream(stream))
 
 
 def ft_attn_paged_workspace_bytes(cfg, B: int, total_q: int, max_q: int) -> int:
@@ -299,7 +320,7 @@ def ft_attn_paged_workspace_bytes(cfg, B: int, total_q: int, max_q: int) -> int:
 def ft_attn_paged_int4(cfg, pages, n_pages, page_size, q, cu_seqlens, kv_len, block_table, B, total_q, max_q, scale, o,
                        workspace, dev_status=None, stream=None) -> int:
     """q, o: BF16 [>= total_q, n_q, d], rows at any stride; block_table: int32 [>= B, pages of a request]."""
-    _on_device(pages, q, cu_seqlens, kv_len, block_table, o, workspace, dev_status)
+    here = _check_device(pages, q, cu_seqlens, kv_len, block_table, o, workspace, dev_status)
     _check_pool(cfg, pages, n_pages, page_size)
     if min(q.shape[0], o.shape[0]) < total_q or min(cu_seqlens.numel() - 1, kv_len.numel(), block_table.shape[0]) < B:
         raise ValueError(f"fewer than {total_q} rows or {B} requests")
@@ -310,7 +331,7 @@ def ft_attn_paged_int4(cfg, pages, n_pages, page_size, q, cu_seqlens, kv_len, bl
     return lib().ft_attn_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, qp, qs,
                                     _plain(cu_seqlens, 4), _plain(kv_len, 4), table, stride, B, total_q, max_q, scale,
                                     op, os_, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _ptr(dev_status), _stream(stream))
+                                    _ptr(dev_status), here if stream is None else _stream(stream))
 
 
 def ft_decode_workspace_bytes(cfg, B: int, max_ctx: int) -> int:
@@ -371,7 +392,7 @@ def ft_rmsnorm_bf16(x, gamma, z, B, H, eps, stream=None) -> int:
 def ft_logprobs(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, top_k, dev_status=None,
                 stream=None) -> int:
     """logits: FP32 or BF16 [N, V], rows at any stride; targets: int32 [N] or None; outputs may be None."""
-    _on_device(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev_status)
+    here = _check_device(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev_status)
     n, v = logits.shape
     dtype = FT_F32 if logits.element_size() == 4 else FT_BF16
     x, stride = _rows(logits, v, 4 if dtype == FT_F32 else 2)
@@ -380,7 +401,7 @@ def ft_logprobs(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, 
             raise ValueError(f"an argument holds {t.numel()} of {size} elements")
     return lib().ft_logprobs(x, dtype, stride, n, v, _plain(targets, 4), top_k, _plain(logprob, 4), _plain(entropy, 4),
                              _plain(rank, 4), _plain(top_ids, 4), _plain(top_logprobs, 4), _ptr(dev_status),
-                             _stream(stream))
+                             here if stream is None else _stream(stream))
 
 
 def ft_read_device_status(dev_status, stream=None) -> int:

@@ -287,30 +287,34 @@ class Attn:
         return worst
 
 
+def _case(*args, **more):
+    return args, more
+
+
 ATTN = [
     # single tokens: one, a tile's edges, pages of each size, ragged, requests without rows
-    Attn(8, 2, 64, 16, [1], [1]), Attn(32, 8, 128, 64, [1], [1025]), Attn(8, 8, 128, 16, [1, 1, 1], [15, 16, 17]),
-    Attn(32, 8, 128, 128, [1] * 5, [127, 128, 129, 1, 700]), Attn(64, 8, 128, 32, [1, 0, 1], [333, 64, 2]),
-    Attn(42, 6, 64, 64, [1] * 9, [5, 63, 64, 65, 1, 400, 128, 31, 33], pad=12),
-    Attn(12, 4, 128, 16, [1, 1], [4000, 3], had=32), Attn(4, 4, 64, 128, [1], [513], had=1),
+    _case(8, 2, 64, 16, [1], [1]), _case(32, 8, 128, 64, [1], [1025]), _case(8, 8, 128, 16, [1, 1, 1], [15, 16, 17]),
+    _case(32, 8, 128, 128, [1] * 5, [127, 128, 129, 1, 700]), _case(64, 8, 128, 32, [1, 0, 1], [333, 64, 2]),
+    _case(42, 6, 64, 64, [1] * 9, [5, 63, 64, 65, 1, 400, 128, 31, 33], pad=12),
+    _case(12, 4, 128, 16, [1, 1], [4000, 3], had=32), _case(4, 4, 64, 128, [1], [513], had=1),
     # drafts of a few tokens
-    Attn(32, 8, 128, 64, [2, 5, 1], [2, 700, 64]), Attn(64, 8, 128, 16, [4, 3], [68, 1000], pad=16), Attn(8, 2, 64, 32, [7, 8], [7, 90]),
+    _case(32, 8, 128, 64, [2, 5, 1], [2, 700, 64]), _case(64, 8, 128, 16, [4, 3], [68, 1000], pad=16), _case(8, 2, 64, 32, [7, 8], [7, 90]),
     # prompts and chunks: row and key tiles' edges, no history, long history, odd groups
-    Attn(8, 2, 64, 16, [33, 1, 65, 130], [33, 50, 65, 1000]), Attn(32, 8, 128, 64, [64, 63, 65], [64, 127, 300]),
-    Attn(16, 2, 128, 32, [129, 0, 17], [129, 10, 400]), Attn(6, 2, 128, 128, [100, 200], [357, 200]),
-    Attn(4, 4, 128, 16, [300, 128], [300, 256]), Attn(42, 6, 64, 64, [90, 40], [217, 40], pad=2), Attn(7, 1, 128, 64, [259], [640]),
-    Attn(64, 8, 128, 64, [48, 80], [1500, 80], had=64),
+    _case(8, 2, 64, 16, [33, 1, 65, 130], [33, 50, 65, 1000]), _case(32, 8, 128, 64, [64, 63, 65], [64, 127, 300]),
+    _case(16, 2, 128, 32, [129, 0, 17], [129, 10, 400]), _case(6, 2, 128, 128, [100, 200], [357, 200]),
+    _case(4, 4, 128, 16, [300, 128], [300, 256]), _case(42, 6, 64, 64, [90, 40], [217, 40], pad=2), _case(7, 1, 128, 64, [259], [640]),
+    _case(64, 8, 128, 64, [48, 80], [1500, 80], had=64),
     # tokens before position 0 see nothing; a request whose cache is empty
-    Attn(8, 2, 64, 16, [5, 3, 1], [2, 0, 0]), Attn(8, 2, 128, 64, [150, 90], [70, 0]), Attn(32, 8, 128, 64, [1, 1], [0, 9]),
+    _case(8, 2, 64, 16, [5, 3, 1], [2, 0, 0]), _case(8, 2, 128, 64, [150, 90], [70, 0]), _case(32, 8, 128, 64, [1, 1], [0, 9]),
     # sharp softmaxes, tiny and huge V scales
-    Attn(8, 2, 128, 64, [40], [500], spread=16.0), Attn(8, 2, 64, 16, [1, 1], [300, 77], spread=16.0),
-    Attn(8, 2, 128, 64, [1, 70], [300, 300], vscale=1e20), Attn(8, 2, 64, 64, [1, 70], [300, 300], vscale=1e-20),
+    _case(8, 2, 128, 64, [40], [500], spread=16.0), _case(8, 2, 64, 16, [1, 1], [300, 77], spread=16.0),
+    _case(8, 2, 128, 64, [1, 70], [300, 300], vscale=1e20), _case(8, 2, 64, 64, [1, 70], [300, 300], vscale=1e-20),
 ]
 
 
 @pytest.mark.parametrize("i", range(len(ATTN)))
 def test_attention(i):
-    a = ATTN[i]
+    a = Attn(*ATTN[i][0], **ATTN[i][1])
     o, st = a.run()
     assert st == 0
     a.check(o)
