@@ -4,13 +4,19 @@
 // A CTA owns up to 256 rows (tokens x heads of a group, two tiles of M = 128) of one
 // request and KV head and walks the visible positions in tiles of 128:
 //   S = Q K^T   A = Q from shared memory, B = K codes from shared memory
-//   O += P V    A = P from tensor memory (over S's columns), B = V codes from shared memory
-// both with FP16 operands and FP32 accumulators in tensor memory (S 2 x 128 columns, O
-// 2 x d columns).  K and V are decoded once per CTA for both tiles: codes become FP16
-// subnormals (7 integer instructions per 8 values, no offset), in the 128-byte-swizzled
+//   O += P V    A = P from tensor memory (over S's columns), B = V from shared memory
+// with FP16 operands and FP32 accumulators in tensor memory (S 2 x 128 columns, O 2 x d
+// columns).  K and V are decoded once per CTA for both tiles into the 128-byte-swizzled
 // K-major layout; the order of the channels inside a K step is the cache's own, and Q is
-// written in the same order.  The scales stay out of the operands: score = S ks + log2 vs
-// in one FMA, the sum of weights takes p / vs (ft_attn_paged.cu).
+// written in the same order.
+//
+// Scales are multiplied into the operands, relative to a power of two per 32 positions:
+// a scale has 8 significant bits and a code 3, so the product is exact in FP16 down to 2^-8
+// of the group's largest scale.  The groups' powers of two, kf for K and 2^f for V, come
+// back as one factor and one term of each score, t = S kf + f: P = 2^(t - m) weighs V's
+// operand, and the sum of weights takes 2^-f per group.  (Scales applied per column in the
+// softmax needed 96 broadcast 16-byte reads a row and tile, 49 KB of shared-memory bandwidth
+// a warp: 5500 cycles per pair of tiles.)
 //
 // Roles: two warpgroups of softmax (one row per thread, a tile each), one warpgroup
 // decoding (the next tile's bytes in flight in registers), one issuing thread.  While one
@@ -28,10 +34,11 @@ namespace tiles {
 
 constexpr int kThreads = 512, kRows = 256, kKeys = 128;
 constexpr int kMmaWarp = 12;
-constexpr int kScaleRing = 4;
+constexpr float kOScale = 512.0f;  // the operands hold V's values x 2^-9
+constexpr int kScaleRing = 4;  // per tile and group of 32 positions: kf, f, 2^-f, mask of the positions that exist
 // Registers of a thread by role (softmax twice, decode, issue): the sum over the four
 // warpgroups is what the block is launched with, kThreads x 128.
-constexpr int kRegSoftmax = 192, kRegDecode = 88, kRegIssue = 40;
+constexpr int kRegSoftmax = 184, kRegDecode = 112, kRegIssue = 32;
 static_assert(2 * kRegSoftmax + kRegDecode + kRegIssue <= 4 * 128, "more registers than the block has");
 
 template <int D>
@@ -40,7 +47,7 @@ struct Cfg {
   static constexpr int kQ = 128 * D * 2;                 // one tile's query operand
   static constexpr int kK = kKeys * D * 2, kV = kKeys * D * 2;  // one stage
   static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffScale = kOffV + 2 * kV;
-  static constexpr int kOffBar = kOffScale + kScaleRing * 3 * kKeys * 4;
+  static constexpr int kOffBar = kOffScale + kScaleRing * 64;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment slack
   static constexpr int kColO = 256;                    // tensor memory: S0, S1, then O0, O1
 };
@@ -94,6 +101,16 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
          ((uint64_t)2 << 61);
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -106,31 +123,6 @@ __device__ __forceinline__ void regs_down() {
 // A wait of a whole warp with one outcome: its accesses to tensor memory are warp-wide.
 __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-
-// Walsh-Hadamard transform of a whole row held by one thread (pairs of channels).
-template <int D>
-__device__ __forceinline__ void row_fwht(f32x2 (&v)[D / 2], int hb) {
-  const f32x2 minus(-1.0f, -1.0f);
-  if (hb > 1) {
-#pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
-      float a, b;
-      v[i].get(a, b);
-      v[i] = f32x2(a + b, a - b);
-    }
-  }
-#pragma unroll
-  for (int s = 1; s < D / 2; s <<= 1) {
-    if (2 * s >= hb) break;
-#pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
-      if (i & s) continue;
-      const f32x2 a = v[i], b = v[i + s];
-      v[i] = add2(a, b);
-      v[i + s] = fma2(b, minus, a);
-    }
-  }
 }
 
 }  // namespace tiles
@@ -226,66 +218,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  float* scales = reinterpret_cast<float*>(sm + C::kOffScale);  // [ring][ks, lv, rs][kKeys]
+  float4* scales = reinterpret_cast<float4*>(sm + C::kOffScale);  // [ring][kf, f, 2^-f, mask][4 groups]
   bool ok = true;
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax: one row per thread
     regs_up<kRegSoftmax>();
     const int t = warp >> 2, row = tid & 127, r = r0 + 128 * t + row;
-    const bool live = 128 * t + row < nrow;
-    const int tok = min(r / p.G, n - 1), hh = r - (r / p.G) * p.G;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    // a warp's 32 rows are read and written by D / 32 lanes each, 32 channels a lane
+    constexpr int LV = D / 32, RW = 32 / LV;
+    const int lj = lane % LV;
+    auto row_at = [&](int it) { return 32 * (warp & 3) + it * RW + lane / LV; };
     if (t < ntile) {
-      {  // the rotated query row as the FP16 operand, channels in the order of the cache's words
-        f32x2 v[D / 2];
-        const uint16_t* src = p.q + (row0 + tok) * p.q_stride + (int64_t)(h * p.G + hh) * D;
-        if (!live) {
+      // ---- the rotated query rows as the FP16 operand, channels in the order of the cache's words
+      // (rows that see nothing need none: the epilogue of tile 0 may then overtake this of tile 1)
+#pragma unroll 1
+      for (int it = 0; it < (nkt > 0 ? LV : 0); ++it) {
+        const int rr = row_at(it), rg = r0 + 128 * t + rr, tok = rg / p.G, hh = rg - tok * p.G;
+        f32x2 v[16];
+        if (128 * t + rr < nrow) {
+          const uint16_t* src = p.q + (row0 + tok) * p.q_stride + (int64_t)(h * p.G + hh) * D + 32 * lj;
+          if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) v[i] = f32x2(0.0f, 0.0f);
-        } else if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+            for (int i = 0; i < 4; ++i) {
+              const uint4 q = *(reinterpret_cast<const uint4*>(src) + i);
+              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+              for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            }
+          } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            for (int i = 0; i < 16; ++i) v[i] = f32x2(bf16_bits_to_f32(src[2 * i]), bf16_bits_to_f32(src[2 * i + 1]));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) v[i] = f32x2(bf16_bits_to_f32(__ldg(src + 2 * i)), bf16_bits_to_f32(__ldg(src + 2 * i + 1)));
+          for (int i = 0; i < 16; ++i) v[i] = f32x2(0.0f, 0.0f);
         }
-        row_fwht<D>(v, p.hb);
-        const float f0 = p.qscale * p.norm, f1 = f0 * 0.0625f;
+        paged_fwht<D>(v, p.hb);
+        const float f0 = p.qscale * p.norm;
         bool bad = false;
-        uint8_t* qs = sm + C::kOffQ + t * C::kQ + row * 128;
+        uint8_t* qs = sm + C::kOffQ + t * C::kQ + rr * 128;
 #pragma unroll
-        for (int w = 0; w < D / 8; ++w) {  // word w = (tig, j): channels 32 j + 2 tig + 8 e + {0, 1}
+        for (int tig = 0; tig < 4; ++tig) {  // word (tig, lj): channels 2 tig + 8 e + {0, 1} of the lane's
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float a, c;
-            v[16 * (w % NJ) + (w / NJ) + 4 * e].get(a, c);
-            a *= (e & 1) ? f1 : f0;
-            c *= (e & 1) ? f1 : f0;
-            const float top = (e & 1) ? 4094.0f : 65504.0f;
-            bad |= !(fabsf(a) <= top) || !(fabsf(c) <= top);
+            v[tig + 4 * e].get(a, c);
+            a *= f0, c *= f0;
+            bad |= !(fabsf(a) <= 65504.0f) || !(fabsf(c) <= 65504.0f);
             const __half2 hv = __floats2half2_rn(a, c);
             o[e] = *reinterpret_cast<const uint32_t*>(&hv);
           }
-          *reinterpret_cast<uint4*>(qs + (w / 8) * (128 * 128) + (((w % 8) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          const int w = tig * NJ + lj;
+          *reinterpret_cast<uint4*>(qs + (w / 8) * (128 * 128) + (((w % 8) ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (bad) set_status(p.status, FT_DEV_RANGE);
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full + 8 * t);
 
+      const int tok = min(r / p.G, n - 1);
       const int lim = kv - n + tok;  // last position this row sees
       const int lim_all = kv - n + (r0 + 128 * t + 32 * (warp & 3)) / p.G;  // and that every row of the warp sees
-      float m = -INFINITY;
-      f32x2 l2(0.0f, 0.0f);
+      float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < nkt; ++j) {
-        const float* sc = scales + (j % kScaleRing) * 3 * kKeys;
         if (!all_wait(s_full + 8 * t, j & 1) || !all_wait(sc_full + 8 * (j % kScaleRing), (j / kScaleRing) & 1)) {
           ok = false;
           break;
@@ -294,97 +292,119 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         uint32_t s[kKeys];
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_ld32(tmem + lane_base + 128 * t + c, s + c);
+        const float4* sc = scales + 4 * (j % kScaleRing);
+        const float4 kf4 = sc[0], f4 = sc[1], rf4 = sc[2];
+        const uint4 mask4 = reinterpret_cast<const uint4*>(sc)[3];
+        const float kf[4] = {kf4.x, kf4.y, kf4.z, kf4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w}, rf[4] = {rf4.x, rf4.y, rf4.z, rf4.w};
         wait_ld();
+        // a tile that some row of the warp sees in part, or with positions on a page outside the pool
+        if (kKeys * j + kKeys - 1 > lim_all || (mask4.x & mask4.y & mask4.z & mask4.w) != 0xFFFFFFFFu) {
+          const uint32_t mask[4] = {mask4.x, mask4.y, mask4.z, mask4.w};
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            s[c] = kKeys * j + c <= lim && ((mask[c / 32] >> (c % 32)) & 1u) ? s[c] : 0xFF800000u;
+        }
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 4) {
-          const float4 ks = *reinterpret_cast<const float4*>(sc + c), lv = *reinterpret_cast<const float4*>(sc + kKeys + c);
-          float x0, x1, x2, x3;
-          fma2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), f32x2(ks.x, ks.y), f32x2(lv.x, lv.y)).get(x0, x1);
-          fma2(f32x2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), f32x2(ks.z, ks.w), f32x2(lv.z, lv.w)).get(x2, x3);
-          s[c] = __float_as_uint(x0), s[c + 1] = __float_as_uint(x1), s[c + 2] = __float_as_uint(x2), s[c + 3] = __float_as_uint(x3);
-        }
-        if (kKeys * j + kKeys - 1 > lim_all) {  // a tile that some row of the warp sees in part
+        for (int g = 0; g < 4; ++g) {
+          float q[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = kKeys * j + c <= lim ? s[c] : 0xFF800000u;
-        }
+          for (int c = 32 * g; c < 32 * g + 32; c += 4)
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
+            for (int k = 0; k < 2; ++k) q[k] = max3(q[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+          mx = fmaxf(mx, fmaf(fmaxf(q[0], q[1]), kf[g], f[g]));
+        }
         const bool need = mx > m + kPLazy;
         if (__any_sync(0xffffffffu, need)) {
           const float to = need ? mx : m;
-          const float f = to == m ? 1.0f : ex2(m - to);
+          const float fac = to == m ? 1.0f : ex2(m - to);
           m = to;
           if (j > 0) {
-            l2 = mul2(l2, f32x2(f, f));
+            l *= fac;
             if (!all_wait(o_full + 8 * t, (j - 1) & 1)) {  // the tensor core is done with O
               ok = false;
               break;
             }
             fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o);
               wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
               tmem_st32(tmem + lane_base + C::kColO + D * t + c, o);
             }
           }
         }
         const float u = kPBias - (m == -INFINITY ? 0.0f : m);
-        const f32x2 u2(u, u);
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 64) {
+        for (int g2 = 0; g2 < 2; ++g2) {
           uint32_t o[32];
 #pragma unroll
-          for (int c = c0; c < c0 + 64; c += 4) {
-            const float4 rs = *reinterpret_cast<const float4*>(sc + 2 * kKeys + c);
-            float x0, x1, x2, x3;
-            add2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), u2).get(x0, x1);
-            add2(f32x2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), u2).get(x2, x3);
-            x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
-            l2 = fma2(f32x2(x0, x1), f32x2(rs.x, rs.y), l2);
-            l2 = fma2(f32x2(x2, x3), f32x2(rs.z, rs.w), l2);
-            const __half2 h0 = __floats2half2_rn(x0, x1), h1 = __floats2half2_rn(x2, x3);
-            o[(c - c0) / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-            o[(c - c0) / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          for (int g = 2 * g2; g < 2 * g2 + 2; ++g) {
+            const f32x2 kf2(kf[g], kf[g]), u2(u + f[g], u + f[g]);
+            f32x2 sum[2] = {f32x2(0.0f, 0.0f), f32x2(0.0f, 0.0f)};
+#pragma unroll
+            for (int c = 32 * g; c < 32 * g + 32; c += 2) {
+              float x0, x1;
+              fma2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), kf2, u2).get(x0, x1);
+              x0 = ex2(x0), x1 = ex2(x1);
+              sum[(c / 2) & 1] = add2(sum[(c / 2) & 1], f32x2(x0, x1));
+              const __half2 hv = __floats2half2_rn(x0, x1);
+              o[(c - 64 * g2) / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            float a, c;
+            add2(sum[0], sum[1]).get(a, c);
+            l = fmaf(a + c, rf[g], l);
           }
-          tmem_st32(tmem + lane_base + 128 * t + c0 / 2, o);
+          tmem_st32(tmem + lane_base + 128 * t + 32 * g2, o);
         }
         wait_st();
         fence_before();
         mbar_arrive(p_full + 8 * t);
       }
-      // ---- epilogue: O / l, the rotation undone, BF16
+      // ---- epilogue: O / l through shared memory (the operands of QK are done with: tile 0 takes
+      // Q's room, tile 1 K's), then rotated back and stored row by row
       if (ok && nkt > 0 && !all_wait(o_full + 8 * t, (nkt - 1) & 1)) ok = false;
       if (ok) {
         fence_after();
-        float la, lb;
-        l2.get(la, lb);
-        const float l = la + lb, inv = l == 0.0f ? 0.0f : kOUp / l;  // a row that sees nothing: zeros
-        const f32x2 f0(inv, inv), f1(inv * 0.0625f, inv * 0.0625f);
-        f32x2 v[D / 2];
-        if (nkt > 0) {
-          uint32_t o[D];
+        const float inv = l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
+        float4* area = reinterpret_cast<float4*>(sm + (t == 0 ? C::kOffQ : C::kOffK));
+        auto at = [&](int rr, int c4) { return area + rr * (D / 4) + (c4 ^ (rr & 7) ^ (c4 >> 3)); };
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (nkt > 0) {
+            tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o);
+            wait_ld();
+          } else {
 #pragma unroll
-          for (int c = 0; c < D; c += 32) tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o + c);
-          wait_ld();
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i)
-            v[i] = mul2(f32x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), (i & 4) ? f1 : f0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 2; ++i) v[i] = f32x2(0.0f, 0.0f);
+          for (int i = 0; i < 32; i += 4)
+            *at(row, (c + i) / 4) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
         }
-        row_fwht<D>(v, p.hb);
-        const f32x2 norm2(p.norm, p.norm);
-        if (live) {
-          uint16_t* dst = p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D;
+        __syncwarp();
+#pragma unroll 1
+        for (int it = 0; it < LV; ++it) {
+          const int rr = row_at(it), rg = r0 + 128 * t + rr, tk = rg / p.G, hh = rg - tk * p.G;
+          f32x2 v[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 q = *at(rr, 8 * lj + i);
+            v[2 * i] = f32x2(q.x, q.y);
+            v[2 * i + 1] = f32x2(q.z, q.w);
+          }
+          paged_fwht<D>(v, p.hb);
+          if (128 * t + rr >= nrow) continue;
+          const f32x2 norm2(p.norm, p.norm);
+          uint16_t* dst = p.o + (row0 + tk) * p.o_stride + (int64_t)(h * p.G + hh) * D + 32 * lj;
           const bool aligned = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -409,35 +429,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ decode K and V
     regs_down<kRegDecode>();
-    const int w4 = warp - 8, dt = tid - 256;
-    constexpr int KR = D / 32;  // K: 16-byte (d = 128) or 8-byte pieces, four (tig) a key
-    // round i covers keys 32 i + 8 w4 .. + 7 of a tile: this lane's K piece is (key lane & 7, column lane >> 3),
-    // its V words are those of channels (g = lane & 7, j = lane >> 3), for d = 64 (j = (lane >> 3) & 1)
-    // with the pairs split between the lane halves
-    uint32_t kw[4][KR];
-    uint32_t vw[4][D == 128 ? 4 : 2];
-    uint32_t sc_next = 0;
-    bool sc_ok = false;
-    auto page_of = [&](int pos) {  // -1 behind the end; a page outside the pool is flagged
-      if (pos >= kv) return -1;
-      const int page = __ldg(table + (pos >> p.L.pshift));
-      if (page >= 0 && page < p.L.npages) return page;
-      set_status(p.status, FT_DEV_RANGE);
-      return -1;
+    const int w4 = warp - 8;  // positions 32 w4 .. 32 w4 + 31 of each tile
+    constexpr int NW = D == 128 ? 4 : 2;  // words of a K piece; V words a lane takes of a group of 8 positions
+    // Group i (positions 8 i .. 8 i + 7 of the warp's): this lane's K piece is (position lane & 7, column
+    // lane >> 3); its V words are those of channels (g = lane & 7, j = lane >> 3) for the four pairs,
+    // for d = 64 (j = (lane >> 3) & 1) for two of them.  Scales and pages belong to position `lane`.
+    uint32_t kw[4][NW], vw[4][NW], sc = 0u;
+    int page = -1, page_next = -1;
+    bool there = false;
+    auto page_of = [&](int j) {  // raw entry; positions behind the end: -1
+      const int pos = kKeys * j + 32 * w4 + lane;
+      return pos < kv ? __ldg(table + (pos >> p.L.pshift)) : -1;
     };
+    // bytes of tile j on their way into registers; the pages of tile j + 1 are looked up with them
     auto load_k = [&](int j) {
-      const int pos = kKeys * j + dt;  // this thread's scale
-      const int sp = page_of(pos);
-      sc_ok = sp >= 0;
-      if (sc_ok)
-        sc_next = ld_stream_u32(p.pages + paged_block(p.L, sp, h) + p.L.soff + 4 * (pos & (p.L.psize - 1)));
+      page = page_next;
+      const int pos = kKeys * j + 32 * w4 + lane;
+      there = pos < kv && (uint32_t)page < (uint32_t)p.L.npages;
+      if (pos < kv && !there) set_status(p.status, FT_DEV_RANGE);
+      if (!there) page = -1;
+      sc = there ? ld_stream_u32(p.pages + paged_block(p.L, page, h) + p.L.soff + 4 * (pos & (p.L.psize - 1))) : 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int p0 = kKeys * j + 32 * i + 8 * w4, page = page_of(p0);
+        const int pg = __shfl_sync(0xffffffffu, page, 8 * i), pin = (kKeys * j + 32 * w4 + 8 * i) & (p.L.psize - 1);
 #pragma unroll
-        for (int k = 0; k < KR; ++k) kw[i][k] = 0u;
-        if (page >= 0) {
-          const uint8_t* src = p.pages + paged_block(p.L, page, h) + ((p0 & (p.L.psize - 1)) + (lane & 7)) * (D / 2) + (lane >> 3) * (D / 8);
+        for (int k = 0; k < NW; ++k) kw[i][k] = 0u;
+        if (pg >= 0) {
+          const uint8_t* src = p.pages + paged_block(p.L, pg, h) + (pin + (lane & 7)) * (D / 2) + (lane >> 3) * (D / 8);
           if constexpr (D == 128) {
             const uint4 q = ld_stream_v4(src);
             kw[i][0] = q.x, kw[i][1] = q.y, kw[i][2] = q.z, kw[i][3] = q.w;
@@ -451,57 +469,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     auto load_v = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int p0 = kKeys * j + 32 * i + 8 * w4, page = page_of(p0);
-        constexpr int NW = D == 128 ? 4 : 2;
+        const int pg = __shfl_sync(0xffffffffu, page, 8 * i), pin = (kKeys * j + 32 * w4 + 8 * i) & (p.L.psize - 1);
 #pragma unroll
         for (int k = 0; k < NW; ++k) vw[i][k] = 0u;
-        if (page >= 0) {
-          const uint8_t* blk = p.pages + paged_block(p.L, page, h) + p.L.voff;
-          const int pair0 = (p0 & (p.L.psize - 1)) >> 1, g = lane & 7;
+        if (pg >= 0) {
+          const uint8_t* blk = p.pages + paged_block(p.L, pg, h) + p.L.voff;
 #pragma unroll
           for (int k = 0; k < NW; ++k) {
-            const int pair = D == 128 ? pair0 + k : pair0 + 2 * (lane >> 4) + k, jj = D == 128 ? lane >> 3 : (lane >> 3) & 1;
-            vw[i][k] = ld_stream_u32(blk + pair * D + (g ^ paged_v_turn<D>(pair)) * (D / 8) + 4 * jj);
+            const int pair = (pin >> 1) + (D == 128 ? k : 2 * (lane >> 4) + k), jj = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+            vw[i][k] = ld_stream_u32(blk + pair * D + ((lane & 7) ^ paged_v_turn<D>(pair)) * (D / 8) + 4 * jj);
           }
         }
       }
+      page_next = page_of(j + 1);
     };
     if (nkt > 0) {
+      page_next = page_of(0);
       load_k(0);
       load_v(0);
     }
     for (int j = 0; j < nkt; ++j) {
       const int st = j & 1;
-      if (j >= 2 && !mbar_wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) {
+      // the 32 positions' scales relative to their largest's power of two, as multipliers of the
+      // decoded words (codes x 2^-24 and, for odd values, x 2^-20): code x (scale / 2^e) x 2^-9
+      const uint32_t ek = max(__reduce_max_sync(0xffffffffu, (sc & 0x7FFFu) >> 7), 27u);
+      const uint32_t ev = max(__reduce_max_sync(0xffffffffu, (sc >> 23) & 0xFFu), 27u);
+      const float mk = __uint_as_float(sc << 16) * __uint_as_float((268u - ek) << 23);
+      const float mv = __uint_as_float(sc & 0xFFFF0000u) * __uint_as_float((268u - ev) << 23);
+      const __half2 mk2 = __floats2half2_rn(mk, mk * 0.0625f);  // (even, odd values)
+      const uint32_t mku = *reinterpret_cast<const uint32_t*>(&mk2);
+      const float mv_next = __shfl_down_sync(0xffffffffu, mv, 1);
+      const __half2 mv2 = __floats2half2_rn(mv, mv_next);  // at even lanes: a pair of positions
+      const uint32_t mvu = *reinterpret_cast<const uint32_t*>(&mv2);
+      const uint32_t exist = __ballot_sync(0xffffffffu, there);
+      if (j >= 2 && !all_wait(k_empty + 8 * st, ((j - 2) >> 1) & 1)) {
         ok = false;
         break;
+      }
+      if (lane == 0) {
+        float* dst = reinterpret_cast<float*>(scales + 4 * (j % kScaleRing)) + w4;
+        dst[0] = __uint_as_float(min(ek + 4u, 254u) << 23);  // 2^(e + 9) / kQUp, e = ek - 126
+        dst[4] = (float)((int)ev - 126);
+        dst[8] = __uint_as_float((ev > 252u ? 1u : 253u - ev) << 23);
+        dst[12] = __uint_as_float(exist);
       }
       {
         uint8_t* kd = sm + C::kOffK + st * C::kK;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = 32 * i + 8 * w4 + (lane & 7);
+          const int key = 32 * w4 + 8 * i + (lane & 7);
+          const uint32_t both = __shfl_sync(0xffffffffu, mku, 8 * i + (lane & 7));
+          const uint32_t m0 = prmt(both, both, 0x1010u), m1 = prmt(both, both, 0x3232u);
 #pragma unroll
-          for (int k = 0; k < KR; ++k) {
+          for (int k = 0; k < NW; ++k) {
             const int w = (lane >> 3) * NJ + k;  // word of the entry: slots 8 w .. 8 w + 7 of the operand's row
             uint32_t r[4];
             paged_word(kw[i][k], r);
             *reinterpret_cast<uint4*>(kd + (w / 8) * (kKeys * 128) + key * 128 + (((w % 8) ^ (key & 7)) << 4)) =
-                make_uint4(r[0], r[1], r[2], r[3]);
+                make_uint4(hmul2(r[0], m0), hmul2(r[1], m1), hmul2(r[2], m0), hmul2(r[3], m1));
           }
         }
-        // scales of the tile; positions behind the end (or on no page) are masked by them
-        float* sc = scales + (j % kScaleRing) * 3 * kKeys;
-        const float vs = fmaxf(__uint_as_float(sc_next & 0xFFFF0000u), kMinScale);
-        sc[dt] = sc_ok ? __uint_as_float(sc_next << 16) * kKsUp : 0.0f;
-        sc[kKeys + dt] = sc_ok ? lg2(vs) : -INFINITY;
-        sc[2 * kKeys + dt] = sc_ok ? rcp(vs) : 0.0f;
       }
       fence_proxy_async_smem();
       mbar_arrive(sc_full + 8 * (j % kScaleRing));
       mbar_arrive(k_full + 8 * st);
       if (j + 1 < nkt) load_k(j + 1);
-      if (j >= 2 && !mbar_wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) {
+      if (j >= 2 && !all_wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) {
         ok = false;
         break;
       }
@@ -509,28 +542,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         uint8_t* vd = sm + C::kOffV + st * C::kV;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int chunk = 4 * i + w4;  // 8 positions
+          const int chunk = 4 * w4 + i;  // 8 positions
           uint8_t* panel = vd + (chunk / 8) * (D * 128);
-          if constexpr (D == 128) {
-            uint32_t r[4][4];
+          uint32_t r[NW][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) paged_word(vw[i][k], r[k]);
+          for (int k = 0; k < NW; ++k) {
+            const uint32_t m0 = __shfl_sync(0xffffffffu, mvu, 8 * i + 2 * (D == 128 ? k : 2 * (lane >> 4) + k));
+            const uint32_t m1 = hmul2(m0, 0x2C002C00u);  // / 16
+            paged_word(vw[i][k], r[k]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int ch = 32 * (lane >> 3) + (lane & 7) + 8 * e;
-              *reinterpret_cast<uint4*>(panel + ch * 128 + (((chunk % 8) ^ (ch & 7)) << 4)) =
-                  make_uint4(r[0][e], r[1][e], r[2][e], r[3][e]);
-            }
-          } else {
-            uint32_t r[2][4];
+            for (int e = 0; e < 4; ++e) r[k][e] = hmul2(r[k][e], (e & 1) ? m1 : m0);
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) paged_word(vw[i][k], r[k]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int ch = 32 * ((lane >> 3) & 1) + (lane & 7) + 8 * e;
-              *reinterpret_cast<uint2*>(panel + ch * 128 + (((chunk % 8) ^ (ch & 7)) << 4) + 8 * (lane >> 4)) =
-                  make_uint2(r[0][e], r[1][e]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int ch = 32 * (D == 128 ? lane >> 3 : (lane >> 3) & 1) + (lane & 7) + 8 * e;
+            uint8_t* dst = panel + ch * 128 + (((chunk % 8) ^ (ch & 7)) << 4);
+            if constexpr (D == 128)
+              *reinterpret_cast<uint4*>(dst) = make_uint4(r[0][e], r[1][e], r[2][e], r[3][e]);
+            else
+              *reinterpret_cast<uint2*>(dst + 8 * (lane >> 4)) = make_uint2(r[0][e], r[1][e]);
           }
         }
       }
