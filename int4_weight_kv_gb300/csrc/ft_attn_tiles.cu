@@ -38,7 +38,8 @@ constexpr float kOScale = 512.0f;  // the operands hold V's values x 2^-9
 constexpr int kScaleRing = 4;  // per tile and group of 32 positions: kf, f, 2^-f, mask of the positions that exist
 // Registers of a thread by role (softmax twice, decode, issue): the sum over the four
 // warpgroups is what the block is launched with, kThreads x 128.
-constexpr int kRegSoftmax = 184, kRegDecode = 112, kRegIssue = 32;
+constexpr int kRegSoftmax = 176, kRegDecode = 96, kRegIssue = 64;
+constexpr int kRegCommon = 128;  // before and after the roles
 static_assert(2 * kRegSoftmax + kRegDecode + kRegIssue <= 4 * 128, "more registers than the block has");
 
 template <int D>
@@ -77,29 +78,40 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The issuing warp runs converged and one lane's predicate (`lead`) guards each operation: addresses
+// and descriptors then stay in uniform registers.  Issued from a branch that a single lane takes, a
+// product took 110 cycles beside the three busy warps of its scheduler; alone on an SM it takes 64.
+// The shared-memory operands' descriptors come as (low word, kDescHi): a step along K adds to the
+// low word only.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row atoms of 1024 bytes, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFF) >> 4) | (1u << 16); }
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
-      "l"(b), "r"(idesc), "r"(acc)
+      "{ .reg .pred p, e; .reg .b64 x, y; mov.b64 x, {%1, %4}; mov.b64 y, {%2, %4}; setp.ne.u32 p, %5, 0;\n"
+      "setp.ne.u32 e, %6, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "n"(ACC ? 1 : 0), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
-      "l"(b), "r"(idesc), "r"(acc)
+      "{ .reg .pred p, e; .reg .b64 y; mov.b64 y, {%2, %4}; setp.ne.u32 p, %5, 0;\n"
+      "setp.ne.u32 e, %6, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.u32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 // FP32 accumulator, FP16 operands, both K-major.
 constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// K-major tile of 128-byte-swizzled rows: 8-row atoms of 1024 bytes.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -193,11 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   const int* table = p.table + (size_t)b * p.table_stride;
 
   const uint32_t bar = sm32 + C::kOffBar;
-  const uint32_t q_full = bar, s_full = bar + 16, p_full = bar + 32, o_full = bar + 48, k_full = bar + 64,
+  const uint32_t s_full = bar + 16, p_full = bar + 32, o_full = bar + 48, k_full = bar + 64,
                  k_empty = bar + 80, v_full = bar + 96, v_empty = bar + 112, sc_full = bar + 128, drained = bar + 160;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 128);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
       mbar_init(o_full + 8 * i, 1);
@@ -214,10 +225,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // ---- the rotated query rows as the FP16 operand, channels in the order of the cache's words: all
+  // warps, D / 32 lanes a row with 32 channels each, the next rows' loads in flight
+  constexpr int LV = D / 32, RW = 32 / LV;     // lanes of a row, rows of a warp at once
+  constexpr int kRowIt = kRows / (RW * (kThreads / 32));  // times that all warps' rows cover the CTA's
+  const int lj = lane % LV;
+  auto row_at = [&](int it) { return it * (kRows / kRowIt) + warp * RW + lane / LV; };
+  auto row_ptr = [&](int rr) {  // element offset of row rr (token, head) beside the row stride
+    const int rg = r0 + rr, tok = rg / p.G;
+    return make_int2(row0 + tok, (h * p.G + rg - tok * p.G) * D + 32 * lj);
+  };
+  if (nkt > 0) {
+    uint4 raw[kRowIt][4];
+#pragma unroll
+    for (int it = 0; it < kRowIt; ++it) {
+      const int rr = row_at(it);
+      const int2 at = row_ptr(rr);
+      const uint16_t* src = p.q + at.x * p.q_stride + at.y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[it][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < nrow) {
+          if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+            raw[it][i] = *(reinterpret_cast<const uint4*>(src) + i);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = (uint32_t)src[8 * i + 2 * k] | ((uint32_t)src[8 * i + 2 * k + 1] << 16);
+            raw[it][i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    const float f0 = p.qscale * p.norm;
+    const f32x2 f2(f0, f0);
+    uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
+#pragma unroll
+    for (int it = 0; it < kRowIt; ++it) {
+      const int rr = row_at(it);
+      f32x2 v[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {raw[it][i].x, raw[it][i].y, raw[it][i].z, raw[it][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+      }
+      paged_fwht<D>(v, p.hb);
+      uint8_t* qs = sm + C::kOffQ + rr * 128;
+      qs += (rr >= 128) ? C::kQ - 128 * 128 : 0;  // the second tile's operand
+#pragma unroll
+      for (int tig = 0; tig < 4; ++tig) {  // word (tig, lj): channels 2 tig + 8 e + {0, 1} of the lane's
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a, c;
+          mul2(v[tig + 4 * e], f2).get(a, c);
+          const __half2 hv = __floats2half2_rn(a, c);
+          o[e] = *reinterpret_cast<const uint32_t*>(&hv);
+          over = hfma2(o[e], 0u, over);
+        }
+        const int w = tig * NJ + lj;
+        *reinterpret_cast<uint4*>(qs + (w / 8) * (128 * 128) + (((w % 8) ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    if ((over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
+    fence_proxy_async_smem();
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  auto out_at = [&](int rr, int c4) {  // 4 channels of row rr on their way out
+    const int q = rr & 127;
+    return reinterpret_cast<float4*>(sm + (rr < 128 ? C::kOffQ : C::kOffK)) + q * (D / 4) + (c4 ^ (q & 7) ^ (c4 >> 3));
+  };
   float4* scales = reinterpret_cast<float4*>(sm + C::kOffScale);  // [ring][kf, f, 2^-f, mask][4 groups]
   bool ok = true;
 
@@ -226,59 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     regs_up<kRegSoftmax>();
     const int t = warp >> 2, row = tid & 127, r = r0 + 128 * t + row;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    // a warp's 32 rows are read and written by D / 32 lanes each, 32 channels a lane
-    constexpr int LV = D / 32, RW = 32 / LV;
-    const int lj = lane % LV;
-    auto row_at = [&](int it) { return 32 * (warp & 3) + it * RW + lane / LV; };
     if (t < ntile) {
-      // ---- the rotated query rows as the FP16 operand, channels in the order of the cache's words
-      // (rows that see nothing need none: the epilogue of tile 0 may then overtake this of tile 1)
-#pragma unroll 1
-      for (int it = 0; it < (nkt > 0 ? LV : 0); ++it) {
-        const int rr = row_at(it), rg = r0 + 128 * t + rr, tok = rg / p.G, hh = rg - tok * p.G;
-        f32x2 v[16];
-        if (128 * t + rr < nrow) {
-          const uint16_t* src = p.q + (row0 + tok) * p.q_stride + (int64_t)(h * p.G + hh) * D + 32 * lj;
-          if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 q = *(reinterpret_cast<const uint4*>(src) + i);
-              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = f32x2(bf16_bits_to_f32(src[2 * i]), bf16_bits_to_f32(src[2 * i + 1]));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = f32x2(0.0f, 0.0f);
-        }
-        paged_fwht<D>(v, p.hb);
-        const float f0 = p.qscale * p.norm;
-        bool bad = false;
-        uint8_t* qs = sm + C::kOffQ + t * C::kQ + rr * 128;
-#pragma unroll
-        for (int tig = 0; tig < 4; ++tig) {  // word (tig, lj): channels 2 tig + 8 e + {0, 1} of the lane's
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a, c;
-            v[tig + 4 * e].get(a, c);
-            a *= f0, c *= f0;
-            bad |= !(fabsf(a) <= 65504.0f) || !(fabsf(c) <= 65504.0f);
-            const __half2 hv = __floats2half2_rn(a, c);
-            o[e] = *reinterpret_cast<const uint32_t*>(&hv);
-          }
-          const int w = tig * NJ + lj;
-          *reinterpret_cast<uint4*>(qs + (w / 8) * (128 * 128) + (((w % 8) ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        if (bad) set_status(p.status, FT_DEV_RANGE);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full + 8 * t);
-
       const int tok = min(r / p.G, n - 1);
       const int lim = kv - n + tok;  // last position this row sees
       const int lim_all = kv - n + (r0 + 128 * t + 32 * (warp & 3)) / p.G;  // and that every row of the warp sees
@@ -364,14 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         fence_before();
         mbar_arrive(p_full + 8 * t);
       }
-      // ---- epilogue: O / l through shared memory (the operands of QK are done with: tile 0 takes
-      // Q's room, tile 1 K's), then rotated back and stored row by row
+      // ---- O / l to shared memory (the operands of QK are done with: tile 0 takes Q's room, tile 1 K's)
       if (ok && nkt > 0 && !all_wait(o_full + 8 * t, (nkt - 1) & 1)) ok = false;
       if (ok) {
         fence_after();
         const float inv = l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
-        float4* area = reinterpret_cast<float4*>(sm + (t == 0 ? C::kOffQ : C::kOffK));
-        auto at = [&](int rr, int c4) { return area + rr * (D / 4) + (c4 ^ (rr & 7) ^ (c4 >> 3)); };
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -384,48 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
           }
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *at(row, (c + i) / 4) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+            *out_at(128 * t + row, (c + i) / 4) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
                                                 __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int it = 0; it < LV; ++it) {
-          const int rr = row_at(it), rg = r0 + 128 * t + rr, tk = rg / p.G, hh = rg - tk * p.G;
-          f32x2 v[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 q = *at(rr, 8 * lj + i);
-            v[2 * i] = f32x2(q.x, q.y);
-            v[2 * i + 1] = f32x2(q.z, q.w);
-          }
-          paged_fwht<D>(v, p.hb);
-          if (128 * t + rr >= nrow) continue;
-          const f32x2 norm2(p.norm, p.norm);
-          uint16_t* dst = p.o + (row0 + tk) * p.o_stride + (int64_t)(h * p.G + hh) * D + 32 * lj;
-          const bool aligned = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float a, c;
-              mul2(v[4 * i + k], norm2).get(a, c);
-              const __nv_bfloat162 bv = __floats2bfloat162_rn(a, c);
-              w[k] = *reinterpret_cast<const uint32_t*>(&bv);
-            }
-            if (aligned) {
-              reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                dst[8 * i + 2 * k] = (uint16_t)w[k];
-                dst[8 * i + 2 * k + 1] = (uint16_t)(w[k] >> 16);
-              }
-            }
-          }
         }
       }
     }
+    regs_down<kRegCommon>();
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ decode K and V
     regs_down<kRegDecode>();
@@ -437,6 +427,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     uint32_t kw[4][NW], vw[4][NW], sc = 0u;
     int page = -1, page_next = -1;
     bool there = false;
+    const uint32_t page_bytes = (uint32_t)p.L.nkv * p.L.block;
+    const uint8_t* base = p.pages + (size_t)h * p.L.block;
+    const int k_lane = (lane & 7) * (D / 2) + (lane >> 3) * (D / 8);
+    int v_lane[NW];  // of pair k (d = 64: of the lane half's two); the chunks' turn repeats every four pairs
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int pair = D == 128 ? k : 2 * (lane >> 4) + k, jj = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+      v_lane[k] = pair * D + ((lane & 7) ^ paged_v_turn<D>(pair)) * (D / 8) + 4 * jj;
+    }
     auto page_of = [&](int j) {  // raw entry; positions behind the end: -1
       const int pos = kKeys * j + 32 * w4 + lane;
       return pos < kv ? __ldg(table + (pos >> p.L.pshift)) : -1;
@@ -448,38 +447,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       there = pos < kv && (uint32_t)page < (uint32_t)p.L.npages;
       if (pos < kv && !there) set_status(p.status, FT_DEV_RANGE);
       if (!there) page = -1;
-      sc = there ? ld_stream_u32(p.pages + paged_block(p.L, page, h) + p.L.soff + 4 * (pos & (p.L.psize - 1))) : 0u;
+      sc = there ? ld_stream_u32(base + (uint64_t)(uint32_t)page * page_bytes + p.L.soff + 4 * (pos & (p.L.psize - 1))) : 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, 8 * i), pin = (kKeys * j + 32 * w4 + 8 * i) & (p.L.psize - 1);
+      for (int q = 0; q < 2; ++q) {  // 16 positions, on one page
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * j + 32 * w4 + 16 * q) & (p.L.psize - 1);
+        const uint8_t* src = base + (uint64_t)(uint32_t)pg * page_bytes + pin * (D / 2) + k_lane;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) kw[i][k] = 0u;
-        if (pg >= 0) {
-          const uint8_t* src = p.pages + paged_block(p.L, pg, h) + (pin + (lane & 7)) * (D / 2) + (lane >> 3) * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 q = ld_stream_v4(src);
-            kw[i][0] = q.x, kw[i][1] = q.y, kw[i][2] = q.z, kw[i][3] = q.w;
-          } else {
-            const uint2 q = ld_stream_v2(src);
-            kw[i][0] = q.x, kw[i][1] = q.y;
+        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+#pragma unroll
+          for (int k = 0; k < NW; ++k) kw[i][k] = 0u;
+          if (pg >= 0) {
+            if constexpr (D == 128) {
+              const uint4 x = ld_stream_v4(src + (i & 1) * 8 * (D / 2));
+              kw[i][0] = x.x, kw[i][1] = x.y, kw[i][2] = x.z, kw[i][3] = x.w;
+            } else {
+              const uint2 x = ld_stream_v2(src + (i & 1) * 8 * (D / 2));
+              kw[i][0] = x.x, kw[i][1] = x.y;
+            }
           }
         }
       }
     };
     auto load_v = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, 8 * i), pin = (kKeys * j + 32 * w4 + 8 * i) & (p.L.psize - 1);
+      for (int q = 0; q < 2; ++q) {
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * j + 32 * w4 + 16 * q) & (p.L.psize - 1);
+        const uint8_t* src = base + (uint64_t)(uint32_t)pg * page_bytes + p.L.voff + pin * (D / 2);
 #pragma unroll
-        for (int k = 0; k < NW; ++k) vw[i][k] = 0u;
-        if (pg >= 0) {
-          const uint8_t* blk = p.pages + paged_block(p.L, pg, h) + p.L.voff;
+        for (int i = 2 * q; i < 2 * q + 2; ++i)
 #pragma unroll
           for (int k = 0; k < NW; ++k) {
-            const int pair = (pin >> 1) + (D == 128 ? k : 2 * (lane >> 4) + k), jj = D == 128 ? lane >> 3 : (lane >> 3) & 1;
-            vw[i][k] = ld_stream_u32(blk + pair * D + ((lane & 7) ^ paged_v_turn<D>(pair)) * (D / 8) + 4 * jj);
+            vw[i][k] = 0u;
+            if (pg >= 0) vw[i][k] = ld_stream_u32(src + (i & 1) * 4 * D + v_lane[k]);
           }
-        }
       }
       page_next = page_of(j + 1);
     };
@@ -570,62 +570,105 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
   } else {
     regs_down<kRegIssue>();
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
       // ---------------------------------------------------------- tensor-core issue
       constexpr uint32_t id_qk = idesc_f16(128, kKeys), id_pv = idesc_f16(128, D);
+      const uint32_t lead = lane == 0 ? 1u : 0u, tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = desc_lo(sm32 + C::kOffQ), k_lo = desc_lo(sm32 + C::kOffK), v_lo = desc_lo(sm32 + C::kOffV);
       auto qk = [&](int t, int j) {
-        const uint32_t qa = sm32 + C::kOffQ + t * C::kQ, ka = sm32 + C::kOffK + (j & 1) * C::kK;
+        const uint32_t qa = q_lo + t * (C::kQ >> 4), ka = k_lo + (j & 1) * (C::kK >> 4), d = tm + 128 * t;
+        mma_ss<false>(d, qa, ka, id_qk, lead);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks / 4) * (128 * 128) + 32 * (ks % 4);
-          mma_ss(tmem + 128 * t, desc_sw128(qa + o), desc_sw128(ka + o), id_qk, ks > 0 ? 1u : 0u);
+        for (int ks = 1; ks < D / 16; ++ks) {
+          const uint32_t o = ((ks / 4) * (128 * 128) + 32 * (ks % 4)) >> 4;
+          mma_ss<true>(d, qa + o, ka + o, id_qk, lead);
         }
-        commit(s_full + 8 * t);
+        commit(s_full + 8 * t, lead);
       };
       auto pv = [&](int t, int j) {
-        const uint32_t va = sm32 + C::kOffV + (j & 1) * C::kV;
+        const uint32_t va = v_lo + (j & 1) * (C::kV >> 4), d = tm + C::kColO + D * t, pa = tm + 128 * t;
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts(tmem + C::kColO + D * t, tmem + 128 * t + 8 * ks, desc_sw128(va + (ks / 4) * (D * 128) + 32 * (ks % 4)), id_pv,
-                 j > 0 || ks > 0 ? 1u : 0u);
-        commit(o_full + 8 * t);
+          mma_ts(d, pa + 8 * ks, va + (((ks / 4) * (D * 128) + 32 * (ks % 4)) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
+        commit(o_full + 8 * t, lead);
       };
       if (nkt > 0) {
-        ok = mbar_wait(k_full, 0);
+        ok = all_wait(k_full, 0);
         for (int t = 0; ok && t < ntile; ++t) {
-          ok = mbar_wait(q_full + 8 * t, 0);
-          fence_after();
-          if (ok) qk(t, 0);
+          qk(t, 0);
         }
-        if (ok) commit(k_empty);
+        if (ok) commit(k_empty, lead);
       }
       for (int j = 0; ok && j < nkt; ++j) {
         const bool more = j + 1 < nkt;
         for (int t = 0; ok && t < ntile; ++t) {
-          ok = (t > 0 || mbar_wait(v_full + 8 * (j & 1), (j >> 1) & 1)) && mbar_wait(p_full + 8 * t, j & 1);
+          ok = (t > 0 || all_wait(v_full + 8 * (j & 1), (j >> 1) & 1)) && all_wait(p_full + 8 * t, j & 1);
           if (!ok) break;
           fence_after();
           pv(t, j);
-          if (t == ntile - 1) commit(v_empty + 8 * (j & 1));
+          if (t == ntile - 1) commit(v_empty + 8 * (j & 1), lead);
           if (more) {
-            if (t == 0) ok = mbar_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1);
+            if (t == 0) ok = all_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1);
             if (!ok) break;
             fence_after();
             qk(t, j + 1);
-            if (t == ntile - 1) commit(k_empty + 8 * ((j + 1) & 1));
+            if (t == ntile - 1) commit(k_empty + 8 * ((j + 1) & 1), lead);
           }
         }
       }
       // tensor memory is freed only when nothing issued here is in flight
-      commit(drained);
-      if (!mbar_wait(drained, 0)) ok = false;
+      commit(drained, lead);
+      if (!all_wait(drained, 0)) ok = false;
     }
-    __syncwarp();
   }
   if (!ok) set_status(p.status, FT_DEV_TIMEOUT);
   fence_before();
-  __syncthreads();
+  const bool all_ok = __syncthreads_and(ok);
   fence_after();
+  // Only now may the others take registers again: the softmax warps have given theirs back before
+  // the barrier.  (Taken earlier, by warps that are through before a softmax warp has come to
+  // take its share, they would leave that warp waiting for registers that nobody returns.)
+  if (warp >= 8) regs_up<kRegCommon>();
+  // ---- the rotation undone and the rows stored, by all warps
+  if (all_ok) {
+    const f32x2 norm2(p.norm, p.norm);
+#pragma unroll 1
+    for (int it = 0; it < kRowIt; ++it) {
+      const int rr = row_at(it);
+      f32x2 v[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 q = *out_at(rr, 8 * lj + i);
+        v[2 * i] = f32x2(q.x, q.y);
+        v[2 * i + 1] = f32x2(q.z, q.w);
+      }
+      paged_fwht<D>(v, p.hb);
+      if (rr >= nrow) continue;
+      const int2 at = row_ptr(rr);
+      uint16_t* dst = p.o + at.x * p.o_stride + at.y;
+      const bool aligned = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a, c;
+          mul2(v[4 * i + k], norm2).get(a, c);
+          const __nv_bfloat162 bv = __floats2bfloat162_rn(a, c);
+          w[k] = *reinterpret_cast<const uint32_t*>(&bv);
+        }
+        if (aligned) {
+          reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            dst[8 * i + 2 * k] = (uint16_t)w[k];
+            dst[8 * i + 2 * k + 1] = (uint16_t)(w[k] >> 16);
+          }
+        }
+      }
+    }
+  }
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
@@ -641,7 +684,7 @@ static cudaError_t launch_tiles_d(const AttnPagedParams& p, cudaStream_t st) {
     // the roles' register shares add up to 128 a thread: a build with fewer would wait for them forever
     cudaFuncAttributes fa = {};
     if (cudaFuncGetAttributes(&fa, attn_tiles_kernel<D>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
-    if (fa.numRegs * 4 < 2 * kRegSoftmax + kRegDecode + kRegIssue) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs < kRegCommon) return cudaErrorInvalidConfiguration;
     allowed[dev] = 1;
   }
   // an upper bound of the 256-row blocks of all requests
