@@ -389,11 +389,10 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
 }
 
 // Joins the partials of the (request, head) pairs that several CTAs shared, one warp
-// per row, in the order of the shares; eight partials' loads in flight.
+// per row, in the order of the shares.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnPagedParams p, const SplitWs ws, int ctas) {
-  constexpr int PW = D + 4, CH = D / 32, kBatch = 8;  // channels CH lane .. + CH - 1 of each lane
-  const int lane = threadIdx.x & 31, rb = 2 * NT;
+  constexpr int PW = D + 4, rb = 2 * NT;
   const int r = 4 * (blockIdx.x % rb) + (threadIdx.x >> 5), bh = blockIdx.x / rb, h = bh % p.L.nkv, b = bh / p.L.nkv;
   const int row0 = p.cu[b], n = p.cu[b + 1] - row0;  // (not the few-rows kernel's: no need to wait)
   griddep_wait();
@@ -402,62 +401,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnPagedParams p,
   const int nv = (next - first) / p.L.nkv, v0 = first + h * nv;
   const int c0 = share_of(units, ctas, v0 + kSegUnits), c1 = share_of(units, ctas, v0 + nv - 1);
   if (c0 == c1) return;
+  const int tok = r / p.G, hh = r - tok * p.G;
   // the first share's partial in its slot 1, the others' in their slot 0
   const float* base = ws.part + (size_t)r * PW;
-  auto row = [&](int c) { return base + (size_t)(2 * c + (c == c0 ? 1 : 0)) * (8 * NT * PW); };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(row(c)));
-  M = warp_max(M);
-  float lt = 0.0f, o[CH] = {};
-  for (int c = c0; c <= c1; c += kBatch) {
-    float2 ml[kBatch];
-    float x[kBatch][CH];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (c + i > c1) continue;
-      const float* q = row(c + i);
-      ml[i] = __ldcg(reinterpret_cast<const float2*>(q));
-      if constexpr (D == 128) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(q + 4) + lane);
-        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(q + 4) + lane);
-        x[i][0] = f.x, x[i][1] = f.y;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (c + i > c1) continue;
-      const float f = ml[i].x == M ? 1.0f : ex2(ml[i].x - M);
-      lt = fmaf(f, ml[i].y, lt);
-#pragma unroll
-      for (int k = 0; k < CH; ++k) o[k] = fmaf(f, x[i][k], o[k]);
-    }
-  }
-  const float inv = lt == 0.0f ? 0.0f : kOUp / lt;
-  // the rotation of neighbouring channels, strides 1 (and 2) in the lane, the others across lanes
-#pragma unroll
-  for (int k = 0; k < CH; ++k) o[k] *= inv;
-#pragma unroll
-  for (int s = 1; s < CH; s <<= 1) {
-    if (s >= p.hb) break;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      if (k & s) continue;
-      const float a = o[k], c = o[k + s];
-      o[k] = a + c;
-      o[k + s] = a - c;
-    }
-  }
-  for (int s = 1; CH * s < p.hb; s <<= 1) {
-    const float sign = (lane & s) ? -1.0f : 1.0f;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) o[k] = fmaf(sign, o[k], __shfl_xor_sync(0xffffffffu, o[k], s));
-  }
-  const int tok = r / p.G, hh = r - tok * p.G;
-  uint16_t* dst = p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D + CH * lane;
-#pragma unroll
-  for (int k = 0; k < CH; ++k) dst[k] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k] * p.norm));
+  join_row<D>(p, c1 - c0 + 1, [&](int i) { return base + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * (8 * NT * PW); }, kOUp,
+              p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D);
 }
 
 // CTAs of the few-rows kernel: every SM filled (its occupancy by registers and ring).
@@ -511,7 +459,7 @@ extern "C" {
 size_t ft_attn_paged_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) {
   if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > ft::kApMaxB || total_q < 0 || max_q < 1) return 0;
   const int nt = ft::few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
-  if (nt == 0) return 16;
+  if (nt == 0) return ft::attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   return ft::align_up((size_t)(B + 1) * 4, 256) + (size_t)ft::few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
 }
 
@@ -564,7 +512,7 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
                     : ft::launch_few<64, 4>(p, workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
   }
-  return ft::launch_attn_tiles(p, c->head_dim, (cudaStream_t)stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  return ft::launch_attn_tiles(p, c->head_dim, workspace, (cudaStream_t)stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -65,7 +65,67 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Requests with many rows (ft_attn_tiles.cu).
-cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, cudaStream_t st);
+// Joins n partials (max, sum, 2 unused, accumulator) of one row and stores it, a warp per row,
+// eight partials' loads in flight; row(i) is partial i, `up` the accumulators' factor.
+template <int D, typename Row>
+__device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row row, float up, uint16_t* dst) {
+  constexpr int CH = D / 32, kBatch = 8;  // channels CH lane .. + CH - 1 of each lane
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(row(i)));
+  M = warp_max(M);
+  float lt = 0.0f, o[CH] = {};
+  for (int c = 0; c < n; c += kBatch) {
+    float2 ml[kBatch];
+    float x[kBatch][CH];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (c + i >= n) continue;
+      const float* q = row(c + i);
+      ml[i] = __ldcg(reinterpret_cast<const float2*>(q));
+      if constexpr (D == 128) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(q + 4) + lane);
+        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(q + 4) + lane);
+        x[i][0] = f.x, x[i][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (c + i >= n) continue;
+      const float f = ml[i].x == M ? 1.0f : ex2(ml[i].x - M);
+      lt = fmaf(f, ml[i].y, lt);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) o[k] = fmaf(f, x[i][k], o[k]);
+    }
+  }
+  const float inv = lt == 0.0f ? 0.0f : up / lt;  // a row that sees nothing: zeros
+  // the rotation of neighbouring channels, strides 1 (and 2) in the lane, the others across lanes
+#pragma unroll
+  for (int k = 0; k < CH; ++k) o[k] *= inv;
+#pragma unroll
+  for (int s = 1; s < CH; s <<= 1) {
+    if (s >= p.hb) break;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      if (k & s) continue;
+      const float a = o[k], c = o[k + s];
+      o[k] = a + c;
+      o[k + s] = a - c;
+    }
+  }
+  for (int s = 1; CH * s < p.hb; s <<= 1) {
+    const float sign = (lane & s) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) o[k] = fmaf(sign, o[k], __shfl_xor_sync(0xffffffffu, o[k], s));
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) dst[CH * lane + k] = __bfloat16_as_ushort(__float2bfloat16_rn(o[k] * p.norm));
+}
+
+// Requests with many rows (ft_attn_tiles.cu); a workspace of attn_tiles_ws bytes.
+size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q);
+cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
 
 }  // namespace ft

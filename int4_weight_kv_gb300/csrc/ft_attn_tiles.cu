@@ -1,8 +1,9 @@
 // Attention over the paged 4-bit cache for requests with many rows (prompts and chunks
 // of prompts), on the fifth-generation tensor cores.
 //
-// A CTA owns up to 256 rows (tokens x heads of a group, two tiles of M = 128) of one
-// request and KV head and walks the visible positions in tiles of 128:
+// A CTA owns up to 256 rows (tokens x heads of a group, two tiles of M = 128; one tile where
+// that leaves SMs without work) of one request and KV head and walks the visible positions,
+// or one of several equal parts of them where rows are few, in tiles of 128:
 //   S = Q K^T   A = Q from shared memory, B = K codes from shared memory
 //   O += P V    A = P from tensor memory (over S's columns), B = V from shared memory
 // with FP16 operands and FP32 accumulators in tensor memory (S 2 x 128 columns, O 2 x d
@@ -33,7 +34,7 @@ namespace ft {
 namespace tiles {
 
 constexpr int kThreads = 512, kRows = 256, kKeys = 128;
-constexpr int kMmaWarp = 12;
+constexpr int kMmaWarp = 12, kPartTiles = 4;
 constexpr float kOScale = 512.0f;  // the operands hold V's values x 2^-9
 constexpr int kScaleRing = 4;  // per tile and group of 32 positions: kf, f, 2^-f, mask of the positions that exist
 // Registers of a thread by role (softmax twice, decode, issue): the sum over the four
@@ -141,8 +142,17 @@ __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity) {
 
 using namespace tiles;
 
+// How the rows and positions are shared out.  With parts > 1 each CTA leaves (max, sum,
+// accumulator) partials, [block][head][part][128][D + 4], and meta[block] = (request, first row,
+// rows, parts taken: at least kPartTiles tiles each) for the kernel that joins them.
+struct TilesSplit {
+  int rows, parts;  // rows of a CTA (256; 128 with several parts), parts of the positions
+  int4* meta;
+  float* part;
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPagedParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPagedParams p, const TilesSplit sp) {
   using C = Cfg<D>;
   constexpr int NJ = D / 32;
   extern __shared__ uint8_t tiles_smem[];
@@ -154,13 +164,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- which rows: block i of all requests' 256-row blocks, the last ones (which see most) first
-  const int h = blockIdx.x % p.L.nkv, want = blockIdx.x / p.L.nkv;
+  griddep_launch();  // the joining kernel waits for this one's end in any case
+  // ---- which rows: block i of all requests' blocks of rows, the last ones (which see most) first
+  const int h = blockIdx.x % p.L.nkv, part = (blockIdx.x / p.L.nkv) % sp.parts, want = blockIdx.x / (p.L.nkv * sp.parts);
   {
     auto blocks = [&](int b, int32_t* status) {
       int row0, n, kv;
       if (!attn_request(p, b, status, row0, n, kv)) return 0;
-      return (int)(((int64_t)n * p.G + kRows - 1) / kRows);
+      return (int)(((int64_t)n * p.G + sp.rows - 1) / sp.rows);
     };
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int sum = 0;
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         const int nb = blocks(b, nullptr);
         if (i < at + nb) {
           find[0] = b;
-          find[1] = (i - at) * kRows;
+          find[1] = (i - at) * sp.rows;
           break;
         }
         at += nb;
@@ -194,14 +205,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     __syncthreads();
   }
   const int b = find[0], r0 = find[1];
-  if (r0 < 0) return;
+  if (r0 < 0) {
+    if (sp.parts > 1 && h == 0 && part == 0 && tid == 0) sp.meta[want] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int row0 = p.cu[b], n = p.cu[b + 1] - row0;
   int kv = p.kv_len[b];
   if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) kv = 0;
-  const int nrow = min((int)((int64_t)n * p.G - r0), kRows);  // rows of this CTA
+  const int nrow = (int)min((int64_t)n * p.G - r0, (int64_t)sp.rows);  // rows of this CTA
   const int ntile = nrow > 128 ? 2 : 1;
   const int last = kv - n + (r0 + nrow - 1) / p.G;               // last visible position of any row
-  const int nkt = last >= 0 ? last / kKeys + 1 : 0;
+  const int all_kt = last >= 0 ? last / kKeys + 1 : 0;
+  const int parts = min(sp.parts, max(1, (all_kt + kPartTiles - 1) / kPartTiles)), per_part = (all_kt + parts - 1) / parts;
+  const int j0 = part * per_part, nkt = max(0, min(all_kt - j0, per_part));  // this CTA's tiles: j0, j0 + 1, ...
+  if (sp.parts > 1 && h == 0 && part == 0 && tid == 0) sp.meta[want] = make_int4(b, r0, nrow, parts);
+  if (part >= parts) return;
   const int* table = p.table + (size_t)b * p.table_stride;
 
   const uint32_t bar = sm32 + C::kOffBar;
@@ -327,11 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         const float kf[4] = {kf4.x, kf4.y, kf4.z, kf4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w}, rf[4] = {rf4.x, rf4.y, rf4.z, rf4.w};
         wait_ld();
         // a tile that some row of the warp sees in part, or with positions on a page outside the pool
-        if (kKeys * j + kKeys - 1 > lim_all || (mask4.x & mask4.y & mask4.z & mask4.w) != 0xFFFFFFFFu) {
+        if (kKeys * (j0 + j) + kKeys - 1 > lim_all || (mask4.x & mask4.y & mask4.z & mask4.w) != 0xFFFFFFFFu) {
           const uint32_t mask[4] = {mask4.x, mask4.y, mask4.z, mask4.w};
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
-            s[c] = kKeys * j + c <= lim && ((mask[c / 32] >> (c % 32)) & 1u) ? s[c] : 0xFF800000u;
+            s[c] = kKeys * (j0 + j) + c <= lim && ((mask[c / 32] >> (c % 32)) & 1u) ? s[c] : 0xFF800000u;
         }
         float mx = -INFINITY;
 #pragma unroll
@@ -397,7 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       if (ok && nkt > 0 && !all_wait(o_full + 8 * t, (nkt - 1) & 1)) ok = false;
       if (ok) {
         fence_after();
-        const float inv = l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
+        const float inv = parts > 1 ? 1.0f : l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
+        float* partial = nullptr;
+        if (parts > 1) {
+          partial = sp.part + ((((size_t)want * p.L.nkv + h) * sp.parts + part) * 128 + row) * (D + 4);
+          partial[0] = m, partial[1] = l;
+        }
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -409,9 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *out_at(128 * t + row, (c + i) / 4) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+          for (int i = 0; i < 32; i += 4) {
+            float4* dst = partial ? reinterpret_cast<float4*>(partial + 4 + c + i) : out_at(128 * t + row, (c + i) / 4);
+            *dst = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                               __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+          }
         }
       }
     }
@@ -437,20 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       v_lane[k] = pair * D + ((lane & 7) ^ paged_v_turn<D>(pair)) * (D / 8) + 4 * jj;
     }
     auto page_of = [&](int j) {  // raw entry; positions behind the end: -1
-      const int pos = kKeys * j + 32 * w4 + lane;
+      const int pos = kKeys * (j0 + j) + 32 * w4 + lane;
       return pos < kv ? __ldg(table + (pos >> p.L.pshift)) : -1;
     };
     // bytes of tile j on their way into registers; the pages of tile j + 1 are looked up with them
     auto load_k = [&](int j) {
       page = page_next;
-      const int pos = kKeys * j + 32 * w4 + lane;
+      const int pos = kKeys * (j0 + j) + 32 * w4 + lane;
       there = pos < kv && (uint32_t)page < (uint32_t)p.L.npages;
       if (pos < kv && !there) set_status(p.status, FT_DEV_RANGE);
       if (!there) page = -1;
       sc = there ? ld_stream_u32(base + (uint64_t)(uint32_t)page * page_bytes + p.L.soff + 4 * (pos & (p.L.psize - 1))) : 0u;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {  // 16 positions, on one page
-        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * j + 32 * w4 + 16 * q) & (p.L.psize - 1);
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * (j0 + j) + 32 * w4 + 16 * q) & (p.L.psize - 1);
         const uint8_t* src = base + (uint64_t)(uint32_t)pg * page_bytes + pin * (D / 2) + k_lane;
 #pragma unroll
         for (int i = 2 * q; i < 2 * q + 2; ++i) {
@@ -471,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     auto load_v = [&](int j) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * j + 32 * w4 + 16 * q) & (p.L.psize - 1);
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * q), pin = (kKeys * (j0 + j) + 32 * w4 + 16 * q) & (p.L.psize - 1);
         const uint8_t* src = base + (uint64_t)(uint32_t)pg * page_bytes + p.L.voff + pin * (D / 2);
 #pragma unroll
         for (int i = 2 * q; i < 2 * q + 2; ++i)
@@ -630,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   // take its share, they would leave that warp waiting for registers that nobody returns.)
   if (warp >= 8) regs_up<kRegCommon>();
   // ---- the rotation undone and the rows stored, by all warps
-  if (all_ok) {
+  if (all_ok && parts == 1) {
     const f32x2 norm2(p.norm, p.norm);
 #pragma unroll 1
     for (int it = 0; it < kRowIt; ++it) {
@@ -672,8 +697,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
+// Joins the parts of each row, a warp per row.
 template <int D>
-static cudaError_t launch_tiles_d(const AttnPagedParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(128) attn_tiles_join_kernel(const AttnPagedParams p, const TilesSplit sp) {
+  griddep_wait();
+  const int h = blockIdx.y, r = 4 * (blockIdx.x % 32) + (threadIdx.x >> 5), block = blockIdx.x / 32;
+  const int4 meta = __ldcg(sp.meta + block);
+  if (r >= meta.z || meta.w == 1) return;
+  const int rg = meta.y + r, tok = rg / p.G, hh = rg - tok * p.G;
+  const float* base = sp.part + (((size_t)block * p.L.nkv + h) * sp.parts * 128 + r) * (D + 4);
+  join_row<D>(p, meta.w, [&](int i) { return base + (size_t)i * 128 * (D + 4); }, kOScale,
+              p.o + (p.cu[meta.x] + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D);
+}
+
+// Rows of a CTA and parts of the positions, from what the host knows (an upper bound of the
+// blocks of all requests).  128 rows where all blocks then still run at once, and as many
+// parts as fill the SMs (up to 16, counting half a block for the requests' remainders).  Measured,
+// 256 rows and one part against this rule (us): 256 tokens over 32768 positions (8B shape) 505 / 229,
+// 64 of each of four requests over 8192 139 / 73, 2000 over 3000 with 4 heads 63 / 38; 5 requests of
+// 777 (8 heads, d 64) run at once only with 256 rows, 21.5 (128 rows: 32.6).
+static void tiles_shape(int nkv, int G, int B, int total_q, int& rows, int& parts, int64_t& blocks) {
+  int sms = ft_host::num_sms();
+  if (sms <= 0) sms = 152;
+  const int64_t all = (int64_t)total_q * G, some = std::min(B, total_q);
+  rows = kRows, parts = 1;
+  blocks = all / kRows + some;
+  if ((all / 128 + some) * nkv > sms) return;
+  rows = 128;
+  blocks = all / 128 + some;
+  const int64_t likely = std::max<int64_t>(1, (2 * (all / 128) + some) * nkv / 2);
+  parts = (int)std::min<int64_t>(16, std::max<int64_t>(1, (sms + likely / 2) / likely));
+}
+
+size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q) {
+  int rows, parts;
+  int64_t blocks;
+  tiles_shape(nkv, G, B, std::max(total_q, 1), rows, parts, blocks);
+  if (parts == 1) return 16;
+  return align_up((size_t)blocks * 16, 256) + (size_t)blocks * nkv * parts * 128 * (head_dim + 4) * 4;
+}
+
+template <int D>
+static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cudaStream_t st) {
   static int allowed[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -687,15 +752,29 @@ static cudaError_t launch_tiles_d(const AttnPagedParams& p, cudaStream_t st) {
     if (fa.numRegs < kRegCommon) return cudaErrorInvalidConfiguration;
     allowed[dev] = 1;
   }
-  // an upper bound of the 256-row blocks of all requests
-  const int64_t blocks = ((int64_t)p.total_q * p.G) / kRows + std::min(p.B, p.total_q);
+  TilesSplit sp = {};
+  int64_t blocks;
+  tiles_shape(p.L.nkv, p.G, p.B, p.total_q, sp.rows, sp.parts, blocks);
   if (blocks * p.L.nkv > INT32_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D><<<(unsigned)(blocks * p.L.nkv), kThreads, Cfg<D>::kSmem, st>>>(p);
-  return cudaGetLastError();
+  sp.meta = static_cast<int4*>(workspace);
+  sp.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up((size_t)blocks * 16, 256));
+  attn_tiles_kernel<D><<<(unsigned)(blocks * p.L.nkv * sp.parts), kThreads, Cfg<D>::kSmem, st>>>(p, sp);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || sp.parts == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks * 32, p.L.nkv);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ft_host::pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_tiles_join_kernel<D>, p, sp);
 }
 
-cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, cudaStream_t st) {
-  return head_dim == 128 ? launch_tiles_d<128>(p, st) : launch_tiles_d<64>(p, st);
+cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st) {
+  return head_dim == 128 ? launch_tiles_d<128>(p, workspace, st) : launch_tiles_d<64>(p, workspace, st);
 }
 
 }  // namespace ft
