@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   const uint32_t raw = smem_u32(tiles_smem);
   uint8_t* sm = tiles_smem + ((1024 - (raw & 1023)) & 1023);
   const uint32_t sm32 = smem_u32(sm);
-  __shared__ int find[3];       // request, first row of the CTA's rows (-1: no work), and the blocks of all requests
+  __shared__ int find[5];       // request, first row of the CTA's rows (-1: no work), the request's first row, rows and positions
   __shared__ int warp_tot[16];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -168,50 +168,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   // ---- which rows: block i of all requests' blocks of rows, the last ones (which see most) first
   const int h = blockIdx.x % p.L.nkv, part = (blockIdx.x / p.L.nkv) % sp.parts, want = blockIdx.x / (p.L.nkv * sp.parts);
   {
-    auto blocks = [&](int b, int32_t* status) {
-      int row0, n, kv;
+    auto blocks = [&](int b, int32_t* status, int& row0, int& n, int& kv) {
       if (!attn_request(p, b, status, row0, n, kv)) return 0;
       return (int)(((int64_t)n * p.G + sp.rows - 1) / sp.rows);
     };
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += blocks(b, blockIdx.x == 0 ? p.status : nullptr);
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) warp_tot[warp] = inc;
+    int32_t* status = blockIdx.x == 0 ? p.status : nullptr;
     if (tid == 0) find[1] = -1;
     __syncthreads();
-    int at = inc - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += warp_tot[w];
-      total += warp_tot[w];
-    }
-    const int i = total - 1 - want;
-    if (i >= at && i < at + sum) {
-      for (int b = b0; b < b1; ++b) {
-        const int nb = blocks(b, nullptr);
-        if (i < at + nb) {
-          find[0] = b;
-          find[1] = (i - at) * sp.rows;
-          break;
+    if (p.B <= 32) {  // a request per lane of the first warp
+      if (warp == 0) {
+        int row0 = 0, n = 0, kv = 0;
+        const int nb = lane < p.B ? blocks(lane, status, row0, n, kv) : 0;
+        int inc = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
         }
-        at += nb;
+        const int i = __shfl_sync(0xffffffffu, inc, 31) - 1 - want;
+        if (i >= inc - nb && i < inc) {
+          find[0] = lane, find[2] = row0, find[3] = n, find[4] = kv;
+          find[1] = (i - (inc - nb)) * sp.rows;
+        }
+      }
+    } else {
+      const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+      int sum = 0, row0, n, kv;
+      for (int b = b0; b < b1; ++b) sum += blocks(b, status, row0, n, kv);
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) warp_tot[warp] = inc;
+      __syncthreads();
+      int at = inc - sum, total = 0;
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) at += warp_tot[w];
+        total += warp_tot[w];
+      }
+      const int i = total - 1 - want;
+      if (i >= at && i < at + sum) {
+        for (int b = b0; b < b1; ++b) {
+          const int nb = blocks(b, nullptr, row0, n, kv);
+          if (i < at + nb) {
+            find[0] = b, find[2] = row0, find[3] = n, find[4] = kv;
+            find[1] = (i - at) * sp.rows;
+            break;
+          }
+          at += nb;
+        }
       }
     }
     __syncthreads();
   }
-  const int b = find[0], r0 = find[1];
+  const int b = find[0], r0 = find[1], row0 = find[2], n = find[3], kv = find[4];
   if (r0 < 0) {
     if (sp.parts > 1 && h == 0 && part == 0 && tid == 0) sp.meta[want] = make_int4(0, 0, 0, 0);
     return;
   }
-  const int row0 = p.cu[b], n = p.cu[b + 1] - row0;
-  int kv = p.kv_len[b];
-  if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) kv = 0;
   const int nrow = (int)min((int64_t)n * p.G - r0, (int64_t)sp.rows);  // rows of this CTA
   const int ntile = nrow > 128 ? 2 : 1;
   const int last = kv - n + (r0 + nrow - 1) / p.G;               // last visible position of any row
@@ -244,53 +261,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   // ---- the rotated query rows as the FP16 operand, channels in the order of the cache's words: all
-  // warps, D / 32 lanes a row with 32 channels each, the next rows' loads in flight
-  constexpr int LV = D / 32, RW = 32 / LV;     // lanes of a row, rows of a warp at once
-  constexpr int kRowIt = kRows / (RW * (kThreads / 32));  // times that all warps' rows cover the CTA's
-  const int lj = lane % LV;
-  auto row_at = [&](int it) { return it * (kRows / kRowIt) + warp * RW + lane / LV; };
-  auto row_ptr = [&](int rr) {  // element offset of row rr (token, head) beside the row stride
+  // warps, D / 32 lanes a row with 32 channels each (8 lanes a row of 16 channels cost less code, which
+  // runs cold, but twice the shuffles: 11.8 thousand cycles against 6.3 for 256 rows)
+  constexpr int LV = D / 32, RW = 32 / LV, kRowStep = RW * (kThreads / 32);  // lanes of a row, rows of a warp, of all warps
+  const int lj = lane % LV, rr0 = warp * RW + lane / LV;
+  auto row_ptr = [&](int rr) {  // row of q and o, and the element in it, of row rr (token, head)
     const int rg = r0 + rr, tok = rg / p.G;
     return make_int2(row0 + tok, (h * p.G + rg - tok * p.G) * D + 32 * lj);
   };
   if (nkt > 0) {
-    uint4 raw[kRowIt][4];
-#pragma unroll
-    for (int it = 0; it < kRowIt; ++it) {
-      const int rr = row_at(it);
+    const float f0 = p.qscale * p.norm;
+    const f32x2 f2(f0, f0);
+    uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
+#pragma unroll 1
+    for (int rr = rr0; rr - lane / LV < 128 * ntile; rr += kRowStep) {  // (a warp's rows together)
+      f32x2 v[16];
       const int2 at = row_ptr(rr);
       const uint16_t* src = p.q + at.x * p.q_stride + at.y;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        raw[it][i] = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
         if (rr < nrow) {
           if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-            raw[it][i] = *(reinterpret_cast<const uint4*>(src) + i);
+            const uint4 q = *(reinterpret_cast<const uint4*>(src) + i);
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
           } else {
-            uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = (uint32_t)src[8 * i + 2 * k] | ((uint32_t)src[8 * i + 2 * k + 1] << 16);
-            raw[it][i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      }
-    }
-    const float f0 = p.qscale * p.norm;
-    const f32x2 f2(f0, f0);
-    uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
-#pragma unroll
-    for (int it = 0; it < kRowIt; ++it) {
-      const int rr = row_at(it);
-      f32x2 v[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {raw[it][i].x, raw[it][i].y, raw[it][i].z, raw[it][i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
       }
       paged_fwht<D>(v, p.hb);
-      uint8_t* qs = sm + C::kOffQ + rr * 128;
-      qs += (rr >= 128) ? C::kQ - 128 * 128 : 0;  // the second tile's operand
+      uint8_t* qs = sm + C::kOffQ + (rr >= 128 ? C::kQ - 128 * 128 : 0) + rr * 128;
 #pragma unroll
       for (int tig = 0; tig < 4; ++tig) {  // word (tig, lj): channels 2 tig + 8 e + {0, 1} of the lane's
         uint32_t o[4];
@@ -658,8 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   if (all_ok && parts == 1) {
     const f32x2 norm2(p.norm, p.norm);
 #pragma unroll 1
-    for (int it = 0; it < kRowIt; ++it) {
-      const int rr = row_at(it);
+    for (int rr = rr0; rr - lane / LV < nrow; rr += kRowStep) {
       f32x2 v[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
