@@ -31,7 +31,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 //   S = K q:     A = K codes (rows positions), B = q (columns the rows)
 //   O^T = V^T P: A = V codes (rows channels), B = P transposed in registers
 // Tiles come through a ring of kApStages per warp by 16-byte asynchronous copies.
-constexpr int kUnit = 16 * kApWarps, kSegUnits = 3;
+constexpr int kUnit = 16 * kApWarps, kSegUnits = 5;
 constexpr int kApStages = 4;
 constexpr int kApMaxB = 8192;
 
@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
   if (u == u_end) return;
   int b;
   {
-    int lo = 0, hi = p.B;  // the request that holds unit u: pref[lo] <= u < pref[lo + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pref[mid] <= u) lo = mid; else hi = mid;
+    // the last request whose prefix sum is <= u, by up to three steps of 32 candidates
+    b = 0;
+    for (int st = p.B > 1024 ? 1024 : p.B > 32 ? 32 : 1; st; st >>= 5) {
+      const int i = b + (lane + 1) * st;
+      b += st * __popc(__ballot_sync(0xffffffffu, i <= p.B && pref[i] <= u));
     }
-    b = lo;
   }
   uint8_t* ring = few_smem + warp * T::kRing;
 
@@ -133,6 +133,16 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     int kv = p.kv_len[b];
     if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) kv = 0;
     const int* table = p.table + (size_t)b * p.table_stride;
+    // the warp's query rows warp, warp + kApWarps, ...: on their way while the pages are looked up
+    constexpr int RPW = 8 * NT / kApWarps;
+    uint16_t raw[RPW][NPL];
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const int r = warp + i * kApWarps, tok = r / p.G, hh = r - tok * p.G;
+      const uint16_t* src = p.q + (row0 + tok) * p.q_stride + (int64_t)(h * p.G + hh) * D;
+#pragma unroll
+      for (int m = 0; m < NPL; ++m) raw[i][m] = r < nrow ? src[lane + 32 * m] : 0;
+    }
     // this warp's tiles: t0, t0 + kApWarps, ... below t1
     const int t0 = k0 * kApWarps + warp, t1 = min(k1 * kApWarps, (kv + 15) / 16);
 
@@ -142,10 +152,10 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     const uint32_t page_bytes = (uint32_t)p.L.nkv * p.L.block, ring0 = smem_u32(ring) + lane * 16;
     const uint8_t* lane_base = p.pages + (size_t)h * p.L.block + lane * 16;
     auto page_at = [&](int t) { return t < t1 ? __ldg(table + ((16 * t) >> p.L.pshift)) : 0; };
-    int page_ahead = page_at(t0);
-    auto load = [&](int t, int slot) {
-      const int page = page_ahead;
-      page_ahead = page_at(t + kApWarps);
+    int first_pages[kApStages];
+#pragma unroll
+    for (int i = 0; i < kApStages; ++i) first_pages[i] = page_at(t0 + i * kApWarps);
+    auto load_page = [&](int t, int slot, int page) {
       if (t < t1) {
         const uint32_t pin = (16 * t) & (p.L.psize - 1), d0 = ring0 + slot * T::kTile;
         if ((uint32_t)page < (uint32_t)p.L.npages) {
@@ -165,15 +175,21 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kApStages - 1; ++i) load(t0 + i * kApWarps, i);
+    for (int i = 0; i < kApStages - 1; ++i) load_page(t0 + i * kApWarps, i, first_pages[i]);
+    int page_ahead = first_pages[kApStages - 1];
+    auto load = [&](int t, int slot) {
+      const int page = page_ahead;
+      page_ahead = page_at(t + kApWarps);
+      load_page(t, slot, page);
+    };
 
     // the rotated query rows as the FP16 operand (channels c % 16 >= 8 divided by 16)
-    for (int r = warp; r < 8 * NT; r += kApWarps) {
-      float v[NPL];
-      const int tok = r / p.G, hh = r - tok * p.G;
-      const uint16_t* src = p.q + (row0 + tok) * p.q_stride + (int64_t)(h * p.G + hh) * D;
 #pragma unroll
-      for (int m = 0; m < NPL; ++m) v[m] = r < nrow ? bf16_bits_to_f32(src[lane + 32 * m]) : 0.0f;
+    for (int i = 0; i < RPW; ++i) {
+      const int r = warp + i * kApWarps;
+      float v[NPL];
+#pragma unroll
+      for (int m = 0; m < NPL; ++m) v[m] = bf16_bits_to_f32(raw[i][m]);
       warp_fwht<NPL>(v, p.hb);
       bool bad = false;
 #pragma unroll
