@@ -215,12 +215,13 @@ size_t ft_kv_pages_bytes(const ft_block_cfg *cfg, int n_pages, int page_size);
  *     cu_seqlens[b]); -1 for rows behind the last one.
  * kv_len may be ctx_len and free_head_out may be free_head (advanced in place);
  * no other arguments may overlap.  A request with a negative length, more
- * positions than its table row holds, or whose new pages end behind the free
- * list sets FT_DEV_CAPACITY and is not served: its rows get slot -1, its kv_len
- * is 0 and its table row is left alone (pages are counted in request order, also
- * those of requests that did not get them).  More rows than n_slots, a head
- * outside [0, n_free] or a page outside [0, n_pages) set FT_DEV_RANGE; such rows
- * are dropped (slot -1).  B <= 8192, else FT_ERR_UNSUPPORTED. */
+ * positions than its table row holds (or than 2^31 - 1), or whose new pages end
+ * behind the free list sets FT_DEV_CAPACITY and is not served: its rows get slot
+ * -1, its kv_len is 0 (also where that is ctx_len) and its table row is left alone
+ * (pages are counted in request order, also those of requests that did not get
+ * them).  More rows than n_slots, a head outside [0, n_free] or a page outside
+ * [0, n_pages) set FT_DEV_RANGE; such rows are dropped (slot -1).  B <= 8192, else
+ * FT_ERR_UNSUPPORTED. */
 int ft_kv_page_map(int page_size, int n_pages, const int32_t *ctx_len, const int32_t *new_len, int B,
                    int32_t *block_table, int table_stride, const int32_t *free_pages, int n_free,
                    const int32_t *free_head, int32_t *free_head_out, int32_t *cu_seqlens, int32_t *kv_len,
@@ -252,16 +253,20 @@ int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_page
  * inside a row, q post-RoPE; o may be q where the strides are equal.  A token at
  * a negative position (kv_len < n_b) sees nothing and gets zeros.  Rows behind
  * cu_seqlens[B] are left as they are.  max_q: an upper bound of n_b; it picks the
- * kernel and sizes the launch.  B <= 8192 and B n_kv table_stride page_size / 64 <
- * 2^31, else FT_ERR_UNSUPPORTED.
+ * kernel and sizes the launch.  B <= 8192, total_q n_q / n_kv < 2^31 and
+ * B n_kv (table_stride page_size / 64 + 6) < 2^31, else FT_ERR_UNSUPPORTED.
  * Arithmetic: q rounded to FP16 after the rotation (|q scale log2(e)| < 1023, else
  * FT_DEV_RANGE), codes exact, softmax weights rounded to FP16 below the products,
- * sums and statistics in FP32.  V scales below 2^-100 count as 2^-100.  Entries
- * behind a token's position may hold anything.  What a request's rows are does not
+ * sums and statistics in FP32.  V scales from 2^-100 to 2^60 are weighed against each
+ * other without loss (smaller ones count as 2^-100; an entry whose scale is 0 has no
+ * values, only a weight).  With more than 32 rows (tokens x heads of a group) K and V
+ * are decoded to FP16 in groups of 32 positions, and scales less than 2^-15 of their
+ * group's largest are rounded.  Entries behind a token's position may hold anything
+ * else; one whose scales are not finite spoils only the rows that see it.  What a request's rows are does not
  * depend on the other requests of the call, up to the order of FP32 sums.
  * Device conditions: cu_seqlens not ascending within [0, total_q], or n_b > max_q:
- * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative or
- * longer than table_stride pages: FT_DEV_CAPACITY, zeros; a page outside the pool:
+ * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative,
+ * longer than table_stride pages or above 2^31 - 257: FT_DEV_CAPACITY, zeros; a page outside the pool:
  * FT_DEV_RANGE, its positions count as masked.
  * The workspace (16-byte aligned) holds partial results during the call only; calls
  * that may run at the same time need one each. */
@@ -394,7 +399,7 @@ int ft_lm_head_bf16(const float *x, const float *gamma, const uint16_t *W, float
  * target of -1 means none: logprob 0, rank -1; any other outside [0, V) gives NaN
  * and -1 and sets FT_DEV_RANGE.  A row with a NaN or +infinity, or with nothing above
  * -infinity, gives NaN (ids and rank -1) and sets FT_DEV_RANGE.  All sums in FP32.
- * top_k <= min(32, V), else FT_ERR_UNSUPPORTED. */
+ * top_k <= min(32, V) and V <= 2^30, else FT_ERR_UNSUPPORTED. */
 int ft_logprobs(const void *logits, int dtype, int64_t row_stride, int N, int V, const int32_t *targets, int top_k,
                 float *logprob, float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
                 int32_t *dev_status, ft_stream stream);

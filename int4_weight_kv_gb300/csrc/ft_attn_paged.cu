@@ -130,8 +130,7 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     u += step;
     if (k0 == k1) continue;  // the share ends in what the segment costs beside its units
     const int row0 = p.cu[b], n = p.cu[b + 1] - row0, nrow = n * p.G;
-    int kv = p.kv_len[b];
-    if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) kv = 0;
+    const int kv = attn_length(p, b, nullptr);
     const int* table = p.table + (size_t)b * p.table_stride;
     // the warp's query rows warp, warp + kApWarps, ...: on their way while the pages are looked up
     constexpr int RPW = 8 * NT / kApWarps;
@@ -275,8 +274,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
         }
       }
       const float ks0 = __uint_as_float(sc0 << 16) * kKsUp, ks1 = __uint_as_float(sc1 << 16) * kKsUp;
-      const float vs0 = fmaxf(__uint_as_float(sc0 & 0xFFFF0000u), kMinScale);
-      const float vs1 = fmaxf(__uint_as_float(sc1 & 0xFFFF0000u), kMinScale);
+      const float v0 = __uint_as_float(sc0 & 0xFFFF0000u), v1 = __uint_as_float(sc1 & 0xFFFF0000u);
+      const float vs0 = v0 == 0.0f ? kNoScale : fmaxf(v0, kMinScale), vs1 = v1 == 0.0f ? kNoScale : fmaxf(v1, kMinScale);
       const float lv0 = lg2(vs0), lv1 = lg2(vs1);
       float rs0 = rcp(vs0), rs1 = rcp(vs1);
 #pragma unroll
@@ -332,8 +331,8 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
         l[c][0] = fmaf(e0, rs0, fmaf(e2, rs1, l[c][0]));
         l[c][1] = fmaf(e1, rs0, fmaf(e3, rs1, l[c][1]));
         const __half2 pa2 = __floats2half2_rn(e0, e1), pb2 = __floats2half2_rn(e2, e3);
-        pb[c][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&pa2));
-        pb[c][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&pb2));
+        pb[c][0] = movmatrix_trans(v0 == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&pa2));
+        pb[c][1] = movmatrix_trans(v1 == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&pb2));
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -492,7 +491,7 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
   if (!q_bf16 || !o_bf16 || !cu_seqlens || !kv_len || !block_table || !workspace || q_stride < row || o_stride < row)
     return FT_ERR_INVALID_ARG;
   if (!ft_host::aligned16(workspace)) return FT_ERR_INVALID_ARG;
-  if (B > ft::kApMaxB) return FT_ERR_UNSUPPORTED;
+  if (B > ft::kApMaxB || (int64_t)total_q * (c->n_q / c->n_kv) > INT32_MAX) return FT_ERR_UNSUPPORTED;
   // units of work are counted in 32 bits
   if (((int64_t)table_stride * page_size / ft::kUnit + 1 + ft::kSegUnits) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
   if (ws_bytes < ft_attn_paged_workspace_bytes(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;

@@ -19,6 +19,10 @@ constexpr float kOUp = 16777216.0f;           // 2^24
 constexpr float kPBias = 10.0f;               // P = 2^(t - m + 10): FP16 normals down to 2^-24 of the largest weight
 constexpr float kPLazy = 4.0f;                // the running max moves when a score passes it by 2^4 (P < 2^14 + rounding)
 constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: smaller V scales count as this (their values are ~0)
+// An entry whose V is zero (scale 0) weighs in the sum of weights alone, with lv = -60: that weight
+// and those of values between 2^-70 and 2^70 stay within FP32's (and P's) range beside each other.
+constexpr uint32_t kNoScaleExp = 67u;           // exponent of 2^-60
+constexpr float kNoScale = 8.6736173798840355e-19f;  // 2^-60
 
 struct AttnPagedParams {
   const uint8_t* pages;
@@ -32,19 +36,24 @@ struct AttnPagedParams {
   float qscale, norm;  // scale log2(e) kQUp; 1 / sqrt(hb)
 };
 
+// One request's length, checked: 0 (every row empty: zeros) where it is negative, passes the table
+// row or is within a tile of 2^31.
+__device__ __forceinline__ int attn_length(const AttnPagedParams& p, int b, int32_t* status) {
+  const int kv = p.kv_len[b];
+  if (kv >= 0 && kv <= INT32_MAX - 256 && ((kv + p.L.psize - 1) >> p.L.pshift) <= p.table_stride) return kv;
+  set_status(status, FT_DEV_CAPACITY);
+  return 0;
+}
+
 // One request's rows and length, checked (conditions to status, which may be NULL); false:
 // nothing of it is computed.
 __device__ __forceinline__ bool attn_request(const AttnPagedParams& p, int b, int32_t* status, int& row0, int& n, int& kv) {
   row0 = p.cu[b];
   n = p.cu[b + 1] - row0;
-  kv = p.kv_len[b];
+  kv = attn_length(p, b, status);
   if (row0 < 0 || n < 0 || row0 > p.total_q - n || n > p.max_q) {
     set_status(status, FT_DEV_RANGE);
     return false;
-  }
-  if (kv < 0 || ((kv + (int64_t)p.L.psize - 1) >> p.L.pshift) > p.table_stride) {
-    set_status(status, FT_DEV_CAPACITY);
-    kv = 0;  // every row empty: zeros
   }
   return true;
 }

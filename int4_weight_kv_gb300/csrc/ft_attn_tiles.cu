@@ -13,7 +13,8 @@
 //
 // Scales are multiplied into the operands, relative to a power of two per 32 positions:
 // a scale has 8 significant bits and a code 3, so the product is exact in FP16 down to 2^-8
-// of the group's largest scale.  The groups' powers of two, kf for K and 2^f for V, come
+// of that power; where a group has smaller scales its operands are made 2^8 times larger (one
+// more product a word, in such groups only) and are exact down to 2^-16.  The groups' powers of two, kf for K and 2^f for V, come
 // back as one factor and one term of each score, t = S kf + f: P = 2^(t - m) weighs V's
 // operand, and the sum of weights takes 2^-f per group.  (Scales applied per column in the
 // softmax needed 96 broadcast 16-byte reads a row and tile, 49 KB of shared-memory bandwidth
@@ -36,6 +37,7 @@ namespace tiles {
 constexpr int kThreads = 512, kRows = 256, kKeys = 128;
 constexpr int kMmaWarp = 12, kPartTiles = 4;
 constexpr float kOScale = 512.0f;  // the operands hold V's values x 2^-9
+constexpr uint32_t kWide = 0x5C005C00u;  // 2^8 in both halves: the factor of a group with a wide range of scales
 constexpr int kScaleRing = 4;  // per tile and group of 32 positions: kf, f, 2^-f, mask of the positions that exist
 // Registers of a thread by role (softmax twice, decode, issue): the sum over the four
 // warpgroups is what the block is launched with, kThreads x 128.
@@ -519,10 +521,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
     for (int j = 0; j < nkt; ++j) {
       const int st = j & 1;
+      // an entry without finite scales (its own row was not finite) must not reach its neighbours, nor
+      // the rows that do not see it: it counts as masked
+      if (((sc >> 7) & 0xFFu) == 0xFFu || ((sc >> 23) & 0xFFu) == 0xFFu) sc = 0u, there = false;
       // the 32 positions' scales relative to their largest's power of two, as multipliers of the
-      // decoded words (codes x 2^-24 and, for odd values, x 2^-20): code x (scale / 2^e) x 2^-9
-      const uint32_t ek = max(__reduce_max_sync(0xffffffffu, (sc & 0x7FFFu) >> 7), 27u);
-      const uint32_t ev = max(__reduce_max_sync(0xffffffffu, (sc >> 23) & 0xFFu), 27u);
+      // decoded words (codes x 2^-24 and, for odd values, x 2^-20): code x (scale / 2^e) x 2^-9,
+      // or x 2^-1 where a scale's exponent is more than 7 below the largest's
+      const uint32_t xk = (sc & 0x7FFFu) >> 7, xv = (sc >> 23) & 0xFFu;
+      uint32_t ek = __reduce_max_sync(0xffffffffu, xk), ev = __reduce_max_sync(0xffffffffu, xv);
+      const bool wide_k = __any_sync(0xffffffffu, xk != 0u && xk + 7u < ek);
+      const bool wide_v = __any_sync(0xffffffffu, xv != 0u && xv + 7u < ev);
+      ek = max(ek, 27u), ev = ev == 0u ? kNoScaleExp : max(ev, 27u);
       const float mk = __uint_as_float(sc << 16) * __uint_as_float((268u - ek) << 23);
       const float mv = __uint_as_float(sc & 0xFFFF0000u) * __uint_as_float((268u - ev) << 23);
       const __half2 mk2 = __floats2half2_rn(mk, mk * 0.0625f);  // (even, odd values)
@@ -537,9 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       }
       if (lane == 0) {
         float* dst = reinterpret_cast<float*>(scales + 4 * (j % kScaleRing)) + w4;
-        dst[0] = __uint_as_float(min(ek + 4u, 254u) << 23);  // 2^(e + 9) / kQUp, e = ek - 126
-        dst[4] = (float)((int)ev - 126);
-        dst[8] = __uint_as_float((ev > 252u ? 1u : 253u - ev) << 23);
+        const uint32_t tv = wide_v ? ev - 8u : ev;
+        dst[0] = __uint_as_float((wide_k ? ek - 4u : min(ek + 4u, 254u)) << 23);  // 2^(e + 9) / kQUp (or 2^-8 of it), e = ek - 126
+        dst[4] = (float)((int)tv - 126);
+        dst[8] = __uint_as_float((tv > 252u ? 1u : 253u - tv) << 23);
         dst[12] = __uint_as_float(exist);
       }
       {
@@ -554,6 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
             const int w = (lane >> 3) * NJ + k;  // word of the entry: slots 8 w .. 8 w + 7 of the operand's row
             uint32_t r[4];
             paged_word(kw[i][k], r);
+            if (wide_k) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) r[e] = hmul2(r[e], kWide);
+            }
             *reinterpret_cast<uint4*>(kd + (w / 8) * (kKeys * 128) + key * 128 + (((w % 8) ^ (key & 7)) << 4)) =
                 make_uint4(hmul2(r[0], m0), hmul2(r[1], m1), hmul2(r[2], m0), hmul2(r[3], m1));
           }
@@ -579,6 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
             const uint32_t m0 = __shfl_sync(0xffffffffu, mvu, 8 * i + 2 * (D == 128 ? k : 2 * (lane >> 4) + k));
             const uint32_t m1 = hmul2(m0, 0x2C002C00u);  // / 16
             paged_word(vw[i][k], r[k]);
+            if (wide_v) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) r[k][e] = hmul2(r[k][e], kWide);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[k][e] = hmul2(r[k][e], (e & 1) ? m1 : m0);
           }

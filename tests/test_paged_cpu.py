@@ -120,6 +120,8 @@ def test_attention_refusals(ft):
     call = lambda **o: lib.ft_attn_paged_int4(ctypes.byref(c), *dict(ok, **o).values(), None, None)  # noqa: E731
     assert call(total=0) == ft.FT_OK and call(wsb=size - 1) == ft.FT_ERR_WORKSPACE
     assert call(ps=40) == ft.FT_ERR_UNSUPPORTED
+    for big in (dict(total=2 ** 29), dict(stride=2 ** 28), dict(B=8193)):
+        assert call(wsb=2 ** 60, **big) == ft.FT_ERR_UNSUPPORTED, big
     for bad in (dict(pages=None), dict(q=None), dict(o=None), dict(cu=None), dict(kv=None), dict(table=None), dict(ws=None),
                 dict(ws=FAKE + 4), dict(B=0), dict(total=-1), dict(max_q=0), dict(stride=0), dict(qs=4095), dict(os=1),
                 dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf"))):
@@ -132,6 +134,7 @@ def test_logprobs_refusals(ft):
     call = lambda **o: lib.ft_logprobs(*dict(ok, **o).values(), None, None)  # noqa: E731
     assert call(N=0) == ft.FT_OK
     assert call(top=33) == ft.FT_ERR_UNSUPPORTED and call(V=3, top=4) == ft.FT_ERR_UNSUPPORTED
+    assert call(V=2 ** 30 + 1, stride=2 ** 31) == ft.FT_ERR_UNSUPPORTED
     for bad in (dict(x=None), dict(dt=2), dict(stride=99), dict(N=-1), dict(V=0), dict(top=-1), dict(ids=None), dict(vals=None),
                 dict(t=None), dict(x=FAKE + 2), dict(x=FAKE + 1, dt=ft.FT_BF16)):
         assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad

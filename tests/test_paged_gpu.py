@@ -248,6 +248,15 @@ class Attn:
         self.qf = self.q.float().cpu().numpy().astype(np.float64)
         self.scale = self.d ** -0.5
 
+    def set_scales(self, b, positions, k=None, v=None):
+        """K and V scales (floats, rounded down to BF16) of request b's positions, in every head."""
+        bits = self.pool_np[:, -4 * self.ps:].view(np.uint16).reshape(self.n_pages, self.n_kv, self.ps, 2)
+        for pos in positions:
+            for i, x in enumerate((k, v)):
+                if x is not None:
+                    bits[self.table[b, pos // self.ps], :, pos % self.ps, i] = np.float32(x).view(np.uint32) >> 16
+        self.pool = torch.from_numpy(self.pool_np.reshape(-1)).cuda()
+
     def run(self, max_q=None, ws=None, stream=None, o=None, status=None, q=None):
         o = torch.full((self.total + 2, self.n_q, self.d), 7.0, dtype=torch.bfloat16, device="cuda") if o is None else o
         max_q = max(self.qlens) if max_q is None else max_q
@@ -261,7 +270,7 @@ class Attn:
         torch.cuda.synchronize()
         return o, int(st.item())
 
-    def check(self, o, reqs=None, heads=None):
+    def check(self, o, reqs=None, heads=None, floor=2.0 ** -35):
         G = self.n_q // self.n_kv
         got = o.float().cpu().numpy().astype(np.float64)
         assert (got[self.total:] == 7.0).all()               # rows behind the last sequence
@@ -279,7 +288,7 @@ class Attn:
                 o64, vn, dn = paged.attend_rows(self.qf[rows, h], kh, vh, self.had or self.d, self.scale, kv - n)
                 err = np.linalg.norm(got[rows, h] - o64, axis=-1)
                 tol = (2.0 ** -10 * dn + 2.0 ** -11 + 2.0 ** -16) * vn + 2.0 ** -8 * np.linalg.norm(o64, axis=-1)
-                tol += kv * 2.0 ** -35 * vs[pages, j].reshape(-1)[:kv].max(initial=0.0) * 7 * self.d ** 0.5
+                tol += kv * floor * vs[pages, j].reshape(-1)[:kv].max(initial=0.0) * 7 * self.d ** 0.5
                 empty = vn == 0
                 assert not got[rows, h][empty].any()
                 assert np.all(err <= tol), (b, h, float(np.max(err / np.maximum(tol, 1e-300))))
@@ -394,6 +403,104 @@ def test_attention_bad_query(n):
     a.check(torch.where(keep, o, want))
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), 2.0 ** 9, 2.0 ** 13])
+@pytest.mark.parametrize("n,d", [(5, 128), (200, 128), (200, 64)])
+def test_attention_later_entries_do_not_reach_earlier_rows(n, d, what):
+    """An entry of the new tokens' own with scales that are not finite, or far above its neighbours', is not there for
+    the tokens before it (its neighbours in the same tile keep all their digits)."""
+    a = Attn(32, 8, d, 64, [n, n], [n + 60, n + 60])
+    first = n // 2                                             # tokens before the entry
+    a.set_scales(0, [60 + first], k=what, v=what)
+    o, _ = a.run()
+    a.check(o, reqs=[1])
+    # request 0 as if it ended before the entry
+    a.qlens, a.kvlens, a.total, a.cu = [first, 0], [60 + first, 0], first, np.array([0, first, first])
+    tail = torch.full_like(o[:2], 7.0)
+    a.check(torch.cat([o[:first], tail]), reqs=[0], floor=2.0 ** -27)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 60, 1.0, 2.0 ** -60])
+@pytest.mark.parametrize("n", [1, 70])
+def test_attention_entries_without_values_keep_their_weight(n, big):
+    """Entries whose V is zero (scale 0) take their part of the softmax, however large or small the others' values are."""
+    a = Attn(8, 2, 128, 64, [n], [70])
+    a.set_scales(0, range(32), v=0.0)                          # whole groups and tiles of them
+    a.set_scales(0, range(32, 70), v=big)
+    a.set_scales(0, [40, 69], v=0.0)
+    o, st = a.run()
+    assert st == 0
+    a.check(o)
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_attention_scales_of_many_sizes(n):
+    """Neighbouring scales that differ by up to 2^15: exact products still."""
+    a = Attn(8, 2, 128, 64, [n], [400])
+    g = np.random.default_rng(3)
+    for pos in range(400):
+        a.set_scales(0, [pos], k=2.0 ** -g.integers(0, 15), v=2.0 ** -g.integers(0, 15))
+    o, st = a.run()
+    assert st == 0
+    a.check(o, floor=2.0 ** -27)     # operands 2^8 larger, so weights of FP16's smallest step 2^-24 count 2^8 times as much
+
+
+@pytest.mark.parametrize("B,n_q,n_kv,d,ps,new,top", [(150, 4, 2, 64, 16, 1, 90), (1100, 2, 1, 64, 16, 1, 40), (40, 8, 2, 128, 64, 20, 200),
+                                                     (600, 2, 2, 64, 32, 9, 60)])
+def test_attention_of_many_requests(B, n_q, n_kv, d, ps, new, top):
+    """More requests than lanes, threads and search steps, some without rows or without a cache."""
+    g = np.random.default_rng(B)
+    q = g.integers(0, new + 1, B)
+    q[g.integers(0, B, 3)] = new
+    if new > 1:
+        q[7] = 33                                              # (a group's rows pass 32: the kernel for many rows)
+    kv = q + g.integers(0, top, B)
+    kv[g.integers(0, B, 3)] = 0
+    a = Attn(n_q, n_kv, d, ps, [int(x) for x in q], [int(x) for x in kv])
+    o, st = a.run()
+    assert st == 0
+    a.check(o)
+
+
+def test_attention_in_parts_over_q_in_place():
+    """Rows over a long cache, in parts that a second kernel joins, beside short requests, written over q."""
+    a = Attn(16, 2, 128, 64, [40, 3, 0, 17], [5000, 3, 70, 40])
+    want, st = a.run()
+    assert st == 0
+    a.check(want, heads=[0, 9, 15])
+    buf = a.q.clone()
+    o, st = a.run(o=buf, q=buf)
+    assert st == 0 and torch.equal(o[:a.total], want[:a.total])
+
+
+@pytest.mark.parametrize("qlens,kvlens", [([1] * 6, [3000, 1, 64, 65, 700, 0]), ([150, 1, 40], [150, 2000, 900]), ([40], [6000])])
+def test_attention_captured_and_replayed(qlens, kvlens):
+    """One capture; the lengths, tables and queries that it reads change on the device between the replays."""
+    a = Attn(32, 8, 128, 64, qlens, kvlens)
+    want, _ = a.run()
+    cu, kv, table, st = _i32(a.cu), _i32(a.kvlens), _i32(a.table), _status()
+    q = a.q.clone()
+    o = torch.full((a.total + 2, a.n_q, a.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ft.ft_attn_paged_workspace_bytes(a.cfg, a.B, a.total, max(qlens)), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ft.check(ft.ft_attn_paged_int4(a.cfg, a.pool, a.n_pages, a.ps, q, cu, kv, table, a.B, a.total, max(qlens), a.scale, o, ws,
+                                       st))
+    for _ in range(2):
+        ws.fill_(0xFF)
+        o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+    short = [max(x // 2, min(x, 1)) for x in kvlens]
+    kv.copy_(_i32(short))
+    q.copy_(a.q.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    a.kvlens = short
+    again, _ = a.run(q=q)
+    assert torch.equal(o, again) and st.item() == 0
+
+
 def test_attention_offsets_past_32_bits():
     """Pages behind the first 4 GiB (and 2^32 bytes of one head's stride) are addressed with 64 bits."""
     cfg, ps, d, h = _cfg(8, 8, 128), 64, 128, 8
@@ -424,6 +531,23 @@ def test_attention_offsets_past_32_bits():
 
 
 # ---------------------------------------------------------------- log probabilities
+def test_lengths_next_to_2_to_31_are_not_served():
+    a = Attn(2, 1, 64, 128, [1], [10])
+    table = torch.zeros((1, 1 << 24), dtype=torch.int32, device="cuda")
+    st, o = _status(), torch.full((1, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for rows in (1, 40):
+        ws = torch.empty(ft.ft_attn_paged_workspace_bytes(a.cfg, 1, rows, rows), dtype=torch.uint8, device="cuda")
+        q = a.q[:1].expand(rows, 2, 64).contiguous()
+        o = torch.full_like(q, 7.0)
+        ft.check(ft.ft_attn_paged_int4(a.cfg, a.pool, a.n_pages, 128, q, _i32([0, rows]), _i32([2 ** 31 - 250]), table, 1, rows, rows,
+                                       0.1, o, ws, st))
+        assert ft.ft_read_device_status(st) == ft.FT_DEV_CAPACITY and not o.any()
+    st, kv, cu, slots = _status(), _i32([7]), _i32([7, 7]), _i32([7] * 5)
+    ft.check(ft.ft_kv_page_map(128, a.n_pages, _i32([2 ** 31 - 2]), _i32([5]), 1, table, _i32([0, 1]), _i32([0]), None, cu, kv, slots, st))
+    assert ft.ft_read_device_status(st) == ft.FT_DEV_CAPACITY
+    assert kv.tolist() == [0] and slots.tolist() == [-1] * 5 and cu.tolist() == [0, 5] and not table.any()
+
+
 def _logprobs(x, t, top, want_all=True):
     n = x.shape[0]
     f = lambda *s: torch.full(s, 5.0, dtype=torch.float32, device="cuda")  # noqa: E731
