@@ -50,7 +50,8 @@ struct Cfg {
   static constexpr int kPanels = D / 64;                 // 128-byte-wide panels of Q and K rows
   static constexpr int kQ = 128 * D * 2;                 // one tile's query operand
   static constexpr int kK = kKeys * D * 2, kV = kKeys * D * 2;  // one stage
-  static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffScale = kOffV + 2 * kV;
+  static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffH = kOffV + 2 * kV;
+  static constexpr int kOffScale = kOffH + D * D * 2;    // H: the rotation's matrix
   static constexpr int kOffBar = kOffScale + kScaleRing * 64;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment slack
   static constexpr int kColO = 256;                    // tensor memory: S0, S1, then O0, O1
@@ -70,6 +71,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* d) {
         "=r"(d[25]), "=r"(d[26]), "=r"(d[27]), "=r"(d[28]), "=r"(d[29]), "=r"(d[30]), "=r"(d[31])
       : "r"(at)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t* d) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
+               : "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
   asm volatile(
@@ -112,9 +119,18 @@ __device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-// FP32 accumulator, FP16 operands, both K-major.
+// FP32 accumulator, FP16 (BF16) operands, both K-major.
 constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+constexpr uint32_t idesc_bf16(int M, int N) { return idesc_f16(M, N) | (1u << 7) | (1u << 10); }
+// Byte offset of 16-byte chunk c of row r in an operand of `rows` rows: K-major, 128-byte swizzle.
+__device__ __forceinline__ uint32_t chunk_at(int rows, int r, int c) {
+  return (uint32_t)((c / 8) * (rows * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+}
+// 16 bytes from global to shared memory, asynchronously; zeros where `there` is false.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -177,8 +193,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     int32_t* status = blockIdx.x == 0 ? p.status : nullptr;
     if (tid == 0) find[1] = -1;
     __syncthreads();
+    // The rotation's matrix as a BF16 operand: row n holds H's entries (+-1, or 0 outside the blocks) of
+    // the channel in slot n of the query operand, whose channels have the order of the cache's words.
+    auto put_h = [&](int first, int step) {
+      for (int i = first; i < D * (D / 8); i += step) {
+        const int nn = i / (D / 8), c = i % (D / 8), w = nn / 8, ch = 32 * (w % NJ) + 2 * (w / NJ) + 8 * ((nn % 8) / 2) + (nn & 1);
+        const int par = ch & (p.hb - 1);
+        uint32_t v[4];
+        if (p.hb >= 8) {  // channels 8 c .. 8 c + 7: one block's or another's; the signs of their low three bits
+          v[0] = ((ch ^ (8 * c)) < p.hb ? 0x3F803F80u : 0u) ^ ((par & 1) ? 0x80000000u : 0u) ^
+                 ((__popc(par & (8 * c)) & 1) ? 0x80008000u : 0u);
+          v[1] = v[0] ^ ((par & 2) ? 0x80008000u : 0u);
+          v[2] = v[0] ^ ((par & 4) ? 0x80008000u : 0u);
+          v[3] = v[1] ^ ((par & 4) ? 0x80008000u : 0u);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int k = 8 * c + 2 * y;
+            const uint32_t a = ((ch ^ k) < p.hb ? 0x3F80u : 0u) | ((uint32_t)__popc(par & k) << 15);
+            const uint32_t b = ((ch ^ (k + 1)) < p.hb ? 0x3F80u : 0u) | ((uint32_t)__popc(par & (k + 1)) << 15);
+            v[y] = (a & 0xFFFFu) | (b << 16);
+          }
+        }
+        *reinterpret_cast<uint4*>(sm + C::kOffH + chunk_at(D, nn, c)) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    };
     if (p.B <= 32) {  // a request per lane of the first warp
-      if (warp == 0) {
+      if (warp > 0) {
+        put_h(tid - 32, kThreads - 32);
+      } else {
         int row0 = 0, n = 0, kv = 0;
         const int nb = lane < p.B ? blocks(lane, status, row0, n, kv) : 0;
         int inc = nb;
@@ -194,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         }
       }
     } else {
+      put_h(tid, kThreads);
       const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
       int sum = 0, row0, n, kv;
       for (int b = b0; b < b1; ++b) sum += blocks(b, status, row0, n, kv);
@@ -235,15 +279,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   const int ntile = nrow > 128 ? 2 : 1;
   const int last = kv - n + (r0 + nrow - 1) / p.G;               // last visible position of any row
   const int all_kt = last >= 0 ? last / kKeys + 1 : 0;
-  const int parts = min(sp.parts, max(1, (all_kt + kPartTiles - 1) / kPartTiles)), per_part = (all_kt + parts - 1) / parts;
+  const int parts = min(sp.parts, max(1, (all_kt + kPartTiles - 1) / kPartTiles)), per_part = parts == 1 ? all_kt : (all_kt + parts - 1) / parts;
   const int j0 = part * per_part, nkt = max(0, min(all_kt - j0, per_part));  // this CTA's tiles: j0, j0 + 1, ...
   if (sp.parts > 1 && h == 0 && part == 0 && tid == 0) sp.meta[want] = make_int4(b, r0, nrow, parts);
   if (part >= parts) return;
   const int* table = p.table + (size_t)b * p.table_stride;
 
+  // ---- the query rows as they are (BF16), zeros behind the last, to V's room: the tensor core rotates them
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+  // each thread's chunks: one of every kStep-th row, its token and head of the group advanced along
+  constexpr int kStep = kThreads / kChunks;
+  auto walk = [&](int rows, auto&& body) {  // body(row, chunk, token's row of q and o, first element in it)
+    const int c = tid % kChunks, rg = r0 + tid / kChunks, dt = kStep / p.G, dh = kStep - dt * p.G;
+    int tok = rg / p.G, hh = rg - tok * p.G;
+#pragma unroll 4
+    for (int rr = tid / kChunks; rr < rows; rr += kStep) {
+      body(rr, c, row0 + tok, (h * p.G + hh) * D + 8 * c);
+      tok += dt, hh += dh;
+      if (hh >= p.G) hh -= p.G, ++tok;
+    }
+  };
+  if (nkt > 0) {
+    walk(128 * ntile, [&](int rr, int c, int token, int at) {
+      const uint16_t* src = p.q + (rr < nrow ? token * p.q_stride + at : 0);
+      const uint32_t to = C::kOffV + (rr >= 128 ? C::kQ : 0) + chunk_at(128, rr & 127, c);
+      if (rr >= nrow || (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+        cp_async16_zfill(sm32 + to, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15), rr < nrow);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = (uint32_t)src[2 * k] | ((uint32_t)src[2 * k + 1] << 16);
+        *reinterpret_cast<uint4*>(sm + to) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    });
+  }
   const uint32_t bar = sm32 + C::kOffBar;
   const uint32_t s_full = bar + 16, p_full = bar + 32, o_full = bar + 48, k_full = bar + 64,
-                 k_empty = bar + 80, v_full = bar + 96, v_empty = bar + 112, sc_full = bar + 128, drained = bar + 160;
+                 k_empty = bar + 80, v_full = bar + 96, v_empty = bar + 112, sc_full = bar + 128, drained = bar + 160,
+                 rot_full = bar + 168, rows_put = bar + 184;  // twice each: the queries' rotation, the outputs'
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -253,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       mbar_init(k_empty + 8 * i, 1);
       mbar_init(v_full + 8 * i, 128);
       mbar_init(v_empty + 8 * i, 1);
+      mbar_init(rot_full + 8 * i, 1);
+      mbar_init(rows_put + 8 * i, 128);
     }
     for (int i = 0; i < kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
     mbar_init(drained, 1);
@@ -262,67 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // ---- the rotated query rows as the FP16 operand, channels in the order of the cache's words: all
-  // warps, D / 32 lanes a row with 32 channels each (8 lanes a row of 16 channels cost less code, which
-  // runs cold, but twice the shuffles: 11.8 thousand cycles against 6.3 for 256 rows)
-  constexpr int LV = D / 32, RW = 32 / LV, kRowStep = RW * (kThreads / 32);  // lanes of a row, rows of a warp, of all warps
-  const int lj = lane % LV, rr0 = warp * RW + lane / LV;
-  auto row_ptr = [&](int rr) {  // row of q and o, and the element in it, of row rr (token, head)
-    const int rg = r0 + rr, tok = rg / p.G;
-    return make_int2(row0 + tok, (h * p.G + rg - tok * p.G) * D + 32 * lj);
-  };
-  if (nkt > 0) {
-    const float f0 = p.qscale * p.norm;
-    const f32x2 f2(f0, f0);
-    uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
-#pragma unroll 1
-    for (int rr = rr0; rr - lane / LV < 128 * ntile; rr += kRowStep) {  // (a warp's rows together)
-      f32x2 v[16];
-      const int2 at = row_ptr(rr);
-      const uint16_t* src = p.q + at.x * p.q_stride + at.y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (rr < nrow) {
-          if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-            const uint4 q = *(reinterpret_cast<const uint4*>(src) + i);
-            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = (uint32_t)src[8 * i + 2 * k] | ((uint32_t)src[8 * i + 2 * k + 1] << 16);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
-      }
-      paged_fwht<D>(v, p.hb);
-      uint8_t* qs = sm + C::kOffQ + (rr >= 128 ? C::kQ - 128 * 128 : 0) + rr * 128;
-#pragma unroll
-      for (int tig = 0; tig < 4; ++tig) {  // word (tig, lj): channels 2 tig + 8 e + {0, 1} of the lane's
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a, c;
-          mul2(v[tig + 4 * e], f2).get(a, c);
-          const __half2 hv = __floats2half2_rn(a, c);
-          o[e] = *reinterpret_cast<const uint32_t*>(&hv);
-          over = hfma2(o[e], 0u, over);
-        }
-        const int w = tig * NJ + lj;
-        *reinterpret_cast<uint4*>(qs + (w / 8) * (128 * 128) + (((w % 8) ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
-    if ((over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
-    fence_proxy_async_smem();
-  }
+  cp_async_wait_all();
+  fence_proxy_async_smem();
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  auto out_at = [&](int rr, int c4) {  // 4 channels of row rr on their way out
-    const int q = rr & 127;
-    return reinterpret_cast<float4*>(sm + (rr < 128 ? C::kOffQ : C::kOffK)) + q * (D / 4) + (c4 ^ (q & 7) ^ (c4 >> 3));
-  };
+  auto out_at = [&](int r, int c) { return (uint32_t)((r * kChunks + (c ^ (r & 7))) << 4); };  // chunk c of row r on its way out
   float4* scales = reinterpret_cast<float4*>(sm + C::kOffScale);  // [ring][kf, f, 2^-f, mask][4 groups]
   bool ok = true;
 
@@ -335,8 +356,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       const int tok = min(r / p.G, n - 1);
       const int lim = kv - n + tok;  // last position this row sees
       const int lim_all = kv - n + (r0 + 128 * t + 32 * (warp & 3)) / p.G;  // and that every row of the warp sees
+      // the rotated query row as the FP16 operand
+      if (nkt > 0 && !all_wait(rot_full + 8 * t, 0)) ok = false;
+      if (ok && nkt > 0) {
+        fence_after();
+        const float f0 = p.qscale * p.norm;
+        uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_base + 128 * t + c, v);
+          wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 hv = __floats2half2_rn(__uint_as_float(v[8 * i + 2 * k]) * f0, __uint_as_float(v[8 * i + 2 * k + 1]) * f0);
+              o[k] = *reinterpret_cast<const uint32_t*>(&hv);
+              over = hfma2(o[k], 0u, over);
+            }
+            *reinterpret_cast<uint4*>(sm + C::kOffQ + C::kQ * t + chunk_at(128, row, c / 8 + i)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if ((over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
+        fence_proxy_async_smem();
+        fence_before();
+        mbar_arrive(rows_put + 8 * t);
+      }
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < nkt; ++j) {
+      for (int j = 0; ok && j < nkt; ++j) {
         if (!all_wait(s_full + 8 * t, j & 1) || !all_wait(sc_full + 8 * (j % kScaleRing), (j / kScaleRing) & 1)) {
           ok = false;
           break;
@@ -417,16 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         fence_before();
         mbar_arrive(p_full + 8 * t);
       }
-      // ---- O / l to shared memory (the operands of QK are done with: tile 0 takes Q's room, tile 1 K's)
       if (ok && nkt > 0 && !all_wait(o_full + 8 * t, (nkt - 1) & 1)) ok = false;
-      if (ok) {
+      if (ok && parts > 1) {
+        // ---- this part's maximum, sum and O for the joining kernel
         fence_after();
-        const float inv = parts > 1 ? 1.0f : l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
-        float* partial = nullptr;
-        if (parts > 1) {
-          partial = sp.part + ((((size_t)want * p.L.nkv + h) * sp.parts + part) * 128 + row) * (D + 4);
-          partial[0] = m, partial[1] = l;
-        }
+        float* partial = sp.part + ((((size_t)want * p.L.nkv + h) * sp.parts + part) * 128 + row) * (D + 4);
+        partial[0] = m, partial[1] = l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -438,10 +483,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4* dst = partial ? reinterpret_cast<float4*>(partial + 4 + c + i) : out_at(128 * t + row, (c + i) / 4);
-            *dst = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                               __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(partial + 4 + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      } else if (ok && nkt > 0) {
+        // ---- O / l as two BF16 operands, the value and what its rounding left (2^-17 remains), over those
+        // of QK, which are done with (tile 0 takes Q's room, tile 1 K's); rotated by the tensor core
+        fence_after();
+        const float inv = l == 0.0f ? 0.0f : kOScale / l;  // a row that sees nothing: zeros
+        uint8_t* own = sm + (t == 0 ? C::kOffQ : C::kOffK);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o);
+          wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = __uint_as_float(o[8 * i + 2 * k]) * inv, b = __uint_as_float(o[8 * i + 2 * k + 1]) * inv;
+              const __nv_bfloat162 hv = __floats2bfloat162_rn(a, b);
+              hi[k] = *reinterpret_cast<const uint32_t*>(&hv);
+              const __nv_bfloat162 lv = __floats2bfloat162_rn(a - __uint_as_float(hi[k] << 16), b - __uint_as_float(hi[k] & 0xFFFF0000u));
+              lo[k] = *reinterpret_cast<const uint32_t*>(&lv);
+            }
+            const uint32_t at = chunk_at(128, row, c / 8 + i);
+            *reinterpret_cast<uint4*>(own + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(own + C::kQ + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        fence_before();
+        mbar_arrive(rows_put + 8 * t);
+        if (!all_wait(rot_full + 8 * t, 1)) ok = false;
+        if (ok) {
+          fence_after();
+          // slots back to channels: chunk e of group jj holds its pairs of four words
+#pragma unroll
+          for (int jj = 0; jj < NJ; ++jj) {
+            uint32_t v[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld8(tmem + lane_base + 128 * t + 8 * (q * NJ + jj), v[q]);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(v[q][2 * e]) * p.norm, __uint_as_float(v[q][2 * e + 1]) * p.norm);
+                w[q] = *reinterpret_cast<const uint32_t*>(&bv);
+              }
+              *reinterpret_cast<uint4*>(own + out_at(row, 4 * jj + e)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
       }
@@ -577,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       mbar_arrive(sc_full + 8 * (j % kScaleRing));
       mbar_arrive(k_full + 8 * st);
       if (j + 1 < nkt) load_k(j + 1);
-      if (j >= 2 && !all_wait(v_empty + 8 * st, ((j - 2) >> 1) & 1)) {
+      // (V's room held the query rows)
+      if (j >= 2 ? !all_wait(v_empty + 8 * st, ((j - 2) >> 1) & 1) : st < ntile && !all_wait(rot_full + 8 * st, 0)) {
         ok = false;
         break;
       }
@@ -619,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     regs_down<kRegIssue>();
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------- tensor-core issue
-      constexpr uint32_t id_qk = idesc_f16(128, kKeys), id_pv = idesc_f16(128, D);
+      constexpr uint32_t id_qk = idesc_f16(128, kKeys), id_pv = idesc_f16(128, D), id_rot = idesc_bf16(128, D);
       const uint32_t lead = lane == 0 ? 1u : 0u, tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t q_lo = desc_lo(sm32 + C::kOffQ), k_lo = desc_lo(sm32 + C::kOffK), v_lo = desc_lo(sm32 + C::kOffV);
       auto qk = [&](int t, int j) {
@@ -639,9 +734,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
           mma_ts(d, pa + 8 * ks, va + (((ks / 4) * (D * 128) + 32 * (ks % 4)) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
         commit(o_full + 8 * t, lead);
       };
+      // rows times H, over S's columns; the rows' n operands one after another
+      auto rotate = [&](int t, uint32_t rows_at, int n) {
+        const uint32_t h_lo = desc_lo(sm32 + C::kOffH), d = tm + 128 * t;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const uint32_t ra = desc_lo(sm32 + rows_at + i * C::kQ);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t a = ra + (((ks / 4) * (128 * 128) + 32 * (ks % 4)) >> 4), b = h_lo + (((ks / 4) * (D * 128) + 32 * (ks % 4)) >> 4);
+            if (ks == 0 && i == 0) mma_ss<false>(d, a, b, id_rot, lead);
+            else mma_ss<true>(d, a, b, id_rot, lead);
+          }
+        }
+        commit(rot_full + 8 * t, lead);
+      };
       if (nkt > 0) {
+        for (int t = 0; t < ntile; ++t) rotate(t, C::kOffV + t * C::kQ, 1);
         ok = all_wait(k_full, 0);
         for (int t = 0; ok && t < ntile; ++t) {
+          ok = all_wait(rows_put + 8 * t, 0);
+          if (!ok) break;
+          fence_after();
           qk(t, 0);
         }
         if (ok) commit(k_empty, lead);
@@ -663,6 +777,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
           }
         }
       }
+      for (int t = 0; ok && nkt > 0 && parts == 1 && t < ntile; ++t) {
+        ok = all_wait(rows_put + 8 * t, 1);
+        if (!ok) break;
+        fence_after();
+        rotate(t, t == 0 ? C::kOffQ : C::kOffK, 2);
+      }
       // tensor memory is freed only when nothing issued here is in flight
       commit(drained, lead);
       if (!all_wait(drained, 0)) ok = false;
@@ -676,44 +796,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   // the barrier.  (Taken earlier, by warps that are through before a softmax warp has come to
   // take its share, they would leave that warp waiting for registers that nobody returns.)
   if (warp >= 8) regs_up<kRegCommon>();
-  // ---- the rotation undone and the rows stored, by all warps
+  // ---- the rows stored, by all warps
   if (all_ok && parts == 1) {
-    const f32x2 norm2(p.norm, p.norm);
-#pragma unroll 1
-    for (int rr = rr0; rr - lane / LV < nrow; rr += kRowStep) {
-      f32x2 v[16];
+    walk(nrow, [&](int rr, int c, int token, int at) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);  // nothing visible: zeros
+      if (nkt > 0) v = *reinterpret_cast<const uint4*>(sm + (rr < 128 ? C::kOffQ : C::kOffK) + out_at(rr & 127, c));
+      uint16_t* dst = p.o + token * p.o_stride + at;
+      if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+        *reinterpret_cast<uint4*>(dst) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 q = *out_at(rr, 8 * lj + i);
-        v[2 * i] = f32x2(q.x, q.y);
-        v[2 * i + 1] = f32x2(q.z, q.w);
+        for (int k = 0; k < 4; ++k) dst[2 * k] = (uint16_t)w[k], dst[2 * k + 1] = (uint16_t)(w[k] >> 16);
       }
-      paged_fwht<D>(v, p.hb);
-      if (rr >= nrow) continue;
-      const int2 at = row_ptr(rr);
-      uint16_t* dst = p.o + at.x * p.o_stride + at.y;
-      const bool aligned = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a, c;
-          mul2(v[4 * i + k], norm2).get(a, c);
-          const __nv_bfloat162 bv = __floats2bfloat162_rn(a, c);
-          w[k] = *reinterpret_cast<const uint32_t*>(&bv);
-        }
-        if (aligned) {
-          reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            dst[8 * i + 2 * k] = (uint16_t)w[k];
-            dst[8 * i + 2 * k + 1] = (uint16_t)(w[k] >> 16);
-          }
-        }
-      }
-    }
+    });
   }
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
