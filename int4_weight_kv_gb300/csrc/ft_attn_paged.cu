@@ -17,8 +17,13 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 
 // ------------------------------------------------------------------ few rows
 // Requests with up to 8 NT rows (tokens x heads of a group) a KV head: every byte of the
-// cache is read once and used for all of them, so the kernel is bound by HBM as long as a
-// 16-position tile costs fewer than about 360 warp instructions.
+// cache is read once and used for all of them.  A 16-position tile costs a warp about 265
+// instructions (360 would take as long as its bytes at the HBM's rate), so loads and arithmetic
+// weigh alike: 32 requests of 4096 positions took 38.9 us, 35.5 without the arithmetic, 34.6
+// without the loads.  What a share costs before its first tile (lengths, pages, first tiles, the
+// rotated queries: about 4 us) and the joining kernel (2 us) come on top.  Measured with 32 heads
+// over 8 of 128: one request of 1025 positions 9.7 us, 32 of up to 4097 26 us (2.8 TB/s); 64 heads,
+// 8 of up to 32769 35 us (3.6 TB/s).
 //
 // The work is the list of (request, head, 64 positions) units in this order; each CTA takes
 // an equal, contiguous share of it whatever the lengths are, and a warp of its four one
@@ -26,6 +31,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 // about as much beside its tiles as kSegUnits units do, so each (request, head) counts that
 // many more, ahead of its first: without them the shares that hold many short requests took
 // twice as long as the others (32 requests of 1 to 4096 positions: 38 us, 54% of the SMs' time).
+// Measured for 2 / 3 / 5: 29.8 / 28.9 / 27.5 us there, - / 37.7 / 37.2 with 64 heads over 32769.
 // A segment that is a whole (request, head) is finished in place; the others leave (max, sum,
 // accumulator) partials, which a second kernel adds in the order of the shares.
 //   S = K q:     A = K codes (rows positions), B = q (columns the rows)

@@ -20,6 +20,17 @@
 // softmax needed 96 broadcast 16-byte reads a row and tile, 49 KB of shared-memory bandwidth
 // a warp: 5500 cycles per pair of tiles.)
 //
+// The rotations are products with H too: the query rows go to shared memory as they are (BF16, over
+// V's room), Q H comes back from tensor memory as the FP16 operand, and at the end O / l, as two
+// BF16 operands, is rotated the same way.  (In registers, by all warps, they took 8.9 and 8.5
+// thousand cycles of a CTA of 256 rows, a fifth of its time at 20 tiles; now 5.4 and 4.0.)
+//
+// Bound by a tile's chain from S to P: 3900 cycles a pair of tiles, of which the tensor core works
+// for 2048, the issue slots are half used and the exponentials a quarter.  Measured (32 heads over 8
+// of 128): 2 x 2048 tokens over 4096 positions 230 us (895 TFLOP/s), 8192 over 32768 1220 TFLOP/s.
+// Slower: P through shared memory, so that the next S need not wait for P V (264 us); P V in two
+// halves (240); two threads a row, 21 warps (308); a second issuing warp (292).
+//
 // Roles: two warpgroups of softmax (one row per thread, a tile each), one warpgroup
 // decoding (the next tile's bytes in flight in registers), one issuing thread.  While one
 // tile's softmax runs, the tensor core works for the other:
@@ -180,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   __shared__ int find[5];       // request, first row of the CTA's rows (-1: no work), the request's first row, rows and positions
   __shared__ int warp_tot[16];
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (by way of a shuffle the compiler knows that a warp agrees on them: uniform branches and registers)
+  auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
 
   griddep_launch();  // the joining kernel waits for this one's end in any case
   // ---- which rows: block i of all requests' blocks of rows, the last ones (which see most) first
@@ -270,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
     __syncthreads();
   }
-  const int b = find[0], r0 = find[1], row0 = find[2], n = find[3], kv = find[4];
+  const int b = uni(find[0]), r0 = uni(find[1]), row0 = uni(find[2]), n = uni(find[3]), kv = uni(find[4]);
   if (r0 < 0) {
     if (sp.parts > 1 && h == 0 && part == 0 && tid == 0) sp.meta[want] = make_int4(0, 0, 0, 0);
     return;
@@ -314,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     });
   }
   const uint32_t bar = sm32 + C::kOffBar;
-  const uint32_t s_full = bar + 16, p_full = bar + 32, o_full = bar + 48, k_full = bar + 64,
-                 k_empty = bar + 80, v_full = bar + 96, v_empty = bar + 112, sc_full = bar + 128, drained = bar + 160,
-                 rot_full = bar + 168, rows_put = bar + 184;  // twice each: the queries' rotation, the outputs'
+  const uint32_t s_full = bar, p_full = bar + 16, o_full = bar + 32, k_full = bar + 48, k_empty = bar + 64,
+                 v_full = bar + 80, sc_full = bar + 96, drained = bar + 128, rot_full = bar + 136, rows_put = bar + 152;
+  // (rot_full, rows_put: twice each, the queries' rotation and the outputs')
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -325,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       mbar_init(k_full + 8 * i, 128);
       mbar_init(k_empty + 8 * i, 1);
       mbar_init(v_full + 8 * i, 128);
-      mbar_init(v_empty + 8 * i, 1);
       mbar_init(rot_full + 8 * i, 1);
       mbar_init(rows_put + 8 * i, 128);
     }
@@ -422,12 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
           const float fac = to == m ? 1.0f : ex2(m - to);
           m = to;
           if (j > 0) {
-            l *= fac;
-            if (!all_wait(o_full + 8 * t, (j - 1) & 1)) {  // the tensor core is done with O
-              ok = false;
-              break;
-            }
-            fence_after();
+            l *= fac;  // (S came after the last product into O, which is done)
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         fence_before();
         mbar_arrive(p_full + 8 * t);
       }
-      if (ok && nkt > 0 && !all_wait(o_full + 8 * t, (nkt - 1) & 1)) ok = false;
+      if (ok && nkt > 0 && !all_wait(o_full + 8 * t, 0)) ok = false;
       if (ok && parts > 1) {
         // ---- this part's maximum, sum and O for the joining kernel
         fence_after();
@@ -671,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       mbar_arrive(sc_full + 8 * (j % kScaleRing));
       mbar_arrive(k_full + 8 * st);
       if (j + 1 < nkt) load_k(j + 1);
-      // (V's room held the query rows)
-      if (j >= 2 ? !all_wait(v_empty + 8 * st, ((j - 2) >> 1) & 1) : st < ntile && !all_wait(rot_full + 8 * st, 0)) {
+      // (QK of tile j - 1 was issued behind PV of tile j - 2; before that V's room held the query rows)
+      if (j >= 2 ? !all_wait(k_empty + 8 * (st ^ 1), ((j - 1) >> 1) & 1) : st < ntile && !all_wait(rot_full + 8 * st, 0)) {
         ok = false;
         break;
       }
@@ -732,7 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
           mma_ts(d, pa + 8 * ks, va + (((ks / 4) * (D * 128) + 32 * (ks % 4)) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
-        commit(o_full + 8 * t, lead);
       };
       // rows times H, over S's columns; the rows' n operands one after another
       auto rotate = [&](int t, uint32_t rows_at, int n) {
@@ -760,22 +766,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         }
         if (ok) commit(k_empty, lead);
       }
+      // What can be waited for before P is there is waited for then, and few things are committed: S of tile j
+      // says that PV of tile j - 1 is done too, as does k_empty for V's room.
       for (int j = 0; ok && j < nkt; ++j) {
         const bool more = j + 1 < nkt;
+        ok = all_wait(v_full + 8 * (j & 1), (j >> 1) & 1) && (!more || all_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1));
         for (int t = 0; ok && t < ntile; ++t) {
-          ok = (t > 0 || all_wait(v_full + 8 * (j & 1), (j >> 1) & 1)) && all_wait(p_full + 8 * t, j & 1);
+          ok = all_wait(p_full + 8 * t, j & 1);
           if (!ok) break;
           fence_after();
           pv(t, j);
-          if (t == ntile - 1) commit(v_empty + 8 * (j & 1), lead);
-          if (more) {
-            if (t == 0) ok = all_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1);
-            if (!ok) break;
-            fence_after();
-            qk(t, j + 1);
-            if (t == ntile - 1) commit(k_empty + 8 * ((j + 1) & 1), lead);
-          }
+          if (more) qk(t, j + 1);
+          else commit(o_full + 8 * t, lead);
         }
+        if (ok && more) commit(k_empty + 8 * ((j + 1) & 1), lead);
       }
       for (int t = 0; ok && nkt > 0 && parts == 1 && t < ntile; ++t) {
         ok = all_wait(rows_put + 8 * t, 1);
