@@ -23,13 +23,17 @@
 // The rotations are products with H too: the query rows go to shared memory as they are (BF16, over
 // V's room), Q H comes back from tensor memory as the FP16 operand, and at the end O / l, as two
 // BF16 operands, is rotated the same way.  (In registers, by all warps, they took 8.9 and 8.5
-// thousand cycles of a CTA of 256 rows, a fifth of its time at 20 tiles; now 5.4 and 4.0.)
+// thousand cycles of a CTA of 256 rows, a fifth of its time at 20 tiles; now 5.7 and 4.3.)
 //
-// Bound by a tile's chain from S to P: 3900 cycles a pair of tiles, of which the tensor core works
-// for 2048, the issue slots are half used and the exponentials a quarter.  Measured (32 heads over 8
-// of 128): 2 x 2048 tokens over 4096 positions 230 us (895 TFLOP/s), 8192 over 32768 1220 TFLOP/s.
-// Slower: P through shared memory, so that the next S need not wait for P V (264 us); P V in two
-// halves (240); two threads a row, 21 warps (308); a second issuing warp (292).
+// Bound by a tile's chain from S over P to the next S: 3600 cycles a pair of tiles, of which the
+// tensor core works for 2048 and half of the issue slots are used.  The softmax takes 1500 of the
+// chain, so what the issuing warp waits for between P and the next S counts in full: it looks at K and
+// V before P is there and commits nothing that another commit says too.  Measured (32 heads over 8 of
+// 128): 2 x 2048 tokens over 4096 positions 218 us (945 TFLOP/s), 8192 over 32768 1270 TFLOP/s.
+// No faster: P through shared memory, so that the next S need not wait for P V; P V in two halves;
+// half tiles with two S by turns (a product with 64 columns takes as long as with 128); two threads a
+// row; a second issuing warp; eight decoding warps; decoding left out altogether (3.2 ms, not 3.1, for
+// the longer case).
 //
 // Roles: two warpgroups of softmax (one row per thread, a tile each), one warpgroup
 // decoding (the next tile's bytes in flight in registers), one issuing thread.  While one

@@ -14,8 +14,8 @@
 // round through a running threshold instead cost 36 us of 213 for k = 1 and 53 of 88 for
 // k = 20, 256 rows of 128256.)
 // CTA 0 joins the slices through distributed shared memory: one launch, no workspace.
-// Bound by HBM for many rows (2048 FP32 rows of 128256, k = 1: 191 us, 5.5 TB/s); a single row by its
-// latency, hence up to 8 CTAs for it (9.1 us, k = 5).
+// Bound by HBM for many rows (2048 FP32 rows of 128256, k = 1: 192 us, 5.5 TB/s); a single row by its
+// latency, hence up to 8 CTAs for it (9.2 us, k = 5).
 //
 // Alternatives are ordered by a 64-bit key (the value as an ordered integer, then the
 // lower index), so ties have one answer whatever order the row is read in.

@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
 // consecutive rows of one head, so that a prompt's entries leave it as contiguous pieces
 // and the two positions of a V pair meet in neighbouring groups of lanes.  The rotated row
 // is quantised in the registers where it was formed: no shared memory.  Bound by the issue slots
-// (450 warp instructions for eight rows, 77% of the slots used): 32768 tokens of 8 heads of 128, K and V,
-// 29 us of append and 25 us of reading back, 2.9 and 3.3 TB/s.
+// (450 warp instructions for eight rows, 380 to read back; 72% of the slots used): 16384 tokens of 8
+// heads of 128, K and V, 26 us and 23 us, 3.3 and 3.7 TB/s.
 constexpr int kRowThreads = 128;
 
 struct PagedRows {
