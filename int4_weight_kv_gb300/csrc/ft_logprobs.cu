@@ -151,6 +151,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobParams p) {
   constexpr int E = BF16 ? 8 : 4, U = kLpElems / E;  // elements of a 16-byte vector, vectors of a thread's round
   constexpr int kStep = U * kLpThreads;              // vectors of the CTA's round
+  griddep_serve();
   extern __shared__ __align__(16) uint8_t lp_smem[];
   LpShared& s = *reinterpret_cast<LpShared*>(lp_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = p.V, top = p.top;
@@ -435,19 +436,7 @@ static cudaError_t launch_logprobs(const LogprobParams& p, int N, cudaStream_t s
     allowed[dev] = 1;
   }
   const int ctas = lp_cluster(N, p.V);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)N * ctas));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = sizeof(LpShared);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<BF16>, p);
+  return launch_served(logprobs_kernel<BF16>, dim3((unsigned)((int64_t)N * ctas)), dim3(kLpThreads), sizeof(LpShared), st, ctas, p);
 }
 
 }  // namespace ft

@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   extern __shared__ int32_t map_smem[];
   __shared__ long long sums[kMapWarps][2];
   __shared__ int bad, most;
+  griddep_serve();
   const int tid = threadIdx.x, B = p.B;
   int32_t* cu = map_smem;       // [B + 1] first row of each request
   int32_t* pg = cu + B + 1;     // [B + 1] first page taken by each request
@@ -259,6 +260,7 @@ __device__ __noinline__ float paged_edge(float y, float s, float c) {
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) append_paged_kernel(const PagedRows p) {
   constexpr int LV = D / 32;
+  griddep_serve();
   int t, h, j, slot;
   paged_row<D>(p, t, h, j, slot);
   const bool is_v = blockIdx.y != 0;
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(kRowThreads) append_paged_kernel(const PagedRo
 // rounded to BF16.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) read_paged_kernel(const PagedRows p) {
+  griddep_serve();
   int t, h, j, slot;
   paged_row<D>(p, t, h, j, slot);
   slot = paged_slot(p, slot, j);
@@ -492,19 +495,10 @@ int ft_kv_page_map(int page_size, int n_pages, const int32_t* ctx_len, const int
     const int sms = ft_host::num_sms();
     ctas = std::max(1, std::min(want, 2 * (sms > 0 ? sms : 152)));
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(ft::kMapThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.clustered ? ctas : 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ft::page_map_kernel, p) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  return ft::launch_served(ft::page_map_kernel, dim3(ctas), dim3(ft::kMapThreads), smem, (cudaStream_t)stream,
+                           p.clustered ? ctas : 1, p) == cudaSuccess
+             ? FT_OK
+             : FT_ERR_CUDA;
 }
 
 int ft_kv_append_paged_int4(const ft_block_cfg* c, void* pages, int n_pages, int page_size, const uint16_t* k_bf16,
@@ -531,8 +525,7 @@ int ft_kv_append_paged_int4(const ft_block_cfg* c, void* pages, int n_pages, int
   const dim3 grid = ft::row_grid(total, c->n_kv, c->head_dim);
   if (grid.x == 0) return FT_ERR_UNSUPPORTED;
   const auto kernel = c->head_dim == 128 ? ft::append_paged_kernel<128> : ft::append_paged_kernel<64>;
-  kernel<<<grid, ft::kRowThreads, 0, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  return ft::launch_served(kernel, grid, dim3(ft::kRowThreads), 0, (cudaStream_t)stream, 1, p) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
 int ft_kv_read_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const int32_t* slots,
@@ -555,8 +548,7 @@ int ft_kv_read_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages,
   const dim3 grid = ft::row_grid(total, c->n_kv, c->head_dim);
   if (grid.x == 0) return FT_ERR_UNSUPPORTED;
   const auto kernel = c->head_dim == 128 ? ft::read_paged_kernel<128> : ft::read_paged_kernel<64>;
-  kernel<<<grid, ft::kRowThreads, 0, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  return ft::launch_served(kernel, grid, dim3(ft::kRowThreads), 0, (cudaStream_t)stream, 1, p) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
 }  // extern "C"
