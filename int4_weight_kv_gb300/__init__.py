@@ -131,17 +131,23 @@ def _ptr(t):
 def _current():
     """(current CUDA device, its current stream's handle).  The stream object that
     torch.cuda.current_stream() builds costs 3 us a call, its handle alone 0.1."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        torch.cuda.init()
-        _raw_stream = (torch.cuda.current_device, get or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
-    dev = _raw_stream[0]()
-    return dev, _raw_stream[1](dev)
+    if _torch is None:
+        _bind_torch()
+    dev = _torch[0]()
+    return dev, _torch[1](dev)
 
 
-_raw_stream = None
+# (current device, its current stream's handle, torch.float16), once torch is there
+_torch = None
+
+
+def _bind_torch():
+    global _torch
+    import torch
+    torch.cuda.init()
+    _torch = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+              getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+              torch.float16)
 
 
 def _stream(stream):
@@ -152,27 +158,30 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _check_device(*tensors) -> int:
-    """Every tensor (None and raw pointers aside) lives on the current CUDA device; returns its current stream."""
-    here, stream = _current()
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != here:
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{here}")
-    return stream
+def _on(t, dev: int) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _plain(t, nbytes: int):
-    """A contiguous tensor of nbytes-wide elements (or None, or a raw pointer)."""
+def _plain(t, nbytes: int, dev: int):
+    """Pointer of a contiguous tensor of nbytes-wide elements on device `dev` (or None, or a raw pointer)."""
     if t is None or isinstance(t, int):
         return t
-    if t.element_size() != nbytes or not t.is_contiguous():
-        raise ValueError(f"need a contiguous tensor of {nbytes}-byte elements, got {t.dtype} with strides {t.stride()}")
+    if t.get_device() != dev or t.element_size() != nbytes or not t.is_contiguous() or t.dtype is _torch[2]:
+        _on(t, dev)
+        raise ValueError(f"need a contiguous tensor of {nbytes}-byte elements (16-bit: BF16), got {t.dtype} with "
+                         f"strides {t.stride()}")
     return t.data_ptr()
 
 
-def _rows(t, inner: int, nbytes: int) -> tuple[int, int]:
-    """(pointer, elements between rows) of a tensor whose rows are `inner` contiguous nbytes-wide elements."""
+def _rows(t, inner: int, nbytes: int, dev: int) -> tuple[int, int]:
+    """(pointer, elements between rows) of a tensor on device `dev` whose rows are `inner` contiguous nbytes-wide
+    elements; 16-bit ones are BF16 or their bits."""
     shape = t.shape
+    if t.get_device() != dev:
+        _on(t, dev)
+    if t.dtype is _torch[2]:
+        raise ValueError("float16 where BF16 is read")
     if t.is_contiguous() and t.element_size() == nbytes and len(shape) >= 2 and t.numel() == shape[0] * inner:
         return t.data_ptr(), inner
     step = t.stride()
@@ -274,14 +283,15 @@ def ft_kv_pages_bytes(cfg, n_pages: int, page_size: int) -> int:
 def ft_kv_page_map(page_size, n_pages, ctx_len, new_len, B, block_table, free_pages, free_head, free_head_out,
                    cu_seqlens, kv_len, slots, dev_status=None, stream=None) -> int:
     """block_table: int32 [B, >= pages of a request]; the other tensors int32, one-dimensional."""
-    here = _check_device(ctx_len, new_len, block_table, free_pages, free_head, free_head_out, cu_seqlens, kv_len, slots, dev_status)
+    dev, here = _current()
     if min(ctx_len.numel(), new_len.numel(), kv_len.numel(), cu_seqlens.numel() - 1, block_table.shape[0]) < B:
         raise ValueError(f"lengths, prefix sums or block tables of fewer than {B} requests")
-    table, stride = _rows(block_table, block_table.shape[1], 4)
-    return lib().ft_kv_page_map(page_size, n_pages, _plain(ctx_len, 4), _plain(new_len, 4), B, table, stride,
-                                _plain(free_pages, 4), free_pages.numel(), _plain(free_head, 4),
-                                _plain(free_head_out, 4), _plain(cu_seqlens, 4), _plain(kv_len, 4), _plain(slots, 4),
-                                slots.numel(), _ptr(dev_status), here if stream is None else _stream(stream))
+    table, stride = _rows(block_table, block_table.shape[1], 4, dev)
+    return lib().ft_kv_page_map(page_size, n_pages, _plain(ctx_len, 4, dev), _plain(new_len, 4, dev), B, table, stride,
+                                _plain(free_pages, 4, dev), free_pages.numel(), _plain(free_head, 4, dev),
+                                _plain(free_head_out, 4, dev), _plain(cu_seqlens, 4, dev), _plain(kv_len, 4, dev),
+                                _plain(slots, 4, dev), slots.numel(), _plain(dev_status, 4, dev),
+                                here if stream is None else _stream(stream))
 
 
 def _check_pool(cfg, pages, n_pages, page_size) -> None:
@@ -291,26 +301,28 @@ def _check_pool(cfg, pages, n_pages, page_size) -> None:
 
 def ft_kv_append_paged_int4(cfg, pages, n_pages, page_size, k, v, slots, total, dev_status=None, stream=None) -> int:
     """k, v: BF16 [>= total, n_kv, d], rows at any stride; slots: int32 [>= total]."""
-    here = _check_device(pages, k, v, slots, dev_status)
+    dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
     if min(k.shape[0], v.shape[0], slots.numel()) < total:
         raise ValueError(f"fewer than {total} rows or slots")
     row = cfg.n_kv * cfg.head_dim
-    kp, ks = _rows(k, row, 2)
-    vp, vs = _rows(v, row, 2)
-    return lib().ft_kv_append_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, kp, ks, vp, vs,
-                                         _plain(slots, 4), total, _ptr(dev_status), here if stream is None else _stream(stream))
+    kp, ks = _rows(k, row, 2, dev)
+    vp, vs = _rows(v, row, 2, dev)
+    return lib().ft_kv_append_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size, kp, ks, vp, vs,
+                                         _plain(slots, 4, dev), total, _plain(dev_status, 4, dev),
+                                         here if stream is None else _stream(stream))
 
 
 def ft_kv_read_paged_int4(cfg, pages, n_pages, page_size, slots, total, k_out, v_out, dev_status=None,
                           stream=None) -> int:
     """k_out, v_out: BF16 [>= total, n_kv, d], contiguous; slots: int32 [>= total]."""
-    here = _check_device(pages, slots, k_out, v_out, dev_status)
+    dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
     if min(k_out.numel(), v_out.numel()) < total * cfg.n_kv * cfg.head_dim or slots.numel() < total:
         raise ValueError(f"fewer than {total} rows or slots")
-    return lib().ft_kv_read_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, _plain(slots, 4), total,
-                                       _plain(k_out, 2), _plain(v_out, 2), _ptr(dev_status), here if stream is None else _stream(stream))
+    return lib().ft_kv_read_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size,
+                                       _plain(slots, 4, dev), total, _plain(k_out, 2, dev), _plain(v_out, 2, dev),
+                                       _plain(dev_status, 4, dev), here if stream is None else _stream(stream))
 
 
 def ft_attn_paged_workspace_bytes(cfg, B: int, total_q: int, max_q: int) -> int:
@@ -320,18 +332,18 @@ def ft_attn_paged_workspace_bytes(cfg, B: int, total_q: int, max_q: int) -> int:
 def ft_attn_paged_int4(cfg, pages, n_pages, page_size, q, cu_seqlens, kv_len, block_table, B, total_q, max_q, scale, o,
                        workspace, dev_status=None, stream=None) -> int:
     """q, o: BF16 [>= total_q, n_q, d], rows at any stride; block_table: int32 [>= B, pages of a request]."""
-    here = _check_device(pages, q, cu_seqlens, kv_len, block_table, o, workspace, dev_status)
+    dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
     if min(q.shape[0], o.shape[0]) < total_q or min(cu_seqlens.numel() - 1, kv_len.numel(), block_table.shape[0]) < B:
         raise ValueError(f"fewer than {total_q} rows or {B} requests")
-    row = cfg.n_q * cfg.head_dim
-    qp, qs = _rows(q, row, 2)
-    op, os_ = _rows(o, row, 2)
-    table, stride = _rows(block_table, block_table.shape[1], 4)
-    return lib().ft_attn_paged_int4(ctypes.byref(cfg), _plain(pages, 1), n_pages, page_size, qp, qs,
-                                    _plain(cu_seqlens, 4), _plain(kv_len, 4), table, stride, B, total_q, max_q, scale,
-                                    op, os_, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _ptr(dev_status), here if stream is None else _stream(stream))
+    row, size = cfg.n_q * cfg.head_dim, workspace.element_size()
+    qp, qs = _rows(q, row, 2, dev)
+    op, os_ = _rows(o, row, 2, dev)
+    table, stride = _rows(block_table, block_table.shape[1], 4, dev)
+    return lib().ft_attn_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size, qp, qs,
+                                    _plain(cu_seqlens, 4, dev), _plain(kv_len, 4, dev), table, stride, B, total_q,
+                                    max_q, scale, op, os_, _plain(workspace, size, dev), workspace.numel() * size,
+                                    _plain(dev_status, 4, dev), here if stream is None else _stream(stream))
 
 
 def ft_decode_workspace_bytes(cfg, B: int, max_ctx: int) -> int:
@@ -392,15 +404,16 @@ def ft_rmsnorm_bf16(x, gamma, z, B, H, eps, stream=None) -> int:
 def ft_logprobs(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, top_k, dev_status=None,
                 stream=None) -> int:
     """logits: FP32 or BF16 [N, V], rows at any stride; targets: int32 [N] or None; outputs may be None."""
-    here = _check_device(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev_status)
+    dev, here = _current()
     n, v = logits.shape
     dtype = FT_F32 if logits.element_size() == 4 else FT_BF16
-    x, stride = _rows(logits, v, 4 if dtype == FT_F32 else 2)
+    x, stride = _rows(logits, v, 4 if dtype == FT_F32 else 2, dev)
     for t, size in ((targets, n), (logprob, n), (entropy, n), (rank, n), (top_ids, n * top_k), (top_logprobs, n * top_k)):
         if t is not None and t.numel() < size:
             raise ValueError(f"an argument holds {t.numel()} of {size} elements")
-    return lib().ft_logprobs(x, dtype, stride, n, v, _plain(targets, 4), top_k, _plain(logprob, 4), _plain(entropy, 4),
-                             _plain(rank, 4), _plain(top_ids, 4), _plain(top_logprobs, 4), _ptr(dev_status),
+    return lib().ft_logprobs(x, dtype, stride, n, v, _plain(targets, 4, dev), top_k, _plain(logprob, 4, dev),
+                             _plain(entropy, 4, dev), _plain(rank, 4, dev), _plain(top_ids, 4, dev),
+                             _plain(top_logprobs, 4, dev), _plain(dev_status, 4, dev),
                              here if stream is None else _stream(stream))
 
 

@@ -761,11 +761,13 @@ def test_binding_refuses_what_it_cannot_pass():
     call = lambda q=a.q, kv=_i32([10]), pool=a.pool, out=o: ft.ft_attn_paged_int4(  # noqa: E731
         a.cfg, pool, a.n_pages, 64, q, _i32([0, 3]), kv, _i32(a.table), 1, 3, 3, 0.1, out, ws)
     assert call() == ft.FT_OK
-    for bad in (dict(q=a.q.cpu()), dict(q=a.q.float()), dict(q=a.q.transpose(1, 2)), dict(kv=_i32([10]).long()), dict(q=a.q[:2]),
+    for bad in (dict(q=a.q.cpu()), dict(q=a.q.float()), dict(q=a.q.half()), dict(out=o.half()), dict(q=a.q.transpose(1, 2)), dict(kv=_i32([10]).long()), dict(q=a.q[:2]),
                 dict(pool=a.pool[:-1]), dict(out=o[:, :, ::2]), dict(kv=torch.tensor([10], dtype=torch.int32))):
         with pytest.raises(ValueError):
             call(**bad)
     x = torch.randn((2, 50), device="cuda")
+    with pytest.raises(ValueError):
+        ft.ft_logprobs(x.half(), _i32([0, 0]), torch.zeros(2, device="cuda"), None, None, None, None, 0)
     with pytest.raises(ValueError):
         ft.ft_logprobs(x[:, ::2], _i32([0, 0]), None, None, _i32([0, 0]), None, None, 0)
     with pytest.raises(ValueError):
