@@ -29,7 +29,7 @@
 // tensor core works for 2048 and half of the issue slots are used.  The softmax takes 1500 of the
 // chain, so what the issuing warp waits for between P and the next S counts in full: it looks at K and
 // V before P is there and commits nothing that another commit says too.  Measured (32 heads over 8 of
-// 128): 2 x 2048 tokens over 4096 positions 218 us (945 TFLOP/s), 8192 over 32768 1270 TFLOP/s.
+// 128): 2 x 2048 tokens over 4096 positions 220 us (935 TFLOP/s), 8192 over 32768 1265 TFLOP/s.
 // No faster: P through shared memory, so that the next S need not wait for P V; P V in two halves;
 // half tiles with two S by turns (a product with 64 columns takes as long as with 128); two threads a
 // row; a second issuing warp; eight decoding warps; decoding left out altogether (3.2 ms, not 3.1, for
