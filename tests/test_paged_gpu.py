@@ -461,6 +461,40 @@ def test_attention_of_many_requests(B, n_q, n_kv, d, ps, new, top):
     a.check(o)
 
 
+@pytest.mark.parametrize("had", [1, 2, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("n,d", [(1, 128), (40, 128), (40, 64)])
+def test_attention_rotations_of_every_size(n, d, had):
+    a = Attn(8, 2, d, 32, [n, 1], [n + 77, 130], had=had)
+    o, st = a.run()
+    assert st == 0
+    a.check(o)
+
+
+@pytest.mark.parametrize("qlens,kvlens", [([1, 1], [700, 33]), ([3, 1], [260, 1])])
+def test_attention_groups_past_the_librarys_limit_are_refused(qlens, kvlens):
+    """64 query heads of one KV head: no configuration of this library (at most eight)."""
+    a = Attn(64, 1, 128, 64, qlens, kvlens)
+    with pytest.raises(ft.FTError):
+        a.run(ws=torch.empty(1 << 24, dtype=torch.uint8, device="cuda"))
+    assert ft.ft_attn_paged_workspace_bytes(a.cfg, 2, a.total, max(qlens)) == 0
+
+
+@pytest.mark.parametrize("qlens", [[1, 2, 1], [90, 2, 40]])
+@pytest.mark.parametrize("off", [1, 4])
+def test_attention_rows_at_odd_addresses(qlens, off):
+    """Rows of q and o that start at no 16-byte boundary, and leave gaps that stay as they were."""
+    a = Attn(8, 2, 128, 16, qlens, [100, 50, 333])
+    want, _ = a.run()
+    row = 8 * 128 + 3
+    qb, ob = (torch.full((off + (a.total + 2) * row,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    view = lambda t: torch.as_strided(t, (a.total + 2, 8, 128), (row, 128, 1), off)  # noqa: E731
+    view(qb).copy_(a.q)
+    o, st = a.run(q=view(qb), o=view(ob))
+    assert st == 0 and torch.equal(o[:a.total], want[:a.total])
+    view(ob)[:a.total] = 7.0
+    assert (ob == 7.0).all()
+
+
 def test_attention_in_parts_over_q_in_place():
     """Rows over a long cache, in parts that a second kernel joins, beside short requests, written over q."""
     a = Attn(16, 2, 128, 64, [40, 3, 0, 17], [5000, 3, 70, 40])
