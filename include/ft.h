@@ -257,17 +257,19 @@ int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_page
  * B n_kv (table_stride page_size / 64 + 6) < 2^31, else FT_ERR_UNSUPPORTED.
  * Arithmetic: q rounded to FP16 after the rotation (|q scale log2(e)| < 1023, else
  * FT_DEV_RANGE), codes exact, softmax weights rounded to FP16 below the products,
- * sums and statistics in FP32.  V scales from 2^-100 to 2^60 are weighed against each
+ * sums and statistics in FP32 (with many rows, below, the sums over positions enter
+ * the rotation back as two BF16 numbers each, 2^-17).  V scales from 2^-100 to 2^60 are weighed against each
  * other without loss (smaller ones count as 2^-100; an entry whose scale is 0 has no
  * values, only a weight).  With more than 32 rows (tokens x heads of a group) K and V
  * are decoded to FP16 in groups of 32 positions, and scales less than 2^-15 of their
  * group's largest are rounded.  Entries behind a token's position may hold anything
- * else; one whose scales are not finite spoils only the rows that see it.  What a request's rows are does not
- * depend on the other requests of the call, up to the order of FP32 sums.
+ * else; one whose scales are not finite spoils only the rows that see it.  What a
+ * request's rows are does not depend on the other requests of the call, up to the
+ * order of FP32 sums and the kernel that max_q picks.
  * Device conditions: cu_seqlens not ascending within [0, total_q], or n_b > max_q:
  * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative,
- * longer than table_stride pages or above 2^31 - 257: FT_DEV_CAPACITY, zeros; a page outside the pool:
- * FT_DEV_RANGE, its positions count as masked.
+ * longer than table_stride pages or above 2^31 - 257: FT_DEV_CAPACITY, zeros; a
+ * page outside the pool: FT_DEV_RANGE, its positions count as masked.
  * The workspace (16-byte aligned) holds partial results during the call only; calls
  * that may run at the same time need one each. */
 size_t ft_attn_paged_workspace_bytes(const ft_block_cfg *cfg, int B, int total_q, int max_q);

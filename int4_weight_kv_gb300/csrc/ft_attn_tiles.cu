@@ -14,9 +14,9 @@
 // Scales are multiplied into the operands, relative to a power of two per 32 positions:
 // a scale has 8 significant bits and a code 3, so the product is exact in FP16 down to 2^-8
 // of that power; where a group has smaller scales its operands are made 2^8 times larger (one
-// more product a word, in such groups only) and are exact down to 2^-16.  The groups' powers of two, kf for K and 2^f for V, come
-// back as one factor and one term of each score, t = S kf + f: P = 2^(t - m) weighs V's
-// operand, and the sum of weights takes 2^-f per group.  (Scales applied per column in the
+// more product a word, in such groups only) and are exact down to 2^-16.  The groups' powers of
+// two, kf for K and 2^f for V, come back as one factor and one term of each score, t = S kf + f:
+// P = 2^(t - m) weighs V's operand, and the sum of weights takes 2^-f per group.  (Scales applied per column in the
 // softmax needed 96 broadcast 16-byte reads a row and tile, 49 KB of shared-memory bandwidth
 // a warp: 5500 cycles per pair of tiles.)
 //
@@ -62,7 +62,6 @@ static_assert(2 * kRegSoftmax + kRegDecode + kRegIssue <= 4 * 128, "more registe
 
 template <int D>
 struct Cfg {
-  static constexpr int kPanels = D / 64;                 // 128-byte-wide panels of Q and K rows
   static constexpr int kQ = 128 * D * 2;                 // one tile's query operand
   static constexpr int kK = kKeys * D * 2, kV = kKeys * D * 2;  // one stage
   static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffH = kOffV + 2 * kV;
