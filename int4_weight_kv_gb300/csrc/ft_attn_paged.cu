@@ -22,7 +22,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 // weigh alike: 32 requests of 4096 positions took 38.9 us, 35.5 without the arithmetic, 34.6
 // without the loads.  What a share costs before its first tile (lengths, pages, first tiles, the
 // rotated queries: about 4 us) and the joining kernel (2 us) come on top.  Measured with 32 heads
-// over 8 of 128: one request of 1025 positions 9.7 us, 32 of up to 4097 26 us (2.8 TB/s); 64 heads,
+// over 8 of 128: one request of 1025 positions 8.6 us, 32 of up to 4097 26 us (2.8 TB/s); 64 heads,
 // 8 of up to 32769 35 us (3.6 TB/s).
 //
 // The work is the list of (request, head, 64 positions) units in this order; each CTA takes
@@ -409,12 +409,12 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
   }
 }
 
-// Joins the partials of the (request, head) pairs that several CTAs shared, one warp
+// Joins the partials of the (request, head) pairs that several CTAs shared, W = 1 or 4 warps
 // per row, in the order of the shares.
-template <int D, int NT>
+template <int D, int NT, int W>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnPagedParams p, const SplitWs ws, int ctas) {
-  constexpr int PW = D + 4, rb = 2 * NT;
-  const int r = 4 * (blockIdx.x % rb) + (threadIdx.x >> 5), bh = blockIdx.x / rb, h = bh % p.L.nkv, b = bh / p.L.nkv;
+  constexpr int PW = D + 4, rb = 2 * NT * W;  // CTAs of a pair
+  const int r = W == 1 ? 4 * (blockIdx.x % rb) + (threadIdx.x >> 5) : blockIdx.x % rb, bh = blockIdx.x / rb, h = bh % p.L.nkv, b = bh / p.L.nkv;
   const int row0 = p.cu[b], n = p.cu[b + 1] - row0;  // (not the few-rows kernel's: no need to wait)
   griddep_wait();
   const int first = __ldcg(ws.pref + b), next = __ldcg(ws.pref + b + 1), units = __ldcg(ws.pref + p.B);
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnPagedParams p,
   const int tok = r / p.G, hh = r - tok * p.G;
   // the first share's partial in its slot 1, the others' in their slot 0
   const float* base = ws.part + (size_t)r * PW;
-  join_row<D>(p, c1 - c0 + 1, [&](int i) { return base + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * (8 * NT * PW); }, kOUp,
+  join_row<D, W>(p, c1 - c0 + 1, [&](int i) { return base + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * (8 * NT * PW); }, kOUp,
               p.o + (row0 + tok) * p.o_stride + (int64_t)(h * p.G + hh) * D);
 }
 
@@ -461,7 +461,11 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.L.nkv * 2 * NT));
+  // Four warps a row where a pair may have more than twelve partials (a warp loads eight at once).
+  // Measured, one against four warps (us; 64 heads over 8): one request of 32768 positions 24.3 / 18.8,
+  // of 1024 10.1 / 9.1, four of 32768 37.3 / 35.9, eight 59.9 / 60.5; 32 of 4096 (32 heads) 37.7 / 40.0.
+  const bool wide = (int64_t)p.B * p.L.nkv * 12 < ctas;
+  cfg.gridDim = dim3((unsigned)(p.B * p.L.nkv * 2 * NT * (wide ? 4 : 1)));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -469,7 +473,7 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ft_host::pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT>, p, ws, ctas);
+  return cudaLaunchKernelEx(&cfg, wide ? attn_join_kernel<D, NT, 4> : attn_join_kernel<D, NT, 1>, p, ws, ctas);
 }
 
 

@@ -74,17 +74,18 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Joins n partials (max, sum, 2 unused, accumulator) of one row and stores it, a warp per row,
-// eight partials' loads in flight; row(i) is partial i, `up` the accumulators' factor.
-template <int D, typename Row>
+// Joins n partials (max, sum, 2 unused, accumulator) of one row and stores it, a warp (or a CTA of
+// W warps) per row, eight partials' loads in flight in each; row(i) is partial i, `up` the
+// accumulators' factor.
+template <int D, int W = 1, typename Row>
 __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row row, float up, uint16_t* dst) {
   constexpr int CH = D / 32, kBatch = 8;  // channels CH lane .. + CH - 1 of each lane
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(row(i)));
   M = warp_max(M);
   float lt = 0.0f, o[CH] = {};
-  for (int c = 0; c < n; c += kBatch) {
+  for (int c = kBatch * warp; c < n; c += kBatch * W) {
     float2 ml[kBatch];
     float x[kBatch][CH];
 #pragma unroll
@@ -107,6 +108,20 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
       lt = fmaf(f, ml[i].y, lt);
 #pragma unroll
       for (int k = 0; k < CH; ++k) o[k] = fmaf(f, x[i][k], o[k]);
+    }
+  }
+  if constexpr (W > 1) {  // the warps' sums, in their order
+    __shared__ float sums[W][D + 1];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) sums[warp][CH * lane + k] = o[k];
+    if (lane == 0) sums[warp][D] = lt;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      lt += sums[w][D];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) o[k] += sums[w][CH * lane + k];
     }
   }
   const float inv = lt == 0.0f ? 0.0f : up / lt;  // a row that sees nothing: zeros
