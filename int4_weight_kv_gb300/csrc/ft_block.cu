@@ -455,7 +455,10 @@ static int run_block(const ft_block_cfg* c, const ft_layer_weights* w, void* cac
     a.s_o = SF(P.s_o);
     a.status = status;
     rope_turns(c->rope_base, c->head_dim, a.rope_turn);
-    if (launch_attn(a, c->head_dim, st, pdl) != cudaSuccess) return FT_ERR_CUDA;
+    // Attention reads positions and history before it waits for its predecessor, which holds behind
+    // this call's QKV kernel (it starts nothing before it has waited itself).  Alone it may follow a
+    // kernel that still writes them (a page map that advances the positions in place): not overlapped.
+    if (launch_attn(a, c->head_dim, st, pdl && (mask & FT_STAGE_QKV)) != cudaSuccess) return FT_ERR_CUDA;
   }
   if (mask & FT_STAGE_O) {
     if (gemv(kRoleO, w->o, P.o_h, P.s_o) != cudaSuccess) return FT_ERR_CUDA;

@@ -1,0 +1,57 @@
+"""The paged cache and the log probabilities at the ends of their ranges: sizes next to
+2^31, entries without finite scales, scales far apart, calls that follow each other with
+nothing in between, and arguments of the wrong type.
+
+Tolerances are those of test_paged_gpu.py (derived there); anything else is exact.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+import int4_weight_kv_gb300 as ft
+from int4_weight_kv_gb300 import runtime as rt
+from tests import gpu_harness as H
+from tests.test_paged_gpu import _gpu, _i32  # noqa: F401 (_gpu: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- one call behind the other
+@pytest.mark.parametrize("B", [1, 20])
+def test_block_stage_behind_a_page_map_that_advances_its_positions(B):
+    """The attention stage reads the positions that a page map has just advanced."""
+    lay = H.make_layer(synth.TINY, 1)
+    pb = H.make_problem(lay, 1, B, 40, max_ctx=64)
+    x = torch.from_numpy(pb.x_f32).cuda()
+    y, new = torch.empty_like(x), _i32([1] * B)
+    table, free = _i32(np.full((B, 8), 0)), _i32(range(8 * B))
+    ws, pos, cu, slots, head = rt.alloc_workspace(lay.cfg, B, 64), _i32([0] * B), _i32([0] * (B + 1)), _i32([0] * B), _i32([0])
+    lo = ft.ft_decode_workspace_layout(lay.cfg, B, 64)
+    n = B * lay.shape.n_q * lay.shape.head_dim
+    args = lambda: (lay.cfg, lay.packed, cache, B, 64, x, y, ft.FT_F32, pos, B, ws)  # noqa: E731
+    res = []
+    for pdl in (0, 1):
+        was = ft.ft_set_pdl(pdl)
+        try:
+            for start in (0, 11, 30):
+                cache = pb.cache.clone()
+                pos.fill_(start)
+                ft.check(ft.ft_decode_block(*args(), None))
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    head.zero_()
+                    for _ in range(4):
+                        ft.check(ft.ft_kv_page_map(16, 8 * B, pos, new, B, table, free, head, head, cu, pos, slots))
+                        ft.check(ft.ft_decode_block_stages(*args(), ft.FT_STAGE_ATTN, None))
+                pos.fill_(start)
+                graph.replay()
+                torch.cuda.synchronize()
+                assert pos.tolist() == [start + 4] * B
+                res.append((ws[lo.o:lo.o + 2 * n].clone(), cache.clone()))
+        finally:
+            ft.ft_set_pdl(was)
+    for (o0, c0), (o1, c1) in zip(res[:3], res[3:]):
+        assert torch.equal(o0, o1) and torch.equal(c0, c1)
