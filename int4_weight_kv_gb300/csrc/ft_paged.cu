@@ -126,23 +126,24 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
     }
   }
   // page id of the free list's entry i, or -1 (and a flag) where it is no page
-  auto fresh = [&](int i) {
+  auto fresh = [&](int64_t i) {
     const int id = __ldg(p.free_pages + head + i);
     if (id >= 0 && id < p.n_pages) return id;
     set_status(p.status, FT_DEV_RANGE);
     return -1;
   };
-  for (int i = first; i < n_taken; i += step) {
-    const int b = last_not_above(pg, B, i);
+  // (indices of 64 bits: a step behind the last entry would pass 2^31 where there are nearly that many)
+  for (int64_t i = first; i < n_taken; i += step) {
+    const int b = last_not_above(pg, B, (int)i);
     const int old = (int)(((long long)ctx_s[b] + round) >> p.pshift);
     if (ctx_s[b] >= 0) p.table[(size_t)b * p.stride + old + (i - pg[b])] = fresh(i);
   }
-  for (int i0 = kMapRun * first; i0 < p.n_slots; i0 += kMapRun * step) {
+  for (int64_t i0 = kMapRun * first; i0 < p.n_slots; i0 += kMapRun * step) {
     int out[kMapRun], b = 0, last_ip = -1, id = -1;
-    if (i0 < total) b = last_not_above(cu, B, i0);
+    if (i0 < total) b = last_not_above(cu, B, (int)i0);
 #pragma unroll
     for (int k = 0; k < kMapRun; ++k) {
-      const int i = i0 + k;
+      const int64_t i = i0 + k;
       out[k] = -1;
       if (i >= total) continue;
       if (i >= cu[b + 1]) {
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
       }
       const int c = ctx_s[b];
       if (c < 0) continue;
-      const int pos = c + (i - cu[b]), ip = pos >> p.pshift;
+      const int pos = c + ((int)i - cu[b]), ip = pos >> p.pshift;
       if (ip != last_ip) {
         const int old = (int)(((long long)c + round) >> p.pshift);
         id = ip < old ? p.table[(size_t)b * p.stride + ip] : fresh(pg[b] + ip - old);

@@ -13,9 +13,48 @@ import synth
 import int4_weight_kv_gb300 as ft
 from int4_weight_kv_gb300 import runtime as rt
 from tests import gpu_harness as H
-from tests.test_paged_gpu import _gpu, _i32  # noqa: F401 (_gpu: a fixture)
+from tests.test_paged_gpu import _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- page map
+@pytest.mark.parametrize("alias", [False, True])
+def test_page_map_slots_up_to_2_to_31(alias):
+    """The slots behind the last row are -1 up to the largest slot map; nothing before it is touched."""
+    n, dev = 2 ** 31 - 1, "cuda"
+    buf = torch.full((n + 8192,), 77, dtype=torch.int32, device=dev)
+    slots = buf[8192:]
+    c, t, h, st, cu = _i32([30, 3]), _i32([[5, 6], [4, 4]]), _i32([0]), _status(), _i32([0] * 3)
+    kv, ho = (c, h) if alias else (_i32([0, 0]), _i32([0]))
+    ft.check(ft.ft_kv_page_map(16, 10, c, _i32([2, 4]), 2, t, _i32([9]), h, ho, cu, kv, slots, st))
+    assert ft.ft_read_device_status(st) == 0
+    assert cu.tolist() == [0, 2, 6] and kv.tolist() == [32, 7] and ho.tolist() == [0]
+    assert slots[:6].tolist() == [6 * 16 + 14, 6 * 16 + 15, 67, 68, 69, 70]
+    assert (buf[:8192] == 77).all()
+    for a in range(6, n, 1 << 28):
+        assert (slots[a:a + (1 << 28)] == -1).all()
+
+
+def test_page_map_takes_up_to_2_to_31_pages():
+    """Sixteen requests that fill their table rows from a free list of 2^31 - 1 entries."""
+    per, dev = 1 << 27, "cuda"
+    n_pages, n_free = (2 ** 31 - 1) // 16, 2 ** 31 - 1
+    free = torch.empty(n_free, dtype=torch.int32, device=dev)
+    for a in range(0, n_free, 1 << 28):
+        b = min(a + (1 << 28), n_free)
+        free[a:b] = (torch.arange(a, b, device=dev) % n_pages).to(torch.int32)
+    table = torch.full((16, per), -1, dtype=torch.int32, device=dev)
+    new = [2 ** 31 - 1] * 15 + [(per - 1) * 16]
+    kv, cu, ho, st, slots = _i32([0] * 16), _i32([0] * 17), _i32([0]), _status(), _i32([7] * 5)
+    ft.check(ft.ft_kv_page_map(16, n_pages, _i32([0] * 16), _i32(new), 16, table, free, None, ho, cu, kv, slots, st))
+    assert ft.ft_read_device_status(st) == ft.FT_DEV_RANGE      # more rows than slots
+    assert ho.tolist() == [n_free] and slots.tolist() == [0, 1, 2, 3, 4]
+    flat = table.view(-1)
+    assert flat[-1].item() == -1
+    for a in range(0, n_free, 1 << 28):
+        b = min(a + (1 << 28), n_free)
+        assert torch.equal(flat[a:b], free[a:b])
 
 
 # ---------------------------------------------------------------- one call behind the other
