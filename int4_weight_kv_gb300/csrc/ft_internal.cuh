@@ -42,7 +42,10 @@ __device__ __forceinline__ unsigned long long globaltimer() {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // The first thing that a kernel launched by launch_served does, in every thread: what ran before is
-// complete, and what comes next may take its places (it waits here in its turn).
+// complete, and what comes next may take its places (it waits here in its turn).  Such a kernel lives
+// while its predecessor still writes, so whatever that may have produced (lengths, slots, pages, rows,
+// logits) is not constant to it: ordinary or __ldcg loads, which stay behind this wait and see all that
+// was written before it, never __ldg or ld.global.nc.
 __device__ __forceinline__ void griddep_serve() {
   griddep_wait();
   griddep_launch();

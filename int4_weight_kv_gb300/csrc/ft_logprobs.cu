@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
   if (ctas > 1) cluster_arrive();  // paired with the wait before the first store to CTA 0
   const uint8_t* base = static_cast<const uint8_t*>(p.x) + row * p.stride * (BF16 ? 2 : 4);
   auto at = [&](int i) {
-    return BF16 ? bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i))
-                : __ldg(reinterpret_cast<const float*>(base) + i);
+    return BF16 ? bf16_bits_to_f32(__ldcg(reinterpret_cast<const uint16_t*>(base) + i))
+                : __ldcg(reinterpret_cast<const float*>(base) + i);
   };
-  const int t = p.target ? p.target[row] : -1;
+  const int t = p.target ? __ldcg(p.target + row) : -1;
   const bool has = t >= 0 && t < V;
   const float xt = has ? at(t) : INFINITY;  // without a target nothing is before it
   // vector v holds elements v E - lead .. + E - 1, 16-byte aligned; the first and the last may be partial
@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
       const int v = r + i * kLpThreads + tid;
       const int e0 = v * E - lead;
       if (r > 0 && r + U * kLpThreads < v1) {  // a round inside the row and the slice
-        q[i] = ld_stream_v4(vec0 + (size_t)v * 16);
+        q[i] = __ldcg(reinterpret_cast<const uint4*>(vec0) + v);
       } else if (v < v1 && e0 >= 0 && e0 + E <= V) {
-        q[i] = ld_stream_v4(vec0 + (size_t)v * 16);
+        q[i] = __ldcg(reinterpret_cast<const uint4*>(vec0) + v);
       } else {
         uint32_t w[4];
 #pragma unroll
@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
           for (int k = 0; k < E; ++k) {
             if (e0 + k < 0 || e0 + k >= V) continue;
             if (BF16) {
-              const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(base) + e0 + k);
+              const uint32_t h = __ldcg(reinterpret_cast<const uint16_t*>(base) + e0 + k);
               w[k / 2] = (k & 1) ? (w[k / 2] & 0xFFFFu) | (h << 16) : (w[k / 2] & 0xFFFF0000u) | h;
             } else {
-              w[k % 4] = __ldg(reinterpret_cast<const uint32_t*>(base) + e0 + k);
+              w[k % 4] = __ldcg(reinterpret_cast<const uint32_t*>(base) + e0 + k);
             }
           }
         }
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
           if (v < v1) {
             const bool inside = e0 >= 0 && e0 + E <= V;
             uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (inside) q = ld_stream_v4(vec0 + (size_t)v * 16);
+            if (inside) q = __ldcg(reinterpret_cast<const uint4*>(vec0) + v);
             const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < E; ++k) {

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   }
   // page id of the free list's entry i, or -1 (and a flag) where it is no page
   auto fresh = [&](int64_t i) {
-    const int id = __ldg(p.free_pages + head + i);
+    const int id = p.free_pages[head + i];
     if (id >= 0 && id < p.n_pages) return id;
     set_status(p.status, FT_DEV_RANGE);
     return -1;
@@ -206,7 +206,7 @@ __device__ __forceinline__ void paged_row(const PagedRows& p, int& t, int& h, in
   const int64_t row = (warp / p.L.nkv) * R + lane / LV;
   t = (int)min(row, (int64_t)p.total);
   j = lane % LV;
-  slot = t < p.total ? __ldg(p.slots + t) : -1;
+  slot = t < p.total ? __ldcg(p.slots + t) : -1;
 }
 // The slot, or -1 (and a flag) where it is none.
 __device__ __forceinline__ int paged_slot(const PagedRows& p, int slot, int j) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kRowThreads) append_paged_kernel(const PagedRo
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        const uint4 q = reinterpret_cast<const uint4*>(src)[i];
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kRowThreads) append_paged_kernel(const PagedRo
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = f32x2(bf16_bits_to_f32(__ldg(src + 2 * i)), bf16_bits_to_f32(__ldg(src + 2 * i + 1)));
+      for (int i = 0; i < 16; ++i) x[i] = f32x2(bf16_bits_to_f32(src[2 * i]), bf16_bits_to_f32(src[2 * i + 1]));
     }
   } else {
 #pragma unroll
@@ -392,14 +392,14 @@ __global__ void __launch_bounds__(kRowThreads) read_paged_kernel(const PagedRows
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (is_v) {
-        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q, j)));
-        const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q + 1, j)));
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q, j));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(blk + p.L.voff + paged_v_word<D>(pos & ~1, 2 * q + 1, j));
         w[q] = prmt(a, b, (pos & 1) ? 0x7632u : 0x5410u);
       } else {
-        w[q] = __ldg(reinterpret_cast<const uint32_t*>(blk + paged_k_word<D>(pos, 2 * q, j)));
+        w[q] = *reinterpret_cast<const uint32_t*>(blk + paged_k_word<D>(pos, 2 * q, j));
       }
     }
-    const uint32_t both = __ldg(reinterpret_cast<const uint32_t*>(blk + p.L.soff + 4 * pos));
+    const uint32_t both = *reinterpret_cast<const uint32_t*>(blk + p.L.soff + 4 * pos);
     s = __uint_as_float(is_v ? both & 0xFFFF0000u : both << 16);
   }
   // the decoded halves are x 2^-24 (e even) and x 2^-20

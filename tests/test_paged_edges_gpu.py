@@ -13,7 +13,7 @@ import synth
 import int4_weight_kv_gb300 as ft
 from int4_weight_kv_gb300 import runtime as rt
 from tests import gpu_harness as H
-from tests.test_paged_gpu import _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
+from tests.test_paged_gpu import _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,6 +58,66 @@ def test_page_map_takes_up_to_2_to_31_pages():
 
 
 # ---------------------------------------------------------------- one call behind the other
+def _chain(cfg, ps, n_kv, d, rows, V):
+    """Three times page map, placement, reading back and log probabilities of what was read, with nothing in between: the same
+    pages and the same slot map with other slots and other data each time.  The results of three replays and an eager run."""
+    g = torch.Generator("cuda").manual_seed(len(rows) + sum(rows))
+    B, total, dev = len(rows), sum(rows), "cuda"
+    need = [-(-n // ps) for n in rows]
+    n_pages = sum(need)
+    pool = torch.zeros(ft.ft_kv_pages_bytes(cfg, n_pages, ps), dtype=torch.uint8, device=dev)
+    free = torch.cat([torch.randperm(n_pages, device=dev, generator=g) for _ in range(3)]).to(torch.int32)
+    head, ctx0, new = _i32([0]), _i32([0] * B), _i32(rows)
+    table, cu, kv = _i32(np.full((B, max(need)), -1)), _i32([0] * (B + 1)), _i32([0] * B)
+    slots, st = _i32([0] * total), _status()
+    x = [torch.randn((total, 2 * n_kv, d), device=dev, generator=g).to(torch.bfloat16) for _ in range(3)]
+    t = _i32([i % V for i in range(total)])
+    f = lambda *s: torch.zeros(s, device=dev)  # noqa: E731
+    bf = lambda: torch.zeros((total, n_kv, d), dtype=torch.bfloat16, device=dev)  # noqa: E731
+    out = [[bf(), bf(), f(total), f(total), _i32([0] * total), _i32([[0] * 3] * total), f(total, 3)] for _ in range(3)]
+
+    def steps():
+        head.zero_()
+        for k in range(3):
+            ko, vo, lp, en, rank, ids, tv = out[k]
+            ft.check(ft.ft_kv_page_map(ps, n_pages, ctx0, new, B, table, free, head, head, cu, kv, slots, st))
+            ft.check(ft.ft_kv_append_paged_int4(cfg, pool, n_pages, ps, x[k][:, :n_kv], x[k][:, n_kv:], slots, total, st))
+            ft.check(ft.ft_kv_read_paged_int4(cfg, pool, n_pages, ps, slots, total, ko, vo, st))
+            ft.check(ft.ft_logprobs(ko.view(total, V), t, lp, en, rank, ids, tv, 3, st))
+
+    steps()
+    torch.cuda.synchronize()
+    res = [[y.clone() for s in out for y in s]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(3):
+        pool.fill_(0xFF)
+        for y in [slots] + [y for s in out for y in s]:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        res.append([y.clone() for s in out for y in s])
+    assert st.item() == 0 and head.item() == 3 * n_pages
+    return res
+
+
+@pytest.mark.parametrize("rows,n_kv,d,ps", [([1] * 32, 8, 128, 64), ([1], 2, 64, 16), ([300, 1, 77, 2000], 8, 128, 32),
+                                            ([5, 64, 700], 4, 64, 16)])
+def test_calls_behind_each_other_with_and_without_overlap(rows, n_kv, d, ps):
+    cfg = _cfg(n_kv, n_kv, d)
+    was = ft.ft_set_pdl(0)
+    try:
+        want = _chain(cfg, ps, n_kv, d, rows, n_kv * d)
+        ft.ft_set_pdl(1)
+        got = _chain(cfg, ps, n_kv, d, rows, n_kv * d)
+    finally:
+        ft.ft_set_pdl(was)
+    for r in want[1:] + got:
+        for x, y in zip(want[0], r):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("B", [1, 20])
 def test_block_stage_behind_a_page_map_that_advances_its_positions(B):
     """The attention stage reads the positions that a page map has just advanced."""
