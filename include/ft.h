@@ -209,8 +209,8 @@ size_t ft_kv_pages_bytes(const ft_block_cfg *cfg, int n_pages, int page_size);
  *   free_pages: int32 [n_free]; the pages added are free_pages[head], head + 1,
  *     ... in request order, with head = *free_head (NULL: 0).
  *   free_head_out: int32, head + pages taken (NULL: not written).
- *   cu_seqlens: int32 [B + 1], prefix sums of new_len.  kv_len: int32 [B],
- *     ctx_len + new_len.
+ *   cu_seqlens: int32 [B + 1], prefix sums of new_len (2^31 - 1 where they pass
+ *     that).  kv_len: int32 [B], ctx_len + new_len.
  *   slots: int32 [n_slots]; slot of row i (request b, position ctx_len[b] + i -
  *     cu_seqlens[b]); -1 for rows behind the last one.
  * kv_len may be ctx_len and free_head_out may be free_head (advanced in place);

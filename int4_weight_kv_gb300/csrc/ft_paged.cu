@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   const int first = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
   if (blockIdx.x == 0) {
     for (int b = tid; b <= B; b += kMapThreads) p.cu[b] = cu[b];
-    for (int b = tid; b < B; b += kMapThreads) p.kv_len[b] = ctx_s[b] < 0 ? 0 : ctx_s[b] + (cu[b + 1] - cu[b]);
+    for (int b = tid; b < B; b += kMapThreads)  // (not from cu, whose sums end at 2^31 - 1)
+      p.kv_len[b] = ctx_s[b] < 0 ? 0 : ctx_s[b] + (b == b0 ? a0 : p.add[b]);
     if (tid == 0) {
       if (p.head_out) *p.head_out = head + n_taken;
       int flags = bad;

@@ -57,6 +57,21 @@ def test_page_map_takes_up_to_2_to_31_pages():
         assert torch.equal(flat[a:b], free[a:b])
 
 
+@pytest.mark.parametrize("alias", [False, True])
+def test_lengths_of_more_rows_than_2_to_31(alias):
+    """kv_len is ctx_len + new_len also where the prefix sums end at 2^31 - 1."""
+    ctx, new = [5, 100, 0, 7], [2 ** 30] * 3 + [0]
+    width = 2 ** 23 + 1
+    free = torch.zeros(3 * width, dtype=torch.int32, device="cuda")
+    table = torch.zeros((4, width), dtype=torch.int32, device="cuda")
+    c, cu, st = _i32(ctx), _i32([0] * 5), _status()
+    kv = c if alias else _i32([0] * 4)
+    ft.check(ft.ft_kv_page_map(128, 3, c, _i32(new), 4, table, free, None, None, cu, kv, _i32([7] * 5), st))
+    assert ft.ft_read_device_status(st) == ft.FT_DEV_RANGE
+    assert cu.tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
+    assert kv.tolist() == [c + n for c, n in zip(ctx, new)]
+
+
 # ---------------------------------------------------------------- one call behind the other
 def _chain(cfg, ps, n_kv, d, rows, V):
     """Three times page map, placement, reading back and log probabilities of what was read, with nothing in between: the same
