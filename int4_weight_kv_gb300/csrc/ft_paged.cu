@@ -481,7 +481,8 @@ int ft_kv_page_map(int page_size, int n_pages, const int32_t* ctx_len, const int
   static int attr_smem[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FT_ERR_CUDA;
-  if (smem > 48 * 1024 && attr_smem[dev] < smem) {
+  // (without the attribute 48 KB hold the kernel's static variables too)
+  if (smem > 48 * 1024 - 1024 && attr_smem[dev] < smem) {
     const int most = (3 * ft::kMapMaxB + 2) * 4;
     if (cudaFuncSetAttribute(ft::page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
       return FT_ERR_CUDA;

@@ -4,6 +4,9 @@ nothing in between, and arguments of the wrong type.
 
 Tolerances are those of test_paged_gpu.py (derived there); anything else is exact.
 """
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -70,6 +73,24 @@ def test_lengths_of_more_rows_than_2_to_31(alias):
     assert ft.ft_read_device_status(st) == ft.FT_DEV_RANGE
     assert cu.tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
     assert kv.tolist() == [c + n for c, n in zip(ctx, new)]
+
+
+def test_page_map_of_every_batch_size_in_a_fresh_process():
+    """Batches around the limits of shared memory, the first of them in a process that has launched nothing else."""
+    code = """
+import torch, int4_weight_kv_gb300 as ft
+i = lambda n: torch.zeros(n, dtype=torch.int32, device='cuda')
+for B in (4095, 4070, 4083, 4084, 4090, 4096, 4097, 8191, 8192):
+    table, slots, kv = i((B, 1)) - 1, i(B), i(B)
+    st = i(1)
+    free = torch.arange(B, dtype=torch.int32, device='cuda')
+    ft.check(ft.ft_kv_page_map(16, B, i(B), i(B) + 1, B, table, free, None, None, i(B + 1), kv, slots, st))
+    assert ft.ft_read_device_status(st) == 0
+    assert torch.equal(slots, 16 * free) and (kv == 1).all() and torch.equal(table[:, 0], free)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- one call behind the other
