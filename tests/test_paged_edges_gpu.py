@@ -12,11 +12,13 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import synth
 import int4_weight_kv_gb300 as ft
 from int4_weight_kv_gb300 import runtime as rt
+from oracle import paged
 from tests import gpu_harness as H
-from tests.test_paged_gpu import _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
+from tests.test_paged_gpu import _bf16, _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +192,29 @@ def test_block_stage_behind_a_page_map_that_advances_its_positions(B):
             ft.ft_set_pdl(was)
     for (o0, c0), (o1, c1) in zip(res[:3], res[3:]):
         assert torch.equal(o0, o1) and torch.equal(c0, c1)
+
+
+# ---------------------------------------------------------------- entries at the ends of their range
+@pytest.mark.parametrize("up", [30, 104, 110, 118])
+@pytest.mark.parametrize("n_kv,d,had", [(8, 128, 0), (2, 64, 0), (2, 128, 1), (2, 64, 16)])
+def test_rows_of_every_size_are_read_back(n_kv, d, had, up):
+    """Rows around 2^up and 2^-up: as their codes and scales say, rotated back (scales reach 2^118 and 2^-121)."""
+    cfg, g = _cfg(n_kv, n_kv, d, had), np.random.default_rng(up)
+    x, xf = _bf16(g, 20, 2 * n_kv, d)
+    size = torch.tensor([2.0 ** (up if i % 2 else -up) for i in range(20)], device="cuda").view(-1, 1, 1)
+    x = (x.float() * size).to(torch.bfloat16)
+    pool = torch.zeros(ft.ft_kv_pages_bytes(cfg, 2, 16), dtype=torch.uint8, device="cuda")
+    st, sl = _status(), _i32(range(20))
+    ft.check(ft.ft_kv_append_paged_int4(cfg, pool, 2, 16, x[:, :n_kv], x[:, n_kv:], sl, 20, st))
+    out = [torch.zeros((20, n_kv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ft.check(ft.ft_kv_read_paged_int4(cfg, pool, 2, 16, sl, 20, *out, st))
+    assert ft.ft_read_device_status(st) == 0
+    codes = paged.unpack_pages(pool.cpu().numpy(), n_kv, 16, d)
+    for c, s, o in ((codes[0], codes[2], out[0]), (codes[1], codes[3], out[1])):
+        c, s = c.transpose(0, 2, 1, 3).reshape(32, n_kv, d)[:20], s.transpose(0, 2, 1).reshape(32, n_kv)[:20]
+        back = oracle.blockdiag_apply(c * s[..., None], had or d)
+        got = o.float().cpu().numpy().astype(np.float64)
+        # as in test_append_codes_and_read: FP32 additions (2^-20 of the row's norm), then half a BF16 step; values
+        # below FP32's smallest normal number lose up to 2^-126 each
+        tol = 2.0 ** -8 * np.abs(back) + 2.0 ** -20 * np.linalg.norm(back, axis=-1, keepdims=True) + d * 2.0 ** -126
+        assert np.isfinite(got).all() and np.all(np.abs(got - back) <= tol)
