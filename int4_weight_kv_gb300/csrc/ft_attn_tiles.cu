@@ -625,9 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
     for (int j = 0; j < nkt; ++j) {
       const int st = j & 1;
-      // an entry without finite scales (its own row was not finite) must not reach its neighbours, nor
-      // the rows that do not see it: it counts as masked
-      if (((sc >> 7) & 0xFFu) == 0xFFu || ((sc >> 23) & 0xFFu) == 0xFFu) sc = 0u, there = false;
+      // An entry without finite scales (its own row was not finite) makes the rows that see it NaN, but must not
+      // reach its neighbours, nor the rows that do not see it: its K operand is NaN, which is one column of S,
+      // masked like any other, and its V operand is 0.
+      const bool poor = ((sc >> 7) & 0xFFu) == 0xFFu || ((sc >> 23) & 0xFFu) == 0xFFu;
+      if (poor) sc = 0u;
       // the 32 positions' scales relative to their largest's power of two, as multipliers of the
       // decoded words (codes x 2^-24 and, for odd values, x 2^-20): code x (scale / 2^e) x 2^-9,
       // or x 2^-1 where a scale's exponent is more than 7 below the largest's
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       const bool wide_k = __any_sync(0xffffffffu, xk != 0u && xk + 7u < ek);
       const bool wide_v = __any_sync(0xffffffffu, xv != 0u && xv + 7u < ev);
       ek = max(ek, 27u), ev = ev == 0u ? kNoScaleExp : max(ev, 27u);
-      const float mk = __uint_as_float(sc << 16) * __uint_as_float((268u - ek) << 23);
+      const float mk = poor ? __uint_as_float(0x7FC00000u) : __uint_as_float(sc << 16) * __uint_as_float((268u - ek) << 23);
       const float mv = __uint_as_float(sc & 0xFFFF0000u) * __uint_as_float((268u - ev) << 23);
       const __half2 mk2 = __floats2half2_rn(mk, mk * 0.0625f);  // (even, odd values)
       const uint32_t mku = *reinterpret_cast<const uint32_t*>(&mk2);

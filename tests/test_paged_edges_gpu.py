@@ -18,7 +18,7 @@ import int4_weight_kv_gb300 as ft
 from int4_weight_kv_gb300 import runtime as rt
 from oracle import paged
 from tests import gpu_harness as H
-from tests.test_paged_gpu import _bf16, _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
+from tests.test_paged_gpu import Attn, _bf16, _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -195,6 +195,30 @@ def test_block_stage_behind_a_page_map_that_advances_its_positions(B):
 
 
 # ---------------------------------------------------------------- entries at the ends of their range
+BAD = [float("nan"), float("inf")]
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("n,kv,d", [(1, 50, 128), (1, 9000, 128), (4, 70, 64), (8, 300, 128), (200, 260, 128), (200, 260, 64),
+                                    (40, 6000, 128)])
+def test_rows_that_see_an_entry_without_finite_scales_are_nan(n, kv, d, bad, which):
+    """NaN in every channel of the rows at and after the entry, whichever kernel serves them and whichever scale it is; the
+    rows before it and the other requests as without it."""
+    a = Attn(16, 2, d, 64, [n, n], [kv, kv])
+    want, _ = a.run()
+    for at in sorted({kv - n + n // 2, kv - 1, kv // 3}):       # among the new tokens, the last, in the history
+        keep = a.pool_np.copy()
+        a.set_scales(0, [at], **{which: bad})
+        o, _ = a.run()
+        first = max(0, at - (kv - n))
+        assert torch.isnan(o[first:n]).all(), at
+        assert torch.equal(o[n:], want[n:])
+        a.pool_np[:] = keep
+        err = (o[:first].float() - want[:first].float()).norm(dim=-1)
+        assert (err <= 2.0 ** -7 * want[:first].float().norm(dim=-1) + 1e-6).all()
+
+
 @pytest.mark.parametrize("up", [30, 104, 110, 118])
 @pytest.mark.parametrize("n_kv,d,had", [(8, 128, 0), (2, 64, 0), (2, 128, 1), (2, 64, 16)])
 def test_rows_of_every_size_are_read_back(n_kv, d, had, up):
