@@ -263,8 +263,9 @@ int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_page
  * values, only a weight).  With more than 32 rows (tokens x heads of a group) K and V
  * are decoded to FP16 in groups of 32 positions, and scales less than 2^-15 of their
  * group's largest are rounded.  Entries behind a token's position may hold anything
- * else; a row that sees one whose scales are not finite is NaN, no other is touched.  What a
- * request's rows are does not depend on the other requests of the call, up to the
+ * else; a row that sees one with a scale that is not finite, or 2^110 and more, is NaN
+ * (none is for scales below 2^109), and no other row is touched.  What a request's rows
+ * are does not depend on the other requests of the call, up to the
  * order of FP32 sums and the kernel that max_q picks.
  * Device conditions: cu_seqlens not ascending within [0, total_q], or n_b > max_q:
  * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative,

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
       const float ks0 = __uint_as_float(sc0 << 16) * kKsUp, ks1 = __uint_as_float(sc1 << 16) * kKsUp;
       const float v0 = __uint_as_float(sc0 & 0xFFFF0000u), v1 = __uint_as_float(sc1 & 0xFFFF0000u);
       const float vs0 = v0 == 0.0f ? kNoScale : fmaxf(v0, kMinScale), vs1 = v1 == 0.0f ? kNoScale : fmaxf(v1, kMinScale);
-      // (a scale that is not finite makes this and with it the scores NaN, whatever they were)
+      // (a scale from 2^110 on, kTooLarge, makes this and with it the scores NaN, whatever they were)
       const float lv0 = fmaf(fmaf(v0, kKsUp, ks0), 0.0f, lg2(vs0)), lv1 = fmaf(fmaf(v1, kKsUp, ks1), 0.0f, lg2(vs1));
       float rs0 = rcp(vs0), rs1 = rcp(vs1);
 #pragma unroll

@@ -19,6 +19,9 @@ constexpr float kOUp = 16777216.0f;           // 2^24
 constexpr float kPBias = 10.0f;               // P = 2^(t - m + 10): FP16 normals down to 2^-24 of the largest weight
 constexpr float kPLazy = 4.0f;                // the running max moves when a score passes it by 2^4 (P < 2^14 + rounding)
 constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: smaller V scales count as this (their values are ~0)
+// Scales from here on (2^110, as BF16 bits) make a row that sees them NaN, as those that are not finite
+// do: past them the factors of scores and sums of weights leave FP32.
+constexpr uint32_t kTooLarge = 0x7680u;
 // An entry whose V is zero (scale 0) weighs in the sum of weights alone, with lv = -60: that weight
 // and those of values between 2^-70 and 2^70 stay within FP32's (and P's) range beside each other.
 constexpr uint32_t kNoScaleExp = 67u;           // exponent of 2^-60

@@ -625,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
     for (int j = 0; j < nkt; ++j) {
       const int st = j & 1;
-      // An entry without finite scales (its own row was not finite) makes the rows that see it NaN, but must not
+      // An entry with a scale from 2^110 on (its own row was not finite) makes the rows that see it NaN, but must not
       // reach its neighbours, nor the rows that do not see it: its K operand is NaN, which is one column of S,
       // masked like any other, and its V operand is 0.
-      const bool poor = ((sc >> 7) & 0xFFu) == 0xFFu || ((sc >> 23) & 0xFFu) == 0xFFu;
+      const bool poor = (sc & 0x7FFFu) >= kTooLarge || ((sc >> 16) & 0x7FFFu) >= kTooLarge;
       if (poor) sc = 0u;
       // the 32 positions' scales relative to their largest's power of two, as multipliers of the
       // decoded words (codes x 2^-24 and, for odd values, x 2^-20): code x (scale / 2^e) x 2^-9,
@@ -653,9 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
       if (lane == 0) {
         float* dst = reinterpret_cast<float*>(scales + 4 * (j % kScaleRing)) + w4;
         const uint32_t tv = wide_v ? ev - 8u : ev;
-        dst[0] = __uint_as_float((wide_k ? ek - 4u : min(ek + 4u, 254u)) << 23);  // 2^(e + 9) / kQUp (or 2^-8 of it), e = ek - 126
+        dst[0] = __uint_as_float((wide_k ? ek - 4u : ek + 4u) << 23);  // 2^(e + 9) / kQUp (or 2^-8 of it), e = ek - 126
         dst[4] = (float)((int)tv - 126);
-        dst[8] = __uint_as_float((tv > 252u ? 1u : 253u - tv) << 23);
+        dst[8] = __uint_as_float((253u - tv) << 23);
         dst[12] = __uint_as_float(exist);
       }
       {

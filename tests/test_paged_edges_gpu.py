@@ -219,6 +219,29 @@ def test_rows_that_see_an_entry_without_finite_scales_are_nan(n, kv, d, bad, whi
         assert (err <= 2.0 ** -7 * want[:first].float().norm(dim=-1) + 1e-6).all()
 
 
+@pytest.mark.parametrize("n,kv", [(1, 200), (8, 300), (40, 200), (40, 6000)])
+def test_largest_scales(n, kv):
+    """Scales up to 2^109 work (keys whose codes are zero: a score of 0 however large the scale); from 2^110 on a row that
+    sees them is NaN."""
+    a = Attn(16, 2, 128, 64, [n], [kv])
+    a.pool_np[:, :64 * 64] = 0                                  # K codes
+    a.set_scales(0, range(kv), k=1.0, v=1.0)
+    want, st = a.run()
+    a.check(want)
+    for k, v in ((2.0 ** 109, 1.0), (1.0, 2.0 ** 109)):
+        a.set_scales(0, range(kv), k=k, v=v)
+        o, st = a.run()
+        assert st == 0
+        # the same sums but for approximations of log2 and 1 / scale good to 2^-22: at most a BF16 step apart
+        ref = want[:n].float() * v
+        assert ((o[:n].float() - ref).abs() <= 2.0 ** -7 * ref.abs()).all()
+    for k, v in ((2.0 ** 110, 1.0), (2.0 ** 127, 1.0), (1.0, 2.0 ** 110), (1.0, 2.0 ** 127)):
+        a.set_scales(0, range(kv), k=1.0, v=1.0)
+        a.set_scales(0, [0], k=k, v=v)
+        o, st = a.run()
+        assert torch.isnan(o[:n]).all()
+
+
 @pytest.mark.parametrize("up", [30, 104, 110, 118])
 @pytest.mark.parametrize("n_kv,d,had", [(8, 128, 0), (2, 64, 0), (2, 128, 1), (2, 64, 16)])
 def test_rows_of_every_size_are_read_back(n_kv, d, had, up):
