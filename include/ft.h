@@ -258,15 +258,17 @@ int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_page
  * Arithmetic: q rounded to FP16 after the rotation (|q scale log2(e)| < 1023, else
  * FT_DEV_RANGE), codes exact, softmax weights rounded to FP16 below the products,
  * sums and statistics in FP32 (with many rows, below, the sums over positions enter
- * the rotation back as two BF16 numbers each, 2^-17).  V scales from 2^-100 to 2^60 are weighed against each
- * other without loss (smaller ones count as 2^-100; an entry whose scale is 0 has no
- * values, only a weight).  With more than 32 rows (tokens x heads of a group) K and V
- * are decoded to FP16 in groups of 32 positions, and scales less than 2^-15 of their
- * group's largest are rounded.  Entries behind a token's position may hold anything
- * else; a row that sees one with a scale that is not finite, or 2^110 and more, is NaN
- * (none is for scales below 2^109), and no other row is touched.  What a request's rows
- * are does not depend on the other requests of the call, up to the
- * order of FP32 sums and the kernel that max_q picks.
+ * the rotation back as two BF16 numbers each, 2^-17).  V scales that lie within a
+ * factor 2^100 of each other, none below 2^-100 (smaller ones count as that), are
+ * weighed against each other without loss: farther apart, weights whose product with
+ * the V scale is under 2^-126 of the row's largest are lost.  An entry whose V scale is
+ * 0 has no values, only a weight, kept beside V scales from 2^-70 to 2^40.  With more
+ * than 32 rows (tokens x heads of a group) K and V are decoded to FP16 in groups of 32
+ * positions, and scales less than 2^-15 of their group's largest are rounded.  Entries
+ * behind a token's position may hold anything else; a row that sees one with a scale
+ * that is not finite, or 2^110 and more, is NaN (none is for scales below 2^109), and no
+ * other row is touched.  What a request's rows are does not depend on the other requests
+ * of the call, up to the order of FP32 sums and the kernel that max_q picks.
  * Device conditions: cu_seqlens not ascending within [0, total_q], or n_b > max_q:
  * FT_DEV_RANGE, that request's rows are not written; a kv_len that is negative,
  * longer than table_stride pages or above 2^31 - 257: FT_DEV_CAPACITY, zeros; a

@@ -22,8 +22,10 @@ constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: smaller V scale
 // Scales from here on (2^110, as BF16 bits) make a row that sees them NaN, as those that are not finite
 // do: past them the factors of scores and sums of weights leave FP32.
 constexpr uint32_t kTooLarge = 0x7680u;
-// An entry whose V is zero (scale 0) weighs in the sum of weights alone, with lv = -60: that weight
-// and those of values between 2^-70 and 2^70 stay within FP32's (and P's) range beside each other.
+// An entry whose V is zero (scale 0) weighs in the sum of weights alone, with lv = -60.  A weight is lost
+// where 2^(t - m) passes below FP32's 2^-126: V scales 2^100 apart leave 2^26 for the softmax's own ratio,
+// more than FP32's digits, and 2^40 is as far above an entry without values.  Values of 2^-70 beside one
+// still have P = 1 at equal scores, 2^14 above FP16's subnormals.
 constexpr uint32_t kNoScaleExp = 67u;           // exponent of 2^-60
 constexpr float kNoScale = 8.6736173798840355e-19f;  // 2^-60
 

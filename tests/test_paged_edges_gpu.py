@@ -265,3 +265,47 @@ def test_rows_of_every_size_are_read_back(n_kv, d, had, up):
         # below FP32's smallest normal number lose up to 2^-126 each
         tol = 2.0 ** -8 * np.abs(back) + 2.0 ** -20 * np.linalg.norm(back, axis=-1, keepdims=True) + d * 2.0 ** -126
         assert np.isfinite(got).all() and np.all(np.abs(got - back) <= tol)
+
+
+@pytest.mark.parametrize("order", ["small_first", "small_last", "mixed"])
+@pytest.mark.parametrize("n,kv", [(1, 70), (1, 9000), (8, 500), (70, 400), (40, 6000)])
+def test_v_scales_a_factor_of_2_to_100_apart(n, kv, order):
+    """Entries whose values are next to nothing keep their weight, whatever comes first, in one share and across several."""
+    a = Attn(16, 2, 128, 64, [n], [kv], spread=3.0)
+    g = np.random.default_rng(kv)
+    pos = np.arange(kv - n + 1)                                  # (every row sees all of these)
+    small = {"small_first": pos < kv // 2, "small_last": pos >= kv // 2, "mixed": g.random(len(pos)) < 0.5}[order]
+    a.set_scales(0, range(kv), v=2.0 ** 50)
+    a.set_scales(0, pos[small], v=2.0 ** -50)
+    o, st = a.run()
+    assert st == 0
+    # many rows: operands of a group with a wide range of scales are 2^8 larger, and so is FP16's smallest step there
+    a.check(o, floor=2.0 ** -27)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 40, 2.0 ** -70])
+@pytest.mark.parametrize("n,kv", [(1, 70), (1, 9000), (70, 400), (40, 6000)])
+def test_entries_without_values_beside_the_ends_of_their_range(n, kv, big):
+    a = Attn(16, 2, 128, 64, [n], [kv], spread=3.0)
+    g = np.random.default_rng(kv)
+    a.set_scales(0, range(kv), v=big)
+    a.set_scales(0, np.nonzero(g.random(kv) < 0.5)[0], v=0.0)
+    o, st = a.run()
+    assert st == 0
+    # FP16's smallest step of a weight counts from the entries without values, whose scale counts as 2^-60
+    a.check(o, floor=2.0 ** -35 * max(1.0, 2.0 ** -60 / big))
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_attention_scales_2_to_15_below_their_neighbours(n):
+    """The documented end of exact products: a scale 2^-15 beside a 1 in every group of 32, for K and for V."""
+    a = Attn(8, 2, 128, 64, [n], [400])
+    g = np.random.default_rng(3)
+    for pos in range(400):
+        a.set_scales(0, [pos], k=2.0 ** -g.integers(0, 16), v=2.0 ** -g.integers(0, 16))
+    for pos in range(0, 400, 32):
+        a.set_scales(0, [pos], k=1.0, v=2.0 ** -15)
+        a.set_scales(0, [min(pos + 5, 399)], k=2.0 ** -15, v=1.0)
+    o, st = a.run()
+    assert st == 0
+    a.check(o, floor=2.0 ** -27)
