@@ -137,8 +137,11 @@ def _current():
     return dev, _torch[1](dev)
 
 
-# (current device, its current stream's handle, torch.float16), once torch is there
+# (current device, its current stream's handle, then the types that pass as INT32, FP32, BF16 or its bits, bytes),
+# once torch is there
 _torch = None
+_I32, _F32, _B16, _U8, _ANY = 2, 3, 4, 5, None
+_KINDS = {_I32: "int32", _F32: "float32", _B16: "bfloat16 (or int16, uint16: its bits)", _U8: "uint8", _ANY: "any type"}
 
 
 def _bind_torch():
@@ -147,7 +150,7 @@ def _bind_torch():
     torch.cuda.init()
     _torch = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
               getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
-              torch.float16)
+              (torch.int32,), (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16), (torch.uint8, torch.int8))
 
 
 def _stream(stream):
@@ -163,34 +166,32 @@ def _on(t, dev: int) -> None:
         raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _plain(t, nbytes: int, dev: int):
-    """Pointer of a contiguous tensor of nbytes-wide elements on device `dev` (or None, or a raw pointer)."""
+def _plain(t, kind: int, dev: int):
+    """Pointer of a contiguous tensor of that kind on device `dev` (or None, or a raw pointer)."""
     if t is None or isinstance(t, int):
         return t
-    if t.get_device() != dev or t.element_size() != nbytes or not t.is_contiguous() or t.dtype is _torch[2]:
+    if t.get_device() != dev or not t.is_contiguous() or (kind and t.dtype not in _torch[kind]):
         _on(t, dev)
-        raise ValueError(f"need a contiguous tensor of {nbytes}-byte elements (16-bit: BF16), got {t.dtype} with "
-                         f"strides {t.stride()}")
+        raise ValueError(f"need a contiguous tensor of {_KINDS[kind]}, got {t.dtype} with strides {t.stride()}")
     return t.data_ptr()
 
 
-def _rows(t, inner: int, nbytes: int, dev: int) -> tuple[int, int]:
-    """(pointer, elements between rows) of a tensor on device `dev` whose rows are `inner` contiguous nbytes-wide
-    elements; 16-bit ones are BF16 or their bits."""
+def _rows(t, inner: int, kind: int, dev: int) -> tuple[int, int]:
+    """(pointer, elements between rows) of a tensor on device `dev` whose rows are `inner` contiguous elements of that
+    kind."""
     shape = t.shape
     if t.get_device() != dev:
         _on(t, dev)
-    if t.dtype is _torch[2]:
-        raise ValueError("float16 where BF16 is read")
-    if t.is_contiguous() and t.element_size() == nbytes and len(shape) >= 2 and t.numel() == shape[0] * inner:
+    good = t.dtype in _torch[kind] and len(shape) >= 2
+    if good and t.is_contiguous() and t.numel() == shape[0] * inner:
         return t.data_ptr(), inner
     step = t.stride()
-    want, good = 1, t.element_size() == nbytes and len(shape) >= 2
+    want = 1
     for i in range(len(shape) - 1, 0, -1):
         good = good and (step[i] == want or shape[i] == 1)
         want *= shape[i]
     if not good or want != inner:
-        raise ValueError(f"need rows of {inner} contiguous {nbytes}-byte elements, got {t.dtype} {tuple(shape)} "
+        raise ValueError(f"need rows of {inner} contiguous elements of {_KINDS[kind]}, got {t.dtype} {tuple(shape)} "
                          f"with strides {step}")
     return t.data_ptr(), step[0] if shape[0] > 1 else max(step[0], inner)
 
@@ -286,11 +287,12 @@ def ft_kv_page_map(page_size, n_pages, ctx_len, new_len, B, block_table, free_pa
     dev, here = _current()
     if min(ctx_len.numel(), new_len.numel(), kv_len.numel(), cu_seqlens.numel() - 1, block_table.shape[0]) < B:
         raise ValueError(f"lengths, prefix sums or block tables of fewer than {B} requests")
-    table, stride = _rows(block_table, block_table.shape[1], 4, dev)
-    return lib().ft_kv_page_map(page_size, n_pages, _plain(ctx_len, 4, dev), _plain(new_len, 4, dev), B, table, stride,
-                                _plain(free_pages, 4, dev), free_pages.numel(), _plain(free_head, 4, dev),
-                                _plain(free_head_out, 4, dev), _plain(cu_seqlens, 4, dev), _plain(kv_len, 4, dev),
-                                _plain(slots, 4, dev), slots.numel(), _plain(dev_status, 4, dev),
+    table, stride = _rows(block_table, block_table.shape[1], _I32, dev)
+    return lib().ft_kv_page_map(page_size, n_pages, _plain(ctx_len, _I32, dev), _plain(new_len, _I32, dev), B, table,
+                                stride, _plain(free_pages, _I32, dev), free_pages.numel(),
+                                _plain(free_head, _I32, dev), _plain(free_head_out, _I32, dev),
+                                _plain(cu_seqlens, _I32, dev), _plain(kv_len, _I32, dev), _plain(slots, _I32, dev),
+                                slots.numel(), _plain(dev_status, _I32, dev),
                                 here if stream is None else _stream(stream))
 
 
@@ -306,10 +308,10 @@ def ft_kv_append_paged_int4(cfg, pages, n_pages, page_size, k, v, slots, total, 
     if min(k.shape[0], v.shape[0], slots.numel()) < total:
         raise ValueError(f"fewer than {total} rows or slots")
     row = cfg.n_kv * cfg.head_dim
-    kp, ks = _rows(k, row, 2, dev)
-    vp, vs = _rows(v, row, 2, dev)
-    return lib().ft_kv_append_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size, kp, ks, vp, vs,
-                                         _plain(slots, 4, dev), total, _plain(dev_status, 4, dev),
+    kp, ks = _rows(k, row, _B16, dev)
+    vp, vs = _rows(v, row, _B16, dev)
+    return lib().ft_kv_append_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size, kp, ks, vp, vs,
+                                         _plain(slots, _I32, dev), total, _plain(dev_status, _I32, dev),
                                          here if stream is None else _stream(stream))
 
 
@@ -320,9 +322,10 @@ def ft_kv_read_paged_int4(cfg, pages, n_pages, page_size, slots, total, k_out, v
     _check_pool(cfg, pages, n_pages, page_size)
     if min(k_out.numel(), v_out.numel()) < total * cfg.n_kv * cfg.head_dim or slots.numel() < total:
         raise ValueError(f"fewer than {total} rows or slots")
-    return lib().ft_kv_read_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size,
-                                       _plain(slots, 4, dev), total, _plain(k_out, 2, dev), _plain(v_out, 2, dev),
-                                       _plain(dev_status, 4, dev), here if stream is None else _stream(stream))
+    return lib().ft_kv_read_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size,
+                                       _plain(slots, _I32, dev), total, _plain(k_out, _B16, dev),
+                                       _plain(v_out, _B16, dev), _plain(dev_status, _I32, dev),
+                                       here if stream is None else _stream(stream))
 
 
 def ft_attn_paged_workspace_bytes(cfg, B: int, total_q: int, max_q: int) -> int:
@@ -336,14 +339,15 @@ def ft_attn_paged_int4(cfg, pages, n_pages, page_size, q, cu_seqlens, kv_len, bl
     _check_pool(cfg, pages, n_pages, page_size)
     if min(q.shape[0], o.shape[0]) < total_q or min(cu_seqlens.numel() - 1, kv_len.numel(), block_table.shape[0]) < B:
         raise ValueError(f"fewer than {total_q} rows or {B} requests")
-    row, size = cfg.n_q * cfg.head_dim, workspace.element_size()
-    qp, qs = _rows(q, row, 2, dev)
-    op, os_ = _rows(o, row, 2, dev)
-    table, stride = _rows(block_table, block_table.shape[1], 4, dev)
-    return lib().ft_attn_paged_int4(ctypes.byref(cfg), _plain(pages, 1, dev), n_pages, page_size, qp, qs,
-                                    _plain(cu_seqlens, 4, dev), _plain(kv_len, 4, dev), table, stride, B, total_q,
-                                    max_q, scale, op, os_, _plain(workspace, size, dev), workspace.numel() * size,
-                                    _plain(dev_status, 4, dev), here if stream is None else _stream(stream))
+    row = cfg.n_q * cfg.head_dim
+    qp, qs = _rows(q, row, _B16, dev)
+    op, os_ = _rows(o, row, _B16, dev)
+    table, stride = _rows(block_table, block_table.shape[1], _I32, dev)
+    return lib().ft_attn_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size, qp, qs,
+                                    _plain(cu_seqlens, _I32, dev), _plain(kv_len, _I32, dev), table, stride, B, total_q,
+                                    max_q, scale, op, os_, _plain(workspace, _ANY, dev),
+                                    workspace.numel() * workspace.element_size(),
+                                    _plain(dev_status, _I32, dev), here if stream is None else _stream(stream))
 
 
 def ft_decode_workspace_bytes(cfg, B: int, max_ctx: int) -> int:
@@ -407,13 +411,13 @@ def ft_logprobs(logits, targets, logprob, entropy, rank, top_ids, top_logprobs, 
     dev, here = _current()
     n, v = logits.shape
     dtype = FT_F32 if logits.element_size() == 4 else FT_BF16
-    x, stride = _rows(logits, v, 4 if dtype == FT_F32 else 2, dev)
+    x, stride = _rows(logits, v, _F32 if dtype == FT_F32 else _B16, dev)
     for t, size in ((targets, n), (logprob, n), (entropy, n), (rank, n), (top_ids, n * top_k), (top_logprobs, n * top_k)):
         if t is not None and t.numel() < size:
             raise ValueError(f"an argument holds {t.numel()} of {size} elements")
-    return lib().ft_logprobs(x, dtype, stride, n, v, _plain(targets, 4, dev), top_k, _plain(logprob, 4, dev),
-                             _plain(entropy, 4, dev), _plain(rank, 4, dev), _plain(top_ids, 4, dev),
-                             _plain(top_logprobs, 4, dev), _plain(dev_status, 4, dev),
+    return lib().ft_logprobs(x, dtype, stride, n, v, _plain(targets, _I32, dev), top_k, _plain(logprob, _F32, dev),
+                             _plain(entropy, _F32, dev), _plain(rank, _I32, dev), _plain(top_ids, _I32, dev),
+                             _plain(top_logprobs, _F32, dev), _plain(dev_status, _I32, dev),
                              here if stream is None else _stream(stream))
 
 

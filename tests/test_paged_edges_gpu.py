@@ -309,3 +309,46 @@ def test_attention_scales_2_to_15_below_their_neighbours(n):
     o, st = a.run()
     assert st == 0
     a.check(o, floor=2.0 ** -27)
+
+
+# ---------------------------------------------------------------- arguments
+def test_binding_refuses_other_types_of_the_same_width():
+    """FP32 where INT32 is read and the other way round, 16-bit and 8-bit types that are not what their bits are taken for."""
+    B, dev = 2, "cuda"
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    f = lambda *s: torch.zeros(s, device=dev)  # noqa: E731
+    ok = dict(ctx=i(B), new=i(B), table=i(B, 2), free=i(4), head=i(1), out=i(1), cu=i(B + 1), kv=i(B), slots=i(4), st=i(1))
+    call = lambda **o: (lambda a: ft.ft_kv_page_map(16, 4, a["ctx"], a["new"], B, a["table"], a["free"], a["head"], a["out"],  # noqa: E731
+                                                    a["cu"], a["kv"], a["slots"], a["st"]))(dict(ok, **o))
+    assert call() == ft.FT_OK
+    for k, v in ok.items():
+        with pytest.raises(ValueError):
+            call(**{k: v.float()})
+    cfg = _cfg(2, 2, 64)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    pool = torch.zeros(ft.ft_kv_pages_bytes(cfg, 2, 16), dtype=torch.uint8, device=dev)
+    ok = dict(pool=pool, k=bf(3, 2, 64), v=bf(3, 2, 64), slots=_i32([0, 1, 2]), st=i(1))
+    add = lambda **o: (lambda a: ft.ft_kv_append_paged_int4(cfg, a["pool"], 2, 16, a["k"], a["v"], a["slots"], 3, a["st"]))(dict(ok, **o))  # noqa: E731
+    read = lambda **o: (lambda a: ft.ft_kv_read_paged_int4(cfg, a["pool"], 2, 16, a["slots"], 3, a["k"], a["v"], a["st"]))(dict(ok, **o))  # noqa: E731
+    for c in (add, read):
+        assert c() == ft.FT_OK
+        assert c(k=ok["k"].view(torch.int16), v=ok["v"].view(torch.int16)) == ft.FT_OK     # BF16 bits
+        for bad in (dict(pool=pool.view(torch.float8_e4m3fn)), dict(pool=pool.bool()), dict(k=ok["k"].half()), dict(v=ok["v"].half()),
+                    dict(slots=ok["slots"].float()), dict(st=f(1))):
+            with pytest.raises(ValueError):
+                c(**bad)
+    ws = torch.zeros(ft.ft_attn_paged_workspace_bytes(cfg, 1, 3, 3), dtype=torch.uint8, device=dev)
+    ok = dict(pool=pool, q=bf(3, 2, 64), o=bf(3, 2, 64), cu=_i32([0, 3]), kv=_i32([3]), table=i(1, 1), st=i(1))
+    att = lambda **o: (lambda a: ft.ft_attn_paged_int4(cfg, a["pool"], 2, 16, a["q"], a["cu"], a["kv"], a["table"], 1, 3, 3, 0.1,  # noqa: E731
+                                                       a["o"], ws, a["st"]))(dict(ok, **o))
+    assert att() == ft.FT_OK
+    for bad in (dict(cu=ok["cu"].float()), dict(kv=ok["kv"].float()), dict(table=f(1, 1)), dict(st=f(1)), dict(pool=pool.view(torch.float8_e5m2))):
+        with pytest.raises(ValueError):
+            att(**bad)
+    ok = dict(x=f(2, 50), t=i(2), lp=f(2), en=f(2), rank=i(2), ids=i(2, 2), tv=f(2, 2), st=i(1))
+    lps = lambda **o: (lambda a: ft.ft_logprobs(a["x"], a["t"], a["lp"], a["en"], a["rank"], a["ids"], a["tv"], 2, a["st"]))(dict(ok, **o))  # noqa: E731
+    assert lps() == ft.FT_OK and lps(x=ok["x"].to(torch.bfloat16)) == ft.FT_OK
+    for k, v in ok.items():
+        with pytest.raises(ValueError):
+            lps(**{k: v.to(torch.int32) if v.dtype == torch.float32 else v.float()})
+    assert lps(x=ok["x"].to(torch.bfloat16).view(torch.int16)) == ft.FT_OK
