@@ -503,8 +503,10 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
     return FT_ERR_INVALID_ARG;
   if (!ft_host::aligned16(workspace)) return FT_ERR_INVALID_ARG;
   if (B > ft::kApMaxB || (int64_t)total_q * (c->n_q / c->n_kv) > INT32_MAX) return FT_ERR_UNSUPPORTED;
-  // units of work are counted in 32 bits
-  if (((int64_t)table_stride * page_size / ft::kUnit + 1 + ft::kSegUnits) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
+  // units of work (a request's and head's positions, one and kSegUnits more) and the joining kernel's CTAs (up
+  // to eight a request and head) are counted in 32 bits
+  static_assert(1 + ft::kSegUnits <= 8, "units of work");
+  if (((int64_t)table_stride * page_size / ft::kUnit + 8) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
   if (ws_bytes < ft_attn_paged_workspace_bytes(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;
   ft::AttnPagedParams p = {};
   p.pages = static_cast<const uint8_t*>(pages);
@@ -538,6 +540,7 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
                     : ft::launch_few<64, 4>(p, workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
   }
+  if (ft::attn_tiles_ctas(p) > INT32_MAX) return FT_ERR_UNSUPPORTED;
   return ft::launch_attn_tiles(p, c->head_dim, workspace, (cudaStream_t)stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 

@@ -155,6 +155,7 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
 
 // Requests with many rows (ft_attn_tiles.cu); a workspace of attn_tiles_ws bytes.
 size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q);
+int64_t attn_tiles_ctas(const AttnPagedParams& p);
 cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
 
 }  // namespace ft

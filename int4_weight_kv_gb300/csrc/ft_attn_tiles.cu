@@ -863,6 +863,13 @@ size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q) {
   return align_up((size_t)blocks * 16, 256) + (size_t)blocks * nkv * parts * 128 * (head_dim + 4) * 4;
 }
 
+int64_t attn_tiles_ctas(const AttnPagedParams& p) {
+  int rows, parts;
+  int64_t blocks;
+  tiles_shape(p.L.nkv, p.G, p.B, p.total_q, rows, parts, blocks);
+  return blocks * p.L.nkv * parts;
+}
+
 template <int D>
 static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cudaStream_t st) {
   static int allowed[64] = {0};
@@ -881,7 +888,6 @@ static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cud
   TilesSplit sp = {};
   int64_t blocks;
   tiles_shape(p.L.nkv, p.G, p.B, p.total_q, sp.rows, sp.parts, blocks);
-  if (blocks * p.L.nkv > INT32_MAX) return cudaErrorInvalidConfiguration;
   sp.meta = static_cast<int4*>(workspace);
   sp.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up((size_t)blocks * 16, 256));
   attn_tiles_kernel<D><<<(unsigned)(blocks * p.L.nkv * sp.parts), kThreads, Cfg<D>::kSmem, st>>>(p, sp);
