@@ -72,18 +72,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Waits for the phase with the given parity to complete; false on timeout.  The timer is first
-// read after 256 polls: its read takes longer than most waits.
+// Waits for the phase with the given parity to complete; false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
-  unsigned long long t0 = 0;
+  const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0) {
-      const unsigned long long now = globaltimer();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) return false;
-    }
+    if ((it & 255u) == 0 && globaltimer() - t0 > kWaitLimitNs) return false;
   }
 }
 
