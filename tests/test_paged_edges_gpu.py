@@ -18,7 +18,7 @@ import int4_weight_kv_gb300 as ft
 from int4_weight_kv_gb300 import runtime as rt
 from oracle import paged
 from tests import gpu_harness as H
-from tests.test_paged_gpu import Attn, _bf16, _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
+from tests.test_paged_gpu import Attn, Server, _bf16, _cfg, _gpu, _i32, _status  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -352,3 +352,53 @@ def test_binding_refuses_other_types_of_the_same_width():
         with pytest.raises(ValueError):
             lps(**{k: v.to(torch.int32) if v.dtype == torch.float32 else v.float()})
     assert lps(x=ok["x"].to(torch.bfloat16).view(torch.int16)) == ft.FT_OK
+
+
+# ---------------------------------------------------------------- together
+def test_generation_loop_step_by_step():
+    """Every step of a captured generation loop against one call over all tokens: each token's log probability, and that the
+    token chosen is the largest logit's.  Both paths differ by the order of FP32 sums, FP16 weights and BF16 outputs."""
+    B, lens, steps = 3, [20, 1, 33], 31
+    s = Server(B)
+    prompt = torch.randint(0, s.V, (sum(lens),), generator=torch.Generator().manual_seed(4)).to(torch.int32).cuda()
+    o = s.forward(_i32(lens), prompt, max(lens))
+    s.choose(o[torch.tensor(np.cumsum(lens) - 1).cuda()].view(B, 1024).float())
+    chosen, lps = [s.tokens.clone()], [s.lp.clone()]
+    s.step()
+    chosen.append(s.tokens.clone())
+    lps.append(s.lp.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.step()
+    for _ in range(steps - 1):
+        graph.replay()
+        chosen.append(s.tokens.clone())
+        lps.append(s.lp.clone())
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    w, seq, got = Server(B), torch.stack(chosen)[..., 0], torch.stack(lps)           # [steps + 1, B]
+    packed, rows, first = [], [], 0
+    for b, n in enumerate(lens):
+        packed += [prompt[first:first + n], seq[:steps, b]]
+        rows += range(sum(lens[:b]) + b * steps + n - 1, sum(lens[:b + 1]) + (b + 1) * steps)
+        first += n
+    total = [n + steps for n in lens]
+    h = w.forward(_i32(total), torch.cat(packed), max(total))[torch.tensor(rows).cuda()].view(-1, 1024).float()
+    # rows in the order of the requests, steps + 1 of each
+    logits = torch.empty((len(rows), w.V), device="cuda")
+    for a in range(0, len(rows), 32):
+        part = h[a:a + 32].contiguous()
+        ft.check(ft.ft_lm_head_bf16(part, w.gamma, w.lm, logits[a:a + 32], part.shape[0], w.V, 1024, 1e-5))
+    t, lp = seq.T.reshape(-1).contiguous(), torch.empty(len(rows), device="cuda")
+    ft.check(ft.ft_logprobs(logits, t, lp, None, None, None, None, 0, w.status))
+    torch.cuda.synchronize()
+    assert w.status.item() == 0
+    # Before its rounding to BF16 an output differs by under 2^-10 (two times FP16's half step of the weights); a rounding
+    # turns that into a whole step, 2^-7 at most, with probability difference / step: variance 2^-17.  The norm passes it on;
+    # a logit sums it over a row of norm 32 with weights of 1/8, a log probability is the difference of two such sums.
+    bound = 5 * 2 ** 0.5 * 2.0 ** -8.5 * 32 / 8
+    err = (lp.view(B, -1).T - got).abs()
+    assert err.max() < bound, err.max().item()
+    gap = logits.max(-1).values - logits.gather(1, t.view(-1, 1).long())[:, 0]
+    assert gap.max() < bound, gap.max().item()
+    print("largest difference of a log probability", err.max().item(), "of a logit", gap.max().item())
