@@ -253,7 +253,8 @@ int ft_kv_read_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_page
  * inside a row, q post-RoPE; o may be q where the strides are equal.  A token at
  * a negative position (kv_len < n_b) sees nothing and gets zeros.  Rows behind
  * cu_seqlens[B] are left as they are.  max_q: an upper bound of n_b; it picks the
- * kernel and sizes the launch.  B <= 8192, total_q n_q / n_kv < 2^31,
+ * kernel, one for all requests of the call, and sizes the launch (single tokens over long
+ * caches beside a long prompt are faster in a call of their own).  B <= 8192, total_q n_q / n_kv < 2^31,
  * B n_kv (table_stride page_size / 64 + 8) < 2^31 and, with more than 32 rows (below),
  * total_q n_q / 256 + B n_kv < 2^31, else FT_ERR_UNSUPPORTED.
  * Arithmetic: q rounded to FP16 after the rotation (|q scale log2(e)| < 1023, else

@@ -17,7 +17,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 
 // ------------------------------------------------------------------ few rows
 // Requests with up to 8 NT rows (tokens x heads of a group) a KV head: every byte of the
-// cache is read once and used for all of them.  A 16-position tile costs a warp about 265
+// cache is read once and used for all of them.  A 16-position tile costs a warp about 270
 // instructions (360 would take as long as its bytes at the HBM's rate), so loads and arithmetic
 // weigh alike: 32 requests of 4096 positions took 38.9 us, 35.5 without the arithmetic, 34.6
 // without the loads.  What a share costs before its first tile (lengths, pages, first tiles, the

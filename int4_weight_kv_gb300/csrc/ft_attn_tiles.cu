@@ -841,7 +841,9 @@ __global__ void __launch_bounds__(128) attn_tiles_join_kernel(const AttnPagedPar
 // parts as fill the SMs (up to 16, counting half a block for the requests' remainders).  Measured,
 // 256 rows and one part against this rule (us): 256 tokens over 32768 positions (8B shape) 505 / 229,
 // 64 of each of four requests over 8192 139 / 73, 2000 over 3000 with 4 heads 63 / 38; 5 requests of
-// 777 (8 heads, d 64) run at once only with 256 rows, 21.5 (128 rows: 32.6).
+// 777 (8 heads, d 64) run at once only with 256 rows, 21.5 (128 rows: 32.6).  Not built: 256 rows with
+// parts.  A 128-row CTA's tile takes nearly as long as one of 256 rows (3400 and 3600 cycles), so 256 to 768
+// tokens over a long history leave time: 226, 428 (512), 477 (640: one part again) and 481 us over 32768.
 static void tiles_shape(int nkv, int G, int B, int total_q, int& rows, int& parts, int64_t& blocks) {
   int sms = ft_host::num_sms();
   if (sms <= 0) sms = 152;

@@ -13,7 +13,8 @@ namespace ft {
 // four consecutive ones per binary search.  Where outputs alias the inputs that they advance
 // (kv_len = ctx_len, free_head_out = free_head) the CTAs are one cluster of up to kMapCtas,
 // which meets once after everyone has read them.  Measured (256 prompts, 260k rows): 31 us for
-// one search a slot by eight CTAs, 5 us so.
+// one search a slot by eight CTAs, 5 us so; 50 us where lengths and head are advanced in place, by eight
+// CTAs (32 requests of one token: 0.3 us more than 4.9).
 constexpr int kMapCtas = 8, kMapThreads = 256, kMapMaxB = 8192, kMapRun = 4;
 
 struct MapParams {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
 // and the two positions of a V pair meet in neighbouring groups of lanes.  The rotated row
 // is quantised in the registers where it was formed: no shared memory.  Bound by the issue slots
 // (450 warp instructions for eight rows, 380 to read back; 72% of the slots used): 16384 tokens of 8
-// heads of 128, K and V, 26 us and 23 us, 3.3 and 3.7 TB/s.
+// heads of 128, K and V, 26 us and 24 us, 3.3 and 3.6 TB/s.
 constexpr int kRowThreads = 128;
 
 struct PagedRows {
