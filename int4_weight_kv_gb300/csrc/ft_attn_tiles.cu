@@ -625,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     }
     for (int j = 0; j < nkt; ++j) {
       const int st = j & 1;
-      // An entry with a scale from 2^110 on (its own row was not finite) makes the rows that see it NaN, but must not
-      // reach its neighbours, nor the rows that do not see it: its K operand is NaN, which is one column of S,
-      // masked like any other, and its V operand is 0.
+      // An entry with a scale from 2^110 on, or one that is not finite (nor was its own row), makes the rows that see
+      // it NaN, but must not reach its neighbours, nor the rows that do not see it: its K operand is NaN, which is
+      // one column of S, masked like any other, and its V operand is 0.
       const bool poor = (sc & 0x7FFFu) >= kTooLarge || ((sc >> 16) & 0x7FFFu) >= kTooLarge;
       if (poor) sc = 0u;
       // the 32 positions' scales relative to their largest's power of two, as multipliers of the
