@@ -283,6 +283,72 @@ int ft_attn_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, 
                        int table_stride, int B, int total_q, int max_q, float scale, uint16_t *o_bf16, int64_t o_stride,
                        void *workspace, size_t ws_bytes, int32_t *dev_status, ft_stream stream);
 
+/* Attention of drafted tokens that form a tree: ft_attn_paged_int4 with a mask among the new tokens.
+ * Token i of request b (row cu_seqlens[b] + i) has its entry at position kv_len[b] - n_b + i (its own
+ * K/V appended before) and sees all positions before kv_len[b] - n_b, and new token j < n_b where bit
+ * j % 32 of tree_mask[(cu_seqlens[b] + i) mask_stride + j / 32] is set; bits from n_b on are ignored.
+ * tree_mask: uint32, row i at i * mask_stride words, ceil(max_q / 32) of them read.  Any pattern will do
+ * (a token that sees itself and its ancestors; all of a block; none): a row that sees nothing gets zeros.
+ * A token whose entry would be at a negative position has none; bits that name it are ignored.  The position
+ * that a token is rotated to (its depth in the tree) need not be that of its entry: see
+ * ft_kv_append_rope_paged_int4.  Everything else (limits, arithmetic, device conditions, workspace) is as there. */
+size_t ft_attn_tree_workspace_bytes(const ft_block_cfg *cfg, int B, int total_q, int max_q);
+int ft_attn_tree_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, int page_size,
+                            const uint16_t *q_bf16, int64_t q_stride, const int32_t *cu_seqlens, const int32_t *kv_len,
+                            const int32_t *block_table, int table_stride, const uint32_t *tree_mask, int64_t mask_stride,
+                            int B, int total_q, int max_q, float scale, uint16_t *o_bf16, int64_t o_stride,
+                            void *workspace, size_t ws_bytes, int32_t *dev_status, ft_stream stream);
+
+/* Moves entries inside the pool, of all KV heads: for each request b < B and j < n, the entry at slot
+ * src_slots[b n + j] goes to slot dst_slots[b n + j], bit for bit (the accepted branch of a tree to
+ * consecutive positions).  The moves of one request happen at once: all its entries are read before
+ * any is written, so their slots may overlap.  A slot of -1 on either side skips the move; any other slot outside the pool
+ * sets FT_DEV_RANGE and skips it.  The destinations must be distinct, and no other request's sources.
+ * src_slots, dst_slots: int32 [B, n]; n <= 256, else FT_ERR_UNSUPPORTED. */
+int ft_kv_move_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pages, int page_size, const int32_t *src_slots,
+                          const int32_t *dst_slots, int B, int n, int32_t *dev_status, ft_stream stream);
+
+/* ---- rows of the fused projection ----------------------------------------
+ * q, k: BF16 bits as the projection leaves them (pre-RoPE), row t at t * stride (elements), [heads, d]
+ * inside a row; views of the fused projection's output work, at any alignment.  In FP32:
+ *   y = gamma * x / sqrt(mean x^2 + cfg->rms_eps) per head (gamma: FP32 [d]; NULL: y = x),
+ *   z_i = y_i cos a - y_(i+d/2) sin a,  z_(i+d/2) = y_(i+d/2) cos a + y_i sin a,  i < d/2,
+ *   a = positions[t] cfg->rope_base^(-2i/d),
+ * the pairing, the frequencies and the exact reduction of the angles being the decode block's.
+ * positions: int32 [total], any values (tokens of a tree share them).  With a norm, |x| < 2^60. */
+
+/* q_out, k_out: z rounded once to BF16, rows at their own strides; an output may be its input where the
+ * strides are equal.  q with q_out, or k with k_out, may be NULL: left out. */
+int ft_qk_norm_rope_bf16(const ft_block_cfg *cfg, const uint16_t *q_bf16, int64_t q_stride, const uint16_t *k_bf16,
+                         int64_t k_stride, const float *gamma_q, const float *gamma_k, const int32_t *positions, int total,
+                         uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride, ft_stream stream);
+
+/* ft_kv_append_paged_int4 of z (k) and of v as it is: k is normalised, rotated to its position, rotated by H
+ * and quantised without a rounding in between, and placed at its slot with v.  Slots as there; the rotation's
+ * position need not be the slot's.  q_bf16 not NULL: z (q) goes to q_out as in ft_qk_norm_rope_bf16, also of
+ * rows whose slot is -1. */
+int ft_kv_append_rope_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pages, int page_size, const uint16_t *k_bf16,
+                                 int64_t k_stride, const uint16_t *v_bf16, int64_t v_stride, const float *gamma_k,
+                                 const int32_t *positions, const int32_t *slots, int total, const uint16_t *q_bf16,
+                                 int64_t q_stride, const float *gamma_q, uint16_t *q_out, int64_t q_out_stride,
+                                 int32_t *dev_status, ft_stream stream);
+
+/* Causal attention of whole prompts over their own rows (post-RoPE BF16, not quantised): sequence b owns rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q, k, v and o, and its row i attends to its rows 0 .. i:
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,   query head h reads KV head h / G.
+ * q, o: [total, n_q, d], k, v: [total, n_kv, d] at their strides (elements); k and v at 16-byte boundaries with
+ * strides of a multiple of 8, else FT_ERR_INVALID_ARG; o may be q where the strides are equal.  Rows that no
+ * sequence owns are left as they are.  max_len: an upper bound of the lengths; it sizes the launch.
+ * Arithmetic: BF16 products, FP32 sums, maxima and statistics, weights rounded to BF16 below the second
+ * product (2^-8 each).  A row that sees a k or v which is not finite is not finite in the channels
+ * concerned (it may be NaN in all of them); rows that do not see it, and other sequences, are not touched.
+ * Device conditions: cu_seqlens not ascending within [0, total], or a length above max_len: FT_DEV_RANGE, that
+ * sequence's rows are not written.  B <= 8192, total n_q / n_kv < 2^31, else FT_ERR_UNSUPPORTED. */
+int ft_attn_prompt_bf16(const ft_block_cfg *cfg, const uint16_t *q_bf16, int64_t q_stride, const uint16_t *k_bf16,
+                        int64_t k_stride, const uint16_t *v_bf16, int64_t v_stride, const int32_t *cu_seqlens, int B,
+                        int total, int max_len, float scale, uint16_t *o_bf16, int64_t o_stride, int32_t *dev_status,
+                        ft_stream stream);
+
 /* ---- the decode block ---------------------------------------------------
  * One token per request b < B at position pos[b] (= L_b, its history length):
  *   rho1 = (mean x^2 + eps)^-1/2;  [q;k;v] = rho1 * W'_qkv x      (row factor

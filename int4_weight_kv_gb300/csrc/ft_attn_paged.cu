@@ -75,7 +75,7 @@ struct FewRows {
   static int smem(int B) { return kArea + kQ + (B + 1) * 4; }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kernel(const AttnPagedParams p,
                                                                                   const SplitWs ws) {
   using T = FewRows<D, NT>;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) lim[t][i] = kv - n + min((8 * t + 2 * tig + i) / p.G, n - 1);
-    const int all = kv - n;  // positions up to this are visible to every row
+    const int all = TREE ? kv - n - 1 : kv - n;  // positions up to this are visible to every row
 
     float acc[NT][KT][4];
     float m[NT][2], l[NT][2], u0[NT][2];  // running max, sum, and max - kPBias (0 for none yet)
@@ -297,10 +297,22 @@ __global__ void __launch_bounds__(kApWarps * 32, NT == 1 ? 4 : 2) attn_few_kerne
         const bool ga = sc0 != 0xFFFFFFFFu, gb = sc1 != 0xFFFFFFFFu;
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          s[c][0] = ga && pa <= lim[c][0] ? s[c][0] : -INFINITY;  // whatever the entry holds
-          s[c][1] = ga && pa <= lim[c][1] ? s[c][1] : -INFINITY;
-          s[c][2] = gb && pb <= lim[c][0] ? s[c][2] : -INFINITY;
-          s[c][3] = gb && pb <= lim[c][1] ? s[c][3] : -INFINITY;
+          if constexpr (TREE) {
+            const int at = p0 - (kv - n);  // the tile's first position among the new tokens
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int tok = min((8 * c + 2 * tig + i) / p.G, n - 1);
+              uint32_t bits = tree_bits(p.mask + (row0 + tok) * p.mask_stride, at, n);
+              if (at < 0) bits |= at <= -16 ? 0xFFFFu : (1u << -at) - 1u;  // the history
+              s[c][i] = ga && ((bits >> g) & 1u) ? s[c][i] : -INFINITY;  // whatever the entry holds
+              s[c][2 + i] = gb && ((bits >> (g + 8)) & 1u) ? s[c][2 + i] : -INFINITY;
+            }
+          } else {
+            s[c][0] = ga && pa <= lim[c][0] ? s[c][0] : -INFINITY;  // whatever the entry holds
+            s[c][1] = ga && pa <= lim[c][1] ? s[c][1] : -INFINITY;
+            s[c][2] = gb && pb <= lim[c][0] ? s[c][2] : -INFINITY;
+            s[c][3] = gb && pb <= lim[c][1] ? s[c][3] : -INFINITY;
+          }
         }
         // 0 x (1 / scale) of an entry that no row sees must be 0
         if (!ga || pa >= kv) rs0 = 0.0f;
@@ -442,7 +454,7 @@ static int few_tiles(int max_q, int G) {
   return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStream_t st) {
   using T = FewRows<D, NT>;
   static int allowed[64] = {0};
@@ -450,7 +462,7 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!allowed[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(attn_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::smem(kApMaxB));
+        cudaFuncSetAttribute(attn_few_kernel<D, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::smem(kApMaxB));
     if (e != cudaSuccess) return e;
     allowed[dev] = 1;
   }
@@ -458,7 +470,7 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   ws.pref = static_cast<int32_t*>(workspace);
   ws.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up((size_t)(p.B + 1) * 4, 256));
   const int ctas = few_ctas(NT);
-  attn_few_kernel<D, NT><<<ctas, kApWarps * 32, T::smem(p.B), st>>>(p, ws);
+  attn_few_kernel<D, NT, TREE><<<ctas, kApWarps * 32, T::smem(p.B), st>>>(p, ws);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -477,22 +489,25 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
   return cudaLaunchKernelEx(&cfg, wide ? attn_join_kernel<D, NT, 4> : attn_join_kernel<D, NT, 1>, p, ws, ctas);
 }
 
-
-}  // namespace ft
-
-extern "C" {
-
-size_t ft_attn_paged_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) {
-  if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > ft::kApMaxB || total_q < 0 || max_q < 1) return 0;
-  const int nt = ft::few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
-  if (nt == 0) return ft::attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
-  return ft::align_up((size_t)(B + 1) * 4, 256) + (size_t)ft::few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
+template <bool TREE>
+static cudaError_t launch_few_any(const AttnPagedParams& p, int head_dim, int nt, void* ws, cudaStream_t st) {
+  if (head_dim == 128)
+    return nt == 1 ? launch_few<128, 1, TREE>(p, ws, st) : nt == 2 ? launch_few<128, 2, TREE>(p, ws, st) : launch_few<128, 4, TREE>(p, ws, st);
+  return nt == 1 ? launch_few<64, 1, TREE>(p, ws, st) : nt == 2 ? launch_few<64, 2, TREE>(p, ws, st) : launch_few<64, 4, TREE>(p, ws, st);
 }
 
-int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const uint16_t* q_bf16,
-                       int64_t q_stride, const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table,
-                       int table_stride, int B, int total_q, int max_q, float scale, uint16_t* o_bf16, int64_t o_stride,
-                       void* workspace, size_t ws_bytes, int32_t* dev_status, ft_stream stream) {
+static size_t attn_ws(const ft_block_cfg* c, int B, int total_q, int max_q) {
+  if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > kApMaxB || total_q < 0 || max_q < 1) return 0;
+  const int nt = few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
+  if (nt == 0) return attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
+  return align_up((size_t)(B + 1) * 4, 256) + (size_t)few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
+}
+
+// Both calls: causal among the new tokens (tree false), or by their masks.
+static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const uint16_t* q_bf16, int64_t q_stride,
+                     const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table, int table_stride, bool tree,
+                     const uint32_t* mask, int64_t mask_stride, int B, int total_q, int max_q, float scale, uint16_t* o_bf16,
+                     int64_t o_stride, void* workspace, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
   const int st = ft_host::check_paged(c, pages, n_pages, page_size);
   if (st != FT_OK) return st;
   if (B < 1 || total_q < 0 || max_q < 1 || table_stride < 1 || !(scale > 0.0f) || !(scale < 3e38f))
@@ -502,15 +517,17 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
   if (!q_bf16 || !o_bf16 || !cu_seqlens || !kv_len || !block_table || !workspace || q_stride < row || o_stride < row)
     return FT_ERR_INVALID_ARG;
   if (!ft_host::aligned16(workspace)) return FT_ERR_INVALID_ARG;
-  if (B > ft::kApMaxB || (int64_t)total_q * (c->n_q / c->n_kv) > INT32_MAX) return FT_ERR_UNSUPPORTED;
+  if (tree && (!mask || (reinterpret_cast<uintptr_t>(mask) & 3u) || mask_stride < ((int64_t)std::min(max_q, total_q) + 31) / 32))
+    return FT_ERR_INVALID_ARG;
+  if (B > kApMaxB || (int64_t)total_q * (c->n_q / c->n_kv) > INT32_MAX) return FT_ERR_UNSUPPORTED;
   // units of work (a request's and head's positions, one and kSegUnits more) and the joining kernel's CTAs (up
   // to eight a request and head) are counted in 32 bits
-  static_assert(1 + ft::kSegUnits <= 8, "units of work");
-  if (((int64_t)table_stride * page_size / ft::kUnit + 8) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
-  if (ws_bytes < ft_attn_paged_workspace_bytes(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;
-  ft::AttnPagedParams p = {};
+  static_assert(1 + kSegUnits <= 8, "units of work");
+  if (((int64_t)table_stride * page_size / kUnit + 8) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
+  if (ws_bytes < attn_ws(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;
+  AttnPagedParams p = {};
   p.pages = static_cast<const uint8_t*>(pages);
-  p.L = ft::paged_layout(*c, n_pages, page_size);
+  p.L = paged_layout(*c, n_pages, page_size);
   p.q = q_bf16;
   p.o = o_bf16;
   p.q_stride = q_stride;
@@ -525,23 +542,41 @@ int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, in
   p.max_q = std::min(max_q, total_q);
   p.G = c->n_q / c->n_kv;
   p.hb = c->had_block;
-  p.qscale = scale * 1.44269504088896341f * ft::kQUp;
-  p.norm = ft::paged_norm(c->had_block);
-  const int nt = ft::few_tiles(p.max_q, p.G);
+  p.qscale = scale * 1.44269504088896341f * kQUp;
+  p.norm = paged_norm(c->had_block);
+  p.mask = tree ? mask : nullptr;
+  p.mask_stride = mask_stride;
+  const int nt = few_tiles(p.max_q, p.G);
   if (nt > 0) {
-    cudaError_t e;
-    if (c->head_dim == 128)
-      e = nt == 1 ? ft::launch_few<128, 1>(p, workspace, (cudaStream_t)stream)
-          : nt == 2 ? ft::launch_few<128, 2>(p, workspace, (cudaStream_t)stream)
-                    : ft::launch_few<128, 4>(p, workspace, (cudaStream_t)stream);
-    else
-      e = nt == 1 ? ft::launch_few<64, 1>(p, workspace, (cudaStream_t)stream)
-          : nt == 2 ? ft::launch_few<64, 2>(p, workspace, (cudaStream_t)stream)
-                    : ft::launch_few<64, 4>(p, workspace, (cudaStream_t)stream);
+    const cudaError_t e = tree ? launch_few_any<true>(p, c->head_dim, nt, workspace, stream) : launch_few_any<false>(p, c->head_dim, nt, workspace, stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
   }
-  if (ft::attn_tiles_ctas(p) > INT32_MAX) return FT_ERR_UNSUPPORTED;
-  return ft::launch_attn_tiles(p, c->head_dim, workspace, (cudaStream_t)stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  if (attn_tiles_ctas(p) > INT32_MAX) return FT_ERR_UNSUPPORTED;
+  return launch_attn_tiles(p, c->head_dim, workspace, stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+}
+
+}  // namespace ft
+
+extern "C" {
+
+size_t ft_attn_paged_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q); }
+size_t ft_attn_tree_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q); }
+
+int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const uint16_t* q_bf16,
+                       int64_t q_stride, const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table,
+                       int table_stride, int B, int total_q, int max_q, float scale, uint16_t* o_bf16, int64_t o_stride,
+                       void* workspace, size_t ws_bytes, int32_t* dev_status, ft_stream stream) {
+  return ft::attn_call(c, pages, n_pages, page_size, q_bf16, q_stride, cu_seqlens, kv_len, block_table, table_stride, false, nullptr, 0, B,
+                       total_q, max_q, scale, o_bf16, o_stride, workspace, ws_bytes, dev_status, (cudaStream_t)stream);
+}
+
+int ft_attn_tree_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const uint16_t* q_bf16,
+                            int64_t q_stride, const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table,
+                            int table_stride, const uint32_t* tree_mask, int64_t mask_stride, int B, int total_q, int max_q,
+                            float scale, uint16_t* o_bf16, int64_t o_stride, void* workspace, size_t ws_bytes,
+                            int32_t* dev_status, ft_stream stream) {
+  return ft::attn_call(c, pages, n_pages, page_size, q_bf16, q_stride, cu_seqlens, kv_len, block_table, table_stride, true, tree_mask,
+                       mask_stride, B, total_q, max_q, scale, o_bf16, o_stride, workspace, ws_bytes, dev_status, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,18 @@ struct AttnPagedParams {
   int32_t* status;
   int table_stride, B, total_q, max_q, G, hb;
   float qscale, norm;  // scale log2(e) kQUp; 1 / sqrt(hb)
+  const uint32_t* mask;  // which new tokens a token sees, by row (kernels for trees)
+  int64_t mask_stride;
 };
+
+// 32 mask bits of a row, from new token `at` on (at may be negative: tokens of the history are not in it),
+// those of tokens from n on being zero.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int at, int n) {
+  const int w = at >> 5, s = at & 31, words = (n + 31) >> 5;
+  const uint32_t lo = w >= 0 && w < words ? __ldg(row + w) : 0u, hi = s && w + 1 >= 0 && w + 1 < words ? __ldg(row + w + 1) : 0u;
+  const uint32_t x = __funnelshift_r(lo, hi, s);
+  return at + 32 <= n ? x : at >= n ? 0u : x & ((1u << (n - at)) - 1u);
+}
 
 // One request's length, checked: 0 (every row empty: zeros) where it is negative, passes the table
 // row or is within a tile of 2^31.
@@ -156,6 +167,6 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
 // Requests with many rows (ft_attn_tiles.cu); a workspace of attn_tiles_ws bytes.
 size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q);
 int64_t attn_tiles_ctas(const AttnPagedParams& p);
-cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
+cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);  // p.mask: a tree's
 
 }  // namespace ft

@@ -321,14 +321,15 @@ static WsPlan make_plan(const ft_block_cfg& c, int B, int max_ctx) {
 // inv_freq[i] = base^(-2i/d) (FP64) divided by 2 pi and scaled by 2^64: the
 // RoPE angle of position p is p * turn[i] turns, reduced modulo one turn by
 // unsigned 64-bit wrap-around.  Cached for the last (base, d) of this thread.
-static void rope_turns(float base, int d, uint64_t (&turn)[64]) {
+void rope_turns(float base, int d, uint64_t (&turn)[64]) {
   thread_local float cb = -1.0f;
   thread_local int cd = -1;
   thread_local uint64_t ct[64];
   if (cb != base || cd != d) {
     for (int i = 0; i < 64; ++i) {
       const double inv_freq = (i < d / 2) ? std::pow((double)base, -2.0 * i / d) : 0.0;
-      ct[i] = (uint64_t)std::ldexp(inv_freq / 6.283185307179586476925, 64);
+      const double turns = inv_freq / 6.283185307179586476925;
+      ct[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);  // (a base below 1 turns by more than once a position)
     }
     cb = base;
     cd = d;

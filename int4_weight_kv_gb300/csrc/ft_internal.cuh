@@ -532,6 +532,9 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 namespace ft {
 
+// RoPE frequencies of a head dimension as 64-bit binary fractions of a turn (ft_block.cu).
+void rope_turns(float base, int d, uint64_t (&turn)[64]);
+
 // Launches a kernel that begins with griddep_serve(), so that its launch overlaps the kernel before
 // it, in clusters of `cluster` CTAs.
 template <typename... Args>

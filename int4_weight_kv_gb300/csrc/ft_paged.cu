@@ -217,15 +217,6 @@ __device__ __forceinline__ int paged_slot(const PagedRows& p, int slot, int j) {
   return -1;
 }
 
-// NaN where either is, else the larger.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-constexpr float kMagic = 12582912.0f;  // 1.5 2^23: |x| r + kMagic rounds to the nearest integer, ties to even
-
 // Codes of words g and g + 1 (values u[e][0] and u[e][1], as kMagic + magnitude; x the signed
 // values) as one register: magnitudes at bits 0, 3, 8, 11, signs at bits 15, 14, 7, 6 of each half.
 __device__ __forceinline__ uint32_t paged_pack(const f32x2 (&x)[4], const f32x2 (&u)[4]) {
@@ -244,20 +235,6 @@ __device__ __forceinline__ uint32_t paged_pack(const f32x2 (&x)[4], const f32x2 
   const uint32_t s02 = prmt(prmt(xs[2][0], xs[0][0], 0x0073u), prmt(xs[2][1], xs[0][1], 0x0073u), 0x5410u);
   const uint32_t s13 = prmt(prmt(xs[3][0], xs[1][0], 0x0073u), prmt(xs[3][1], xs[1][1], 0x0073u), 0x5410u);
   return w | (s02 & 0x80808080u) | ((s13 >> 1) & 0x40404040u);
-}
-
-// Magnitude of the code of y = fl(|x| norm) by scale s, min(rne(fl(y / s)), 7), decided without a
-// division where c = rne(y / s) is right but perhaps for the side of a boundary.  With t the
-// nearest boundary, y - t s is exact; the FP32 quotient is t itself (and the even neighbour its
-// code) while that is within half a step of t, else its sign decides.
-__device__ __noinline__ float paged_edge(float y, float s, float c) {
-  if (!(s >= 1e-30f)) return s > 0.0f ? fminf(rintf(__fdiv_rn(y, s)), 7.0f) : 0.0f;
-  const float t = fmaf(-c, s, y) > 0.0f ? c + 0.5f : c - 0.5f, rem = fmaf(-t, s, y);
-  const float step = __uint_as_float((__float_as_uint(t) & 0x7F800000u) - (24u << 23));  // half a step above t
-  const float half = (rem < 0.0f && t == 0.5f) ? 0.5f * step : step;                     // below a power of two: half of it
-  const float lo = t - 0.5f, hi = t + 0.5f;
-  if (fabsf(rem) <= s * half) return ((int)lo & 1) ? hi : lo;
-  return fminf(rem > 0.0f ? hi : lo, 7.0f);
 }
 
 template <int D>
@@ -439,6 +416,56 @@ __global__ void __launch_bounds__(kRowThreads, 9) read_paged_kernel(const PagedR
   }
 }
 
+// ------------------------------------------------------------------ moving entries
+// A CTA per request and KV head: every entry of the request's moves is read into shared memory before
+// any is written.  Latency: slots, entries, barrier, stores.
+constexpr int kMoveThreads = 128, kMoveMax = 256;
+
+struct MoveParams {
+  const int32_t *src, *dst;
+  uint8_t* pages;
+  PagedLayout L;
+  int n;
+  int32_t* status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_paged_kernel(const MoveParams p) {
+  constexpr int NK = D / 8, NV = D / 4, NW = NK + NV + 1;  // an entry: K words, V halfwords (positions share their words), scales
+  extern __shared__ uint32_t move_smem[];
+  __shared__ int from[kMoveMax], to[kMoveMax];
+  griddep_serve();
+  const int h = blockIdx.x % p.L.nkv, b = blockIdx.x / p.L.nkv;
+  for (int i = threadIdx.x; i < p.n; i += kMoveThreads) {
+    const int a = __ldcg(p.src + (int64_t)b * p.n + i), z = __ldcg(p.dst + (int64_t)b * p.n + i);
+    auto bad = [&](int s) { return s < -1 || (s >= 0 && (s >> p.L.pshift) >= p.L.npages); };
+    if (h == 0 && (bad(a) || bad(z))) set_status(p.status, FT_DEV_RANGE);
+    const bool none = a < 0 || z < 0 || bad(a) || bad(z) || a == z;
+    from[i] = none ? -1 : a;
+    to[i] = z;
+  }
+  __syncthreads();
+  auto words = [&](const int* slots, auto&& body) {  // body(word, its place in the pool): K whole words, then V halves, then scales
+    for (int i = threadIdx.x; i < p.n * NW; i += kMoveThreads) {
+      const int m = i / NW, w = i - m * NW;
+      if (from[m] < 0) continue;
+      const int slot = slots[m], pos = slot & (p.L.psize - 1);
+      uint8_t* blk = p.pages + paged_block(p.L, slot >> p.L.pshift, h);
+      if (w < NK) body(i, blk + pos * (D / 2) + 4 * w, true);
+      else if (w < NK + NV) body(i, blk + p.L.voff + paged_v_word<D>(pos, (w - NK) & 7, (w - NK) >> 3), false);
+      else body(i, blk + p.L.soff + 4 * pos, true);
+    }
+  };
+  words(from, [&](int i, const uint8_t* at, bool whole) {
+    move_smem[i] = whole ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+  });
+  __syncthreads();
+  words(to, [&](int i, uint8_t* at, bool whole) {
+    if (whole) *reinterpret_cast<uint32_t*>(at) = move_smem[i];
+    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)move_smem[i];
+  });
+}
+
 // Grid over (rows, heads) x (K, V); 0 blocks: too many.
 static dim3 row_grid(int total, int nkv, int d) {
   const int per = 32 / (d / 32);
@@ -558,6 +585,37 @@ int ft_kv_read_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages,
   if (grid.x == 0) return FT_ERR_UNSUPPORTED;
   const auto kernel = c->head_dim == 128 ? ft::read_paged_kernel<128> : ft::read_paged_kernel<64>;
   return ft::launch_served(kernel, grid, dim3(ft::kRowThreads), 0, (cudaStream_t)stream, 1, p) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+}
+
+int ft_kv_move_paged_int4(const ft_block_cfg* c, void* pages, int n_pages, int page_size, const int32_t* src_slots,
+                          const int32_t* dst_slots, int B, int n, int32_t* dev_status, ft_stream stream) {
+  const int st = ft_host::check_paged(c, pages, n_pages, page_size);
+  if (st != FT_OK) return st;
+  if (B < 0 || n < 0) return FT_ERR_INVALID_ARG;
+  if (B == 0 || n == 0) return FT_OK;
+  if (!src_slots || !dst_slots) return FT_ERR_INVALID_ARG;
+  if (n > ft::kMoveMax || (int64_t)B * c->n_kv > INT32_MAX) return FT_ERR_UNSUPPORTED;
+  ft::MoveParams p = {};
+  p.src = src_slots;
+  p.dst = dst_slots;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.L = ft::paged_layout(*c, n_pages, page_size);
+  p.n = n;
+  p.status = dev_status;
+  const int words = c->head_dim / 8 + c->head_dim / 4 + 1;
+  const auto kernel = c->head_dim == 128 ? ft::move_paged_kernel<128> : ft::move_paged_kernel<64>;
+  static int allowed[64][2] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FT_ERR_CUDA;
+  int& ok = allowed[dev][c->head_dim == 128];
+  if (!ok) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ft::kMoveMax * words * 4) != cudaSuccess) return FT_ERR_CUDA;
+    ok = 1;
+  }
+  return ft::launch_served(kernel, dim3((unsigned)(B * c->n_kv)), dim3(ft::kMoveThreads), (size_t)n * words * 4, (cudaStream_t)stream, 1,
+                           p) == cudaSuccess
+             ? FT_OK
+             : FT_ERR_CUDA;
 }
 
 }  // extern "C"

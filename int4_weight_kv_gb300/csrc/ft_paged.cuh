@@ -123,6 +123,29 @@ __device__ __forceinline__ void paged_fwht(f32x2 (&v)[16], int hb) {
   }
 }
 
+// NaN where either is, else the larger.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kMagic = 12582912.0f;  // 1.5 2^23: |x| r + kMagic rounds to the nearest integer, ties to even
+
+// Magnitude of the code of y = fl(|x| norm) by scale s, min(rne(fl(y / s)), 7), decided without a
+// division where c = rne(y / s) is right but perhaps for the side of a boundary.  With t the
+// nearest boundary, y - t s is exact; the FP32 quotient is t itself (and the even neighbour its
+// code) while that is within half a step of t, else its sign decides.
+static __device__ __noinline__ float paged_edge(float y, float s, float c) {
+  if (!(s >= 1e-30f)) return s > 0.0f ? fminf(rintf(__fdiv_rn(y, s)), 7.0f) : 0.0f;
+  const float t = fmaf(-c, s, y) > 0.0f ? c + 0.5f : c - 0.5f, rem = fmaf(-t, s, y);
+  const float step = __uint_as_float((__float_as_uint(t) & 0x7F800000u) - (24u << 23));  // half a step above t
+  const float half = (rem < 0.0f && t == 0.5f) ? 0.5f * step : step;                     // below a power of two: half of it
+  const float lo = t - 0.5f, hi = t + 0.5f;
+  if (fabsf(rem) <= s * half) return ((int)lo & 1) ? hi : lo;
+  return fminf(rem > 0.0f ? hi : lo, 7.0f);
+}
+
 inline float paged_norm(int hb) { return (float)(1.0 / std::sqrt((double)hb)); }
 
 }  // namespace ft

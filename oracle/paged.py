@@ -8,6 +8,7 @@ the page layout is read word by word from its definition in include/ft.h.
 import numpy as np
 
 from .hadamard import blockdiag_apply
+from .rope import rope_apply
 
 
 def page_map(page_size, ctx, new, table, free, head=0, n_slots=None):
@@ -81,6 +82,52 @@ def attend_rows(q, k_hat, v_hat, had_block, scale, first_pos):
         vn[i] = w @ vlen[:seen]
         dn[i] = scale * np.max(np.abs(k_hat[:seen]) @ np.abs(qt[i]))
     return o, vn, dn
+
+
+def norm_rope(x, gamma, pos, base, eps):
+    """Rows x [heads, d] of one token: per-head RMS norm with gains gamma (None: none), then the rotation to pos."""
+    x = np.asarray(x, np.float64)
+    if gamma is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(gamma, np.float64)
+    return rope_apply(x, int(pos), base)
+
+
+def attend_seen(q, k_hat, v_hat, had_block, scale, seen):
+    """q [n, d] of one query head, k_hat and v_hat [len, d] (rotated entries), seen bool [n, len].  Returns what
+    attend_rows does."""
+    n, d = q.shape
+    qt = blockdiag_apply(q, had_block)
+    o, vn, dn = np.zeros((n, d)), np.zeros(n), np.zeros(n)
+    vlen = np.linalg.norm(v_hat, axis=-1)
+    for i in range(n):
+        j = np.nonzero(seen[i])[0]
+        if not len(j):
+            continue
+        s = scale * (k_hat[j] @ qt[i])
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        o[i] = blockdiag_apply(w @ v_hat[j], had_block)
+        vn[i] = w @ vlen[j]
+        dn[i] = scale * np.max(np.abs(k_hat[j]) @ np.abs(qt[i]))
+    return o, vn, dn
+
+
+def tree_rows(parents):
+    """Parents of one request's drafted tokens (-1: the history) -> bool [n, n]: itself and its ancestors."""
+    see = np.zeros((len(parents), len(parents)), bool)
+    for i, up in enumerate(parents):
+        if up >= 0:
+            see[i] = see[up]
+        see[i, i] = True
+    return see
+
+
+def mask_words(see, words):
+    """bool [n, m] -> int32 [n, words], bit j % 32 of word j / 32 for column j."""
+    bits = np.zeros((see.shape[0], 32 * words), np.uint64)
+    bits[:, :see.shape[1]] = see
+    w = (bits.reshape(-1, words, 32) << np.arange(32, dtype=np.uint64)).sum(-1)
+    return w.astype(np.uint32).view(np.int32)
 
 
 def logprobs(x, targets, top):

@@ -1,0 +1,121 @@
+"""Rows of the fused projection, draft trees, moved entries and prompt attention without a GPU: the
+oracle's pins and the refusals of the entry points (every call here returns before a launch)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import paged
+import synth
+
+FAKE = 4096  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def ft():
+    from int4_weight_kv_gb300 import build as b
+    b.build()
+    import int4_weight_kv_gb300 as m
+    return m
+
+
+# ---------------------------------------------------------------- oracle pins
+def test_tree_rows_hand_case():
+    #   0 - 1 - 3
+    #     \ 2        4 is another root
+    see = paged.tree_rows([-1, 0, 0, 1, -1])
+    want = [[1, 0, 0, 0, 0], [1, 1, 0, 0, 0], [1, 0, 1, 0, 0], [1, 1, 0, 1, 0], [0, 0, 0, 0, 1]]
+    np.testing.assert_array_equal(see, np.array(want, bool))
+    assert paged.mask_words(see, 1)[:, 0].tolist() == [1, 3, 5, 11, 16]
+    wide = np.zeros((1, 40), bool)
+    wide[0, [0, 31, 32, 39]] = True
+    assert paged.mask_words(wide, 2).tolist() == [[-(1 << 31) + 1, 1 + 128]]
+
+
+def test_attend_seen_is_attend_rows():
+    g = np.random.default_rng(5)
+    q, k, v = g.normal(size=(4, 64)), g.normal(size=(9, 64)), g.normal(size=(9, 64))
+    seen = np.arange(9)[None, :] <= 5 + np.arange(4)[:, None]
+    for a, b in zip(paged.attend_seen(q, k, v, 32, 0.1, seen), paged.attend_rows(q, k, v, 32, 0.1, 5)):
+        np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-14)
+    seen[2] = False
+    assert not paged.attend_seen(q, k, v, 32, 0.1, seen)[0][2].any()
+
+
+def test_norm_rope_closed_forms():
+    x = np.full((1, 64), 3.0)
+    np.testing.assert_allclose(paged.norm_rope(x, np.full(64, 2.0), 0, 1e4, 0.0), np.full((1, 64), 2.0))
+    g = np.random.default_rng(1)
+    y = g.normal(size=(2, 128))
+    z = paged.norm_rope(y, None, 7, 1e4, 1e-5)
+    np.testing.assert_allclose(np.linalg.norm(z, axis=-1), np.linalg.norm(y, axis=-1))
+    c = (y[:, :64] + 1j * y[:, 64:]) * np.exp(7j * 1e4 ** (-np.arange(64) / 64))
+    np.testing.assert_allclose(z, np.concatenate([c.real, c.imag], -1), atol=1e-12)
+
+
+# ---------------------------------------------------------------- refusals
+def _caller(name, ft, c, ok, tail):
+    fn = getattr(ft.lib(), name)
+    return lambda **o: fn(ctypes.byref(c), *dict(ok, **o).values(), *tail)
+
+
+def test_norm_rope_refusals(ft):
+    c = ft.cfg_from_shape(synth.L8B)
+    ok = dict(q=FAKE, qs=4096, k=FAKE, ks=1024, gq=None, gk=None, pos=FAKE, total=3, qo=FAKE, qos=4096, ko=FAKE, kos=1024)
+    call = _caller("ft_qk_norm_rope_bf16", ft, c, ok, (None,))
+    assert call(total=0) == ft.FT_OK and call(total=0, q=None, qo=None) == ft.FT_OK
+    for bad in (dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(q=None, qo=None, k=None, ko=None), dict(total=-1),
+                dict(pos=None), dict(qs=4095), dict(ks=1023), dict(qos=4095), dict(kos=0)):
+        assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
+    call = _caller("ft_qk_norm_rope_bf16", ft, ft.make_cfg(512, 8, 2, 96, 512, had_block=32), ok, (None,))
+    assert call() == ft.FT_ERR_UNSUPPORTED
+
+
+def test_append_rope_refusals(ft):
+    c = ft.cfg_from_shape(synth.L8B)
+    ok = dict(pages=FAKE, n=8, ps=64, k=FAKE, ks=1024, v=FAKE, vs=1024, gk=None, pos=FAKE, slots=FAKE, total=3, q=None, qs=0,
+              gq=None, qo=None, qos=0)
+    call = _caller("ft_kv_append_rope_paged_int4", ft, c, ok, (None, None))
+    assert call(total=0) == ft.FT_OK and call(ps=8) == ft.FT_ERR_UNSUPPORTED
+    for bad in (dict(pages=None), dict(pages=FAKE + 8), dict(n=0), dict(k=None), dict(v=None), dict(slots=None), dict(pos=None),
+                dict(total=-1), dict(ks=1023), dict(vs=0), dict(q=FAKE), dict(qo=FAKE), dict(q=FAKE, qo=FAKE, qs=4096, qos=4095),
+                dict(q=FAKE, qo=FAKE, qs=100, qos=4096)):
+        assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
+
+
+def test_move_refusals(ft):
+    c = ft.cfg_from_shape(synth.L8B)
+    ok = dict(pages=FAKE, n=8, ps=64, src=FAKE, dst=FAKE, B=2, m=4)
+    call = _caller("ft_kv_move_paged_int4", ft, c, ok, (None, None))
+    assert call(B=0) == ft.FT_OK and call(m=0) == ft.FT_OK
+    assert call(ps=48) == ft.FT_ERR_UNSUPPORTED and call(m=257) == ft.FT_ERR_UNSUPPORTED and call(B=2 ** 29) == ft.FT_ERR_UNSUPPORTED
+    for bad in (dict(pages=None), dict(pages=FAKE + 4), dict(n=0), dict(src=None), dict(dst=None), dict(B=-1), dict(m=-1)):
+        assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
+
+
+def test_tree_refusals(ft):
+    c = ft.cfg_from_shape(synth.L8B)
+    size = ft.ft_attn_tree_workspace_bytes(c, 4, 100, 40)
+    assert size > 0 and ft.ft_attn_tree_workspace_bytes(c, 0, 100, 40) == 0 and ft.ft_attn_tree_workspace_bytes(c, 4, 100, 0) == 0
+    ok = dict(pages=FAKE, n=8, ps=64, q=FAKE, qs=4096, cu=FAKE, kv=FAKE, table=FAKE, stride=4, mask=FAKE, ms=2, B=4, total=100,
+              max_q=40, scale=0.1, o=FAKE, os=4096, ws=FAKE, wsb=size)
+    call = _caller("ft_attn_tree_paged_int4", ft, c, ok, (None, None))
+    assert call(total=0) == ft.FT_OK and call(wsb=size - 1) == ft.FT_ERR_WORKSPACE and call(ps=40) == ft.FT_ERR_UNSUPPORTED
+    for big in (dict(total=2 ** 29), dict(stride=2 ** 28), dict(B=8193)):
+        assert call(wsb=2 ** 60, **big) == ft.FT_ERR_UNSUPPORTED, big
+    for bad in (dict(pages=None), dict(q=None), dict(o=None), dict(cu=None), dict(kv=None), dict(table=None), dict(ws=None),
+                dict(ws=FAKE + 4), dict(B=0), dict(total=-1), dict(max_q=0), dict(stride=0), dict(qs=4095), dict(os=1),
+                dict(scale=0.0), dict(scale=float("nan")), dict(mask=None), dict(mask=FAKE + 2), dict(ms=1), dict(ms=0)):
+        assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
+
+
+def test_prompt_refusals(ft):
+    c = ft.cfg_from_shape(synth.L8B)
+    ok = dict(q=FAKE, qs=4096, k=FAKE, ks=1024, v=FAKE, vs=1024, cu=FAKE, B=4, total=100, max_len=40, scale=0.1, o=FAKE, os=4096)
+    call = _caller("ft_attn_prompt_bf16", ft, c, ok, (None, None))
+    assert call(total=0) == ft.FT_OK
+    assert call(B=8193) == ft.FT_ERR_UNSUPPORTED and call(total=2 ** 29) == ft.FT_ERR_UNSUPPORTED
+    for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(cu=None), dict(B=0), dict(total=-1), dict(max_len=0),
+                dict(qs=4095), dict(ks=1023), dict(vs=1023), dict(os=0), dict(scale=0.0), dict(scale=float("inf")), dict(k=FAKE + 8),
+                dict(v=FAKE + 2), dict(ks=1028), dict(vs=1025)):
+        assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
