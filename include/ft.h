@@ -336,14 +336,15 @@ int ft_kv_append_rope_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pag
 /* Causal attention of whole prompts over their own rows (post-RoPE BF16, not quantised): sequence b owns rows
  * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q, k, v and o, and its row i attends to its rows 0 .. i:
  *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,   query head h reads KV head h / G.
- * q, o: [total, n_q, d], k, v: [total, n_kv, d] at their strides (elements); k and v at 16-byte boundaries with
- * strides of a multiple of 8, else FT_ERR_INVALID_ARG; o may be q where the strides are equal.  Rows that no
+ * q, o: [total, n_q, d], k, v: [total, n_kv, d] at their strides (elements); q, k and v at 16-byte
+ * boundaries with strides of a multiple of 8, else FT_ERR_INVALID_ARG; o may be q where the strides are equal.  Rows that no
  * sequence owns are left as they are.  max_len: an upper bound of the lengths; it sizes the launch.
  * Arithmetic: BF16 products, FP32 sums, maxima and statistics, weights rounded to BF16 below the second
  * product (2^-8 each).  A row that sees a k or v which is not finite is not finite in the channels
  * concerned (it may be NaN in all of them); rows that do not see it, and other sequences, are not touched.
  * Device conditions: cu_seqlens not ascending within [0, total], or a length above max_len: FT_DEV_RANGE, that
- * sequence's rows are not written.  B <= 8192, total n_q / n_kv < 2^31, else FT_ERR_UNSUPPORTED. */
+ * sequence's rows are not written.  B <= 8192, total n_q / n_kv < 2^31, strides below 2^39, else
+ * FT_ERR_UNSUPPORTED. */
 int ft_attn_prompt_bf16(const ft_block_cfg *cfg, const uint16_t *q_bf16, int64_t q_stride, const uint16_t *k_bf16,
                         int64_t k_stride, const uint16_t *v_bf16, int64_t v_stride, const int32_t *cu_seqlens, int B,
                         int total, int max_len, float scale, uint16_t *o_bf16, int64_t o_stride, int32_t *dev_status,

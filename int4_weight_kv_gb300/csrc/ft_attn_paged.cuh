@@ -74,12 +74,7 @@ __device__ __forceinline__ bool attn_request(const AttnPagedParams& p, int b, in
   return true;
 }
 
-// MUFU operations without the denormal handling of the library functions.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+// (as ex2: without the denormal handling of the library functions)
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -117,5 +117,6 @@ def test_prompt_refusals(ft):
     assert call(B=8193) == ft.FT_ERR_UNSUPPORTED and call(total=2 ** 29) == ft.FT_ERR_UNSUPPORTED
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(cu=None), dict(B=0), dict(total=-1), dict(max_len=0),
                 dict(qs=4095), dict(ks=1023), dict(vs=1023), dict(os=0), dict(scale=0.0), dict(scale=float("inf")), dict(k=FAKE + 8),
-                dict(v=FAKE + 2), dict(ks=1028), dict(vs=1025)):
+                dict(v=FAKE + 2), dict(ks=1028), dict(vs=1025), dict(q=FAKE + 2), dict(qs=4100)):
         assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
+    assert call(ks=2 ** 40) == ft.FT_ERR_UNSUPPORTED

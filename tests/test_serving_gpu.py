@@ -275,7 +275,7 @@ class Tree(Attn):
                 tol = (2.0 ** -10 * dn + 2.0 ** -11 + 2.0 ** -16) * vn + 2.0 ** -8 * np.linalg.norm(o64, axis=-1)
                 tol += kv * floor * vs[pages, j].reshape(-1)[:kv].max(initial=0.0) * 7 * self.d ** 0.5
                 assert not got[rows, h][vn == 0].any()
-                assert np.all(err <= tol), (b, h, float(np.max(err / np.maximum(tol, 1e-300))))
+                assert (err <= tol).all(), (b, h, float(np.max(err / np.maximum(tol, 1e-300))))
 
 
 TREES = [
@@ -414,7 +414,7 @@ class Prompt:
                 dn = (self.scale * (q[at].abs() @ k.abs().T).masked_fill(late, 0).amax(-1)).cpu().numpy()
                 err = np.linalg.norm(got[a:z, h][at.cpu().numpy()] - o64, axis=-1)
                 tol = (2.0 ** -16 * dn + 2.0 ** -8 + 2.0 ** -15) * vn + 2.0 ** -8 * np.linalg.norm(o64, axis=-1)
-                assert np.all(err <= tol), (b, h, float(np.max(err / np.maximum(tol, 1e-300))))
+                assert (err <= tol).all(), (b, h, float(np.max(err / np.maximum(tol, 1e-300))))
 
 
 PROMPTS = [
