@@ -29,8 +29,9 @@ namespace prompt {
 using namespace tiles;
 
 constexpr int kThreads = 384, kKeys = 128;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kLookWarp = 10, kLookThreads = 64;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLookWarp = 11;  // (two issuing warps)
 constexpr float kLazy = 8.0f;
+constexpr int kPassLeft = 3;  // products of a batch issued behind the turn's end
 // Registers of a thread: softmax twice, the others; the sum over the three warpgroups is what the block is
 // launched with, kThreads x kRegLaunch.
 constexpr int kRegSoftmax = 208, kRegOther = 88, kRegLaunch = 168;
@@ -138,20 +139,23 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
     }
   }
   const uint32_t bar = sm32 + C::kOffBar;
-  const uint32_t q_full = bar, s_full = bar + 8, p_full = bar + 24, o_full = bar + 40, drained = bar + 56, looked = bar + 64, full = bar + 88,
+  const uint32_t q_full = bar, s_full = bar + 8, p_full = bar + 24, o_full = bar + 40, drained = bar + 56, looked = bar + 64,
+                 p_half = bar + 88, turn = bar + 104, full = bar + 120,
                  empty = full + 8 * C::kSlots;
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
+      mbar_init(p_half + 8 * i, 128);
+      mbar_init(turn + 8 * i, 1);
       mbar_init(o_full + 8 * i, 1);
     }
-    mbar_init(drained, 1);
-    for (int i = 0; i < 3; ++i) mbar_init(looked + 8 * i, kLookThreads);
+    mbar_init(drained, 2);
+    for (int i = 0; i < 3; ++i) mbar_init(looked + 8 * i, 32);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 3);  // the products', and both looking warps': they follow every tile, so that none passes them by
+      mbar_init(empty + 8 * i, 3);  // both issuing warps' products, and the looking warp: it follows every tile, so that none passes it by
     }
     mbar_fence_init();
   }
@@ -236,6 +240,11 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
             o[(c - 64 * g) / 2] = *reinterpret_cast<const uint32_t*>(&v);
           }
           tmem_st32(tmem + lane_base + 128 * t + 32 * g, o);
+          if (g == 0) {
+            wait_st();
+            fence_before();
+            mbar_arrive(p_half + 8 * t);
+          }
         }
         float a, c;
         add2(sum[0], sum[1]).get(a, c);
@@ -261,29 +270,45 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
       if (ok) {
         fence_after();
         const float inv = 1.0f / l;
-        const bool store = row < per_tile * p.G && tok < n;
-        uint16_t* dst = p.o + (row0 + (store ? tok : 0)) * p.o_stride + (int64_t)(h * p.G + row % p.G) * D;
-        const bool wide = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-#pragma unroll
+        // Each four lanes exchange 16-byte pieces, so that they store 64 bytes of a row together (a row a lane
+        // takes the load-store unit a cycle a lane: 4.2 thousand cycles for the tile).
+        const int quad = lane & 3, r_first = row & ~3;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
+          uint32_t o[32], w[4][4];
           tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o);
           wait_ld();
-          if (!store) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const __nv_bfloat162 v =
                   __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-              w[k] = *reinterpret_cast<const uint32_t*>(&v);
+              w[i][k] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            if (wide) {
-              *reinterpret_cast<uint4*>(dst + c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int x = 2; x > 0; x >>= 1)  // w[i] of lane q goes to w[q] of lane i
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i & x) continue;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool up = quad & x;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i][k] : w[i + x][k], x);
+                if (up) w[i][k] = got;
+                else w[i + x][k] = got;
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r_first + i, to = tok0 + t * per_tile + r / p.G;
+            if (r >= per_tile * p.G || to >= n) continue;
+            uint16_t* dst = p.o + (row0 + to) * p.o_stride + (int64_t)(h * p.G + r % p.G) * D + c + 8 * quad;
+            if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) dst[c + 8 * i + 2 * k] = (uint16_t)w[k], dst[c + 8 * i + 2 * k + 1] = (uint16_t)(w[k] >> 16);
+              for (int k = 0; k < 4; ++k) dst[2 * k] = (uint16_t)w[i][k], dst[2 * k + 1] = (uint16_t)(w[i][k] >> 16);
             }
           }
         }
@@ -317,58 +342,81 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         for (int i = max(0, done - C::kSlots); i < done; ++i)
           if (!mbar_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1)) ok = false;
       }
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------- tensor-core issue
+    } else if (warp < kLookWarp) {
+      // ---------------------------------------------------------- tensor-core issue, a warp for each tile
       constexpr uint32_t id_qk = idesc_bf16(128, kKeys), id_pv = idesc_bf16(128, D) | kBMn;
       const uint32_t lead = lane == 0 ? 1u : 0u, tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t q_lo = desc_lo(sm32 + C::kOffQ), ring = sm32 + C::kOffRing;
-      auto qk = [&](int t, int j) {
-        const uint32_t qa = q_lo + t * (C::kTile >> 4), ka = desc_lo(ring + (2 * j) % C::kSlots * C::kTile), d = tm + 128 * t;
-        mma_ss<false>(d, qa, ka, id_qk, lead);
+      const int t = warp - kMmaWarp, mine = t == 0 ? nkt0 : nkt;
+      const uint32_t ds = tm + 128 * t, d_o = tm + C::kColO + D * t, qa = q_lo + t * (C::kTile >> 4);
+      // the last products of Q K^T are issued when the other tile's turn has begun: no gap between the two
+      auto qk = [&](int j, auto&& pass) {
+        const uint32_t ka = desc_lo(ring + (2 * j) % C::kSlots * C::kTile);
+        mma_ss<false>(ds, qa, ka, id_qk, lead);
 #pragma unroll
         for (int ks = 1; ks < D / 16; ++ks) {
           const uint32_t o = ((ks / 4) * (128 * 128) + 32 * (ks % 4)) >> 4;
-          mma_ss<true>(d, qa + o, ka + o, id_qk, lead);
+          if (ks == D / 16 - kPassLeft) pass();
+          mma_ss<true>(ds, qa + o, ka + o, id_qk, lead);
         }
         commit(s_full + 8 * t, lead);
       };
-      auto pv = [&](int t, int j) {
-        const uint32_t va = desc_lo_mn(ring + (2 * j + 1) % C::kSlots * C::kTile), d = tm + C::kColO + D * t, pa = tm + 128 * t;
+      auto pv = [&](int j, int half) {
+        const uint32_t va = desc_lo_mn(ring + (2 * j + 1) % C::kSlots * C::kTile);
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks) mma_ts(d, pa + 8 * ks, va + ((ks * 2048) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
+        for (int k = 0; k < 4; ++k) {
+          const int ks = 4 * half + k;
+          mma_ts(d_o, ds + 8 * ks, va + ((ks * 2048) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
+        }
       };
       auto arrived = [&](int i) { return all_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1); };
-      if (nkt > 0) {
+      // (a tile that is not there, or that does not see the last positions, lets go of what it leaves out)
+      auto release = [&](int i) { commit(empty + 8 * (i % C::kSlots), lead); };
+      if (t < ntile) {
         ok = all_wait(q_full, 0) && arrived(0);
         if (ok) {
           fence_after();
-          for (int t = 0; t < ntile; ++t) qk(t, 0);
-          commit(empty, lead);
+          qk(0, [] {});
         }
-      }
-      for (int j = 0; ok && j < nkt; ++j) {
-        ok = arrived(2 * j + 1) && (j < part || all_wait(looked + 8 * (j - part), 0)) && (j + 1 >= nkt || arrived(2 * j + 2));
-        for (int t = 0; ok && t < ntile; ++t) {
-          const int mine = t == 0 ? nkt0 : nkt;
-          if (j >= mine) continue;
+        // The tiles take the tensor core by turns, tile 0 first: left alone they fall into step, both softmaxes at
+        // once and then both tiles' products.
+        const bool turns = ntile == 2;
+        auto pass = [&] {
+          if (turns && lead) mbar_arrive(turn + 8 * (t ^ 1));
+        };
+        for (int j = 0; ok && j < mine; ++j) {
+          release(2 * j);
+          ok = arrived(2 * j + 1) && (j < part || all_wait(looked + 8 * (j - part), 0)) && (j + 1 >= mine || arrived(2 * j + 2)) &&
+               all_wait(p_half + 8 * t, j & 1) && (!turns || (t == 0 && j == 0) || all_wait(turn + 8 * t, t == 0 ? (j - 1) & 1 : j & 1));
+          if (!ok) break;
+          fence_after();
+          pv(j, 0);
           ok = all_wait(p_full + 8 * t, j & 1);
           if (!ok) break;
           fence_after();
-          pv(t, j);
-          if (j + 1 < mine) qk(t, j + 1);
-          else commit(o_full + 8 * t, lead);
+          pv(j, 1);
+          release(2 * j + 1);
+          if (j + 1 < mine) {
+            qk(j + 1, pass);
+          } else {
+            commit(o_full + 8 * t, lead);
+            pass();
+          }
         }
-        if (ok && j + 1 < nkt) {
-          commit(empty + 8 * ((2 * j + 1) % C::kSlots), lead);
-          commit(empty + 8 * ((2 * j + 2) % C::kSlots), lead);
+        for (int j = mine; ok && t == 0 && j < nkt; ++j) {  // tile 1 goes on alone
+          ok = all_wait(turn, (j - 1) & 1);
+          pass();
         }
+      }
+      for (int i = t < ntile ? 2 * mine : 0; ok && i < 2 * nkt; ++i) {
+        ok = arrived(i);
+        if (ok) release(i);
       }
       // tensor memory is freed only when nothing issued here is in flight
       commit(drained, lead);
       if (!all_wait(drained, 0)) ok = false;
     } else {
       // ---------------------------------------------------------- V tiles that some row sees in part
-      const int me = tid - 32 * kLookWarp;
       for (int i = 0; i < 2 * nkt; ++i) {
         if (!all_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1)) {
           ok = false;
@@ -380,7 +428,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
           continue;
         }
         uint8_t* v = sm + C::kOffRing + (i % C::kSlots) * C::kTile;
-        for (int r = me; r < kKeys; r += kLookThreads) {
+        for (int r = lane; r < kKeys; r += 32) {
           const int key = kKeys * j + r;
           if (key <= tok0) continue;  // every row sees it
           bool clear = key >= n;
