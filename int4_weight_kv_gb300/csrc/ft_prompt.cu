@@ -31,7 +31,7 @@ using namespace tiles;
 constexpr int kThreads = 384, kKeys = 128;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLookWarp = 11;  // (two issuing warps)
 constexpr float kLazy = 8.0f;
-constexpr int kPassLeft = 3;  // products of a batch issued behind the turn's end
+constexpr int kPassLeft = 1;  // products of a batch issued behind the end of its turn (1, 2, 3, 5: 344, 349, 360, 371 us for 8192 tokens)
 // Registers of a thread: softmax twice, the others; the sum over the three warpgroups is what the block is
 // launched with, kThreads x kRegLaunch.
 constexpr int kRegSoftmax = 208, kRegOther = 88, kRegLaunch = 168;
@@ -42,7 +42,7 @@ struct Cfg {
   static constexpr int kTile = 128 * D * 2;              // Q, K or V: 128 rows
   static constexpr int kSlots = D == 128 ? 5 : 8;         // of the ring that K and V tiles come through: K0 V0 K1 V1 ...
   static constexpr int kOffQ = 0, kOffRing = 2 * kTile, kOffBar = kOffRing + kSlots * kTile;
-  static constexpr int kSmem = kOffBar + 256 + 1024;      // 1024: alignment slack
+  static constexpr int kSmem = kOffBar + 512 + 1024;      // 1024: alignment slack
   static constexpr int kColO = 256;                       // tensor memory: S0, S1, then O0, O1
 };
 
@@ -139,15 +139,14 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
     }
   }
   const uint32_t bar = sm32 + C::kOffBar;
-  const uint32_t q_full = bar, s_full = bar + 8, p_full = bar + 24, o_full = bar + 40, drained = bar + 56, looked = bar + 64,
-                 p_half = bar + 88, turn = bar + 104, full = bar + 120,
+  const uint32_t q_full = bar, s_full = bar + 8, o_full = bar + 24, drained = bar + 40, looked = bar + 48, turn = bar + 72,
+                 p_part = bar + 88, full = bar + 136,
                  empty = full + 8 * C::kSlots;
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 128);
-      mbar_init(p_half + 8 * i, 128);
+      for (int k = 0; k < 3; ++k) mbar_init(p_part + 16 * k + 8 * i, 128);
       mbar_init(turn + 8 * i, 1);
       mbar_init(o_full + 8 * i, 1);
     }
@@ -228,30 +227,27 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         const f32x2 scale2(p.scale, p.scale), u2(u, u);
         f32x2 sum[2] = {f32x2(0.0f, 0.0f), f32x2(0.0f, 0.0f)};
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t o[32];
+        for (int g = 0; g < 4; ++g) {
+          uint32_t o[16];
 #pragma unroll
-          for (int c = 64 * g; c < 64 * g + 64; c += 2) {
+          for (int c = 32 * g; c < 32 * g + 32; c += 2) {
             float x0, x1;
             fma2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, u2).get(x0, x1);
             x0 = ex2(x0), x1 = ex2(x1);
             sum[(c / 2) & 1] = add2(sum[(c / 2) & 1], f32x2(x0, x1));
             const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
-            o[(c - 64 * g) / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            o[(c - 32 * g) / 2] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          tmem_st32(tmem + lane_base + 128 * t + 32 * g, o);
-          if (g == 0) {
+          tmem_st16(tmem + lane_base + 128 * t + 16 * g, o);
+          if (g > 0) {  // P is handed over in a half and two quarters
             wait_st();
             fence_before();
-            mbar_arrive(p_half + 8 * t);
+            mbar_arrive(p_part + 16 * (g - 1) + 8 * t);
           }
         }
         float a, c;
         add2(sum[0], sum[1]).get(a, c);
         l += a + c;
-        wait_st();
-        fence_before();
-        mbar_arrive(p_full + 8 * t);
       }
       // a row of V that is not finite, among those that this row sees
       for (int j = part; ok && j < mine; ++j) {
@@ -361,13 +357,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         }
         commit(s_full + 8 * t, lead);
       };
-      auto pv = [&](int j, int half) {
+      auto pv = [&](int j, int from, int to) {
         const uint32_t va = desc_lo_mn(ring + (2 * j + 1) % C::kSlots * C::kTile);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int ks = 4 * half + k;
-          mma_ts(d_o, ds + 8 * ks, va + ((ks * 2048) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
-        }
+        for (int ks = from; ks < to; ++ks) mma_ts(d_o, ds + 8 * ks, va + ((ks * 2048) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
       };
       auto arrived = [&](int i) { return all_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1); };
       // (a tile that is not there, or that does not see the last positions, lets go of what it leaves out)
@@ -387,14 +380,18 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         for (int j = 0; ok && j < mine; ++j) {
           release(2 * j);
           ok = arrived(2 * j + 1) && (j < part || all_wait(looked + 8 * (j - part), 0)) && (j + 1 >= mine || arrived(2 * j + 2)) &&
-               all_wait(p_half + 8 * t, j & 1) && (!turns || (t == 0 && j == 0) || all_wait(turn + 8 * t, t == 0 ? (j - 1) & 1 : j & 1));
+               all_wait(p_part + 8 * t, j & 1) && (!turns || (t == 0 && j == 0) || all_wait(turn + 8 * t, t == 0 ? (j - 1) & 1 : j & 1));
           if (!ok) break;
           fence_after();
-          pv(j, 0);
-          ok = all_wait(p_full + 8 * t, j & 1);
+          pv(j, 0, 4);
+          ok = all_wait(p_part + 16 + 8 * t, j & 1);
           if (!ok) break;
           fence_after();
-          pv(j, 1);
+          pv(j, 4, 6);
+          ok = all_wait(p_part + 32 + 8 * t, j & 1);
+          if (!ok) break;
+          fence_after();
+          pv(j, 6, 8);
           release(2 * j + 1);
           if (j + 1 < mine) {
             qk(j + 1, pass);
