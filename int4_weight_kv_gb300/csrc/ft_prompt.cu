@@ -31,6 +31,8 @@ using namespace tiles;
 constexpr int kThreads = 384, kKeys = 128;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLookWarp = 11;  // (two issuing warps)
 constexpr float kLazy = 8.0f;
+constexpr int kWorks = 2;  // items known ahead
+constexpr int kLooks = 8;  // partly visible tiles of V looked through ahead: more than the ring holds, and one item's, together
 constexpr int kPassLeft = 1;  // products of a batch issued behind the end of its turn (1, 2, 3, 5: 344, 349, 360, 371 us for 8192 tokens)
 // Registers of a thread: softmax twice, the others; the sum over the three warpgroups is what the block is
 // launched with, kThreads x kRegLaunch.
@@ -42,7 +44,7 @@ struct Cfg {
   static constexpr int kTile = 128 * D * 2;              // Q, K or V: 128 rows
   static constexpr int kSlots = D == 128 ? 5 : 8;         // of the ring that K and V tiles come through: K0 V0 K1 V1 ...
   static constexpr int kOffQ = 0, kOffRing = 2 * kTile, kOffBar = kOffRing + kSlots * kTile;
-  static constexpr int kSmem = kOffBar + 512 + 1024;      // 1024: alignment slack
+  static constexpr int kBars = 512, kSmem = kOffBar + kBars + 1024;  // 1024: alignment slack
   static constexpr int kColO = 256;                       // tensor memory: S0, S1, then O0, O1
 };
 
@@ -83,75 +85,68 @@ __device__ __forceinline__ bool sequence(const Params& p, int b, int32_t* status
   return true;
 }
 
+// What a CTA works on: tokens tok0, tok0 + 1, ... of one sequence for KV head h, and what follows from them.
+struct Item {
+  int tok0, row0, n, h;  // tok0 < 0: no more
+  int ntile, nkt, nkt0, part;
+  __device__ __forceinline__ Item(const Params& p, int4 w) : tok0(w.x), row0(w.y), n(w.z), h(w.w) {
+    const int per_tile = 128 / p.G, end = min(tok0 + p.ntile * per_tile, n);
+    ntile = (end - tok0 + per_tile - 1) / per_tile;
+    nkt = (end + kKeys - 1) / kKeys;  // position tiles that the last tile of rows sees, and
+    nkt0 = (min(tok0 + per_tile, n) + kKeys - 1) / kKeys;  // the first one
+    part = (tok0 + 1) / kKeys;  // from this tile on (three at most) some row sees a position that another does not
+  }
+};
+
+// A place in a ring of N barriers: slot and the parity of its current use.
+template <int N>
+struct Cursor {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, parity ^= 1;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D>;
+  using Ring = Cursor<C::kSlots>;
   extern __shared__ uint8_t prompt_smem[];
   const uint32_t raw = smem_u32(prompt_smem);
   uint8_t* sm = prompt_smem + ((1024 - (raw & 1023)) & 1023);
   const uint32_t sm32 = smem_u32(sm);
-  __shared__ int find[3];  // first token of the CTA's (-1: no work), the sequence's first row, its tokens
-  __shared__ int warp_tot[kThreads / 32];
+  __shared__ __align__(16) int4 work[kWorks];
+  __shared__ __align__(16) uint32_t answer[4];  // of the request for another CTA's place
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t poison[3][4];  // rows of V that are not finite, by partly visible tile
+  __shared__ uint32_t poison[kLooks][4];  // rows of V that are not finite, by partly visible tile
   auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
+  const int per_tile = 128 / p.G;
 
-  // ---- which rows: block `want` of all sequences' blocks of tokens, the last ones (which see most) first
-  const int per_tile = 128 / p.G, per_cta = p.ntile * per_tile;  // tokens
-  const int h = blockIdx.x % p.nkv, want = blockIdx.x / p.nkv;
-  {
-    auto blocks = [&](int b, int32_t* status, int& row0, int& n) {
-      return sequence(p, b, status, row0, n) ? (n + per_cta - 1) / per_cta : 0;
-    };
-    int32_t* status = blockIdx.x == 0 ? p.status : nullptr;
-    if (tid == 0) find[0] = -1;
-    if (tid < 12) poison[tid / 4][tid % 4] = 0u;
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    int sum = 0, row0, n;
-    for (int b = b0; b < b1; ++b) sum += blocks(b, status, row0, n);
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    int at = inc - sum, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += warp_tot[w];
-      total += warp_tot[w];
-    }
-    const int i = total - 1 - want;
-    if (i >= at && i < at + sum) {
-      for (int b = b0; b < b1; ++b) {
-        const int nb = blocks(b, nullptr, row0, n);
-        if (i < at + nb) {
-          find[0] = (i - at) * per_cta, find[1] = row0, find[2] = n;
-          break;
-        }
-        at += nb;
-      }
-    }
-  }
   const uint32_t bar = sm32 + C::kOffBar;
-  const uint32_t q_full = bar, s_full = bar + 8, o_full = bar + 24, drained = bar + 40, looked = bar + 48, turn = bar + 72,
-                 p_part = bar + 88, full = bar + 136,
-                 empty = full + 8 * C::kSlots;
-  if (tid == 0) {
-    mbar_init(q_full, 1);
+  const uint32_t q_full = bar, q_empty = bar + 16, s_full = bar + 32, o_full = bar + 48, turn = bar + 64, p_part = bar + 80,
+                 work_full = bar + 128, work_empty = work_full + 8 * kWorks, answered = work_empty + 8 * kWorks, drained = answered + 8,
+                 looked = drained + 8, full = looked + 8 * kLooks, empty = full + 8 * C::kSlots;
+  static_assert(128 + 16 * kWorks + 16 + 8 * kLooks + 16 * C::kSlots <= C::kBars, "barriers");
+  if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      for (int k = 0; k < 3; ++k) mbar_init(p_part + 16 * k + 8 * i, 128);
-      mbar_init(turn + 8 * i, 1);
       mbar_init(o_full + 8 * i, 1);
+      mbar_init(turn + 8 * i, 1);
+      for (int k = 0; k < 3; ++k) mbar_init(p_part + 16 * k + 8 * i, 128);
     }
+    for (int i = 0; i < kWorks; ++i) {
+      mbar_init(work_full + 8 * i, 1);
+      mbar_init(work_empty + 8 * i, 8 + 2 + 1);  // the warps of softmax, issue and looking
+    }
+    mbar_init(answered, 1);
     mbar_init(drained, 2);
-    for (int i = 0; i < 3; ++i) mbar_init(looked + 8 * i, 32);
+    for (int i = 0; i < kLooks; ++i) mbar_init(looked + 8 * i, 32);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 3);  // both issuing warps' products, and the looking warp: it follows every tile, so that none passes it by
@@ -166,26 +161,38 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  const int tok0 = uni(find[0]), row0 = uni(find[1]), n = uni(find[2]);
-  const int end = min(tok0 + per_cta, n);                             // this CTA's tokens: tok0 .. end - 1
-  const int ntile = tok0 < 0 ? 0 : min(p.ntile, (end - tok0 + per_tile - 1) / per_tile);
-  auto tiles_of = [&](int t) { return (min(tok0 + (t + 1) * per_tile, n) + kKeys - 1) / kKeys; };  // position tiles that tile t sees
-  const int nkt = ntile > 0 ? tiles_of(ntile - 1) : 0, nkt0 = ntile > 0 ? tiles_of(0) : 0;
-  const int part = (tok0 + 1) / kKeys;  // from this tile on (three at most) some row sees a position that another does not
+  griddep_serve();  // (barriers and tensor memory are set up beside the kernel before this one)
   bool ok = true;
+  // The k-th item, for a whole warp; tok0 < 0 behind the last one, or where the wait ran out.
+  auto take = [&](uint32_t k) {
+    const int slot = k % kWorks;
+    int4 w = make_int4(-1, 0, 0, 0);
+    if (all_wait(work_full + 8 * slot, (k / kWorks) & 1)) w = work[slot];
+    else ok = false;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(work_empty + 8 * slot);
+    return make_int4(uni(w.x), uni(w.y), uni(w.z), uni(w.w));
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax: one row per thread
     regs_up<kRegSoftmax>();
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    if (t < ntile) {
-      const int tok = tok0 + t * per_tile + row / p.G;             // (may be behind the last one: not stored)
-      const int seen = tok0 + t * per_tile + 32 * (warp & 3) / p.G;  // every row of the warp sees this position
-      const int mine = t == 0 ? nkt0 : nkt;
+    uint32_t tiles_done = 0, items_done = 0, looks_done = 0;
+    for (uint32_t k = 0; ok; ++k) {
+      const int4 got = take(k);
+      if (got.x < 0) break;
+      const Item w(p, got);
+      const uint32_t look0 = looks_done;
+      looks_done += w.nkt - w.part;
+      if (t >= w.ntile) continue;
+      const int tok = w.tok0 + t * per_tile + row / p.G;                     // (may be behind the last one: not stored)
+      const int seen = w.tok0 + t * per_tile + 32 * (warp & 3) / p.G;  // every row of the warp sees this position
+      const int mine = t == 0 ? w.nkt0 : w.nkt;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < mine; ++j) {
-        if (!all_wait(s_full + 8 * t, j & 1)) {
+      for (int j = 0; j < mine; ++j, ++tiles_done) {
+        if (!all_wait(s_full + 8 * t, tiles_done & 1)) {
           ok = false;
           break;
         }
@@ -250,19 +257,21 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         l += a + c;
       }
       // a row of V that is not finite, among those that this row sees
-      for (int j = part; ok && j < mine; ++j) {
-        if (!all_wait(looked + 8 * (j - part), 0)) {
+      for (int j = w.part; ok && j < mine; ++j) {
+        const uint32_t look = look0 + (j - w.part);
+        if (!all_wait(looked + 8 * (look % kLooks), (look / kLooks) & 1)) {
           ok = false;
           break;
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int lim = tok - kKeys * j - 32 * g;
-          const uint32_t bits = poison[j - part][g] & (lim < 0 ? 0u : lim >= 31 ? 0xFFFFFFFFu : (2u << lim) - 1u);
+          const uint32_t bits = poison[look % kLooks][g] & (lim < 0 ? 0u : lim >= 31 ? 0xFFFFFFFFu : (2u << lim) - 1u);
           if (bits) l = __uint_as_float(0x7FC00000u);
         }
       }
-      if (ok && !all_wait(o_full + 8 * t, 0)) ok = false;
+      if (ok && !all_wait(o_full + 8 * t, items_done & 1)) ok = false;
+      ++items_done;
       if (ok) {
         fence_after();
         const float inv = 1.0f / l;
@@ -271,7 +280,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         const int quad = lane & 3, r_first = row & ~3;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t o[32], w[4][4];
+          uint32_t o[32], x[4][4];
           tmem_ld32(tmem + lane_base + C::kColO + D * t + c, o);
           wait_ld();
 #pragma unroll
@@ -280,31 +289,31 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
             for (int k = 0; k < 4; ++k) {
               const __nv_bfloat162 v =
                   __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-              w[i][k] = *reinterpret_cast<const uint32_t*>(&v);
+              x[i][k] = *reinterpret_cast<const uint32_t*>(&v);
             }
 #pragma unroll
-          for (int x = 2; x > 0; x >>= 1)  // w[i] of lane q goes to w[q] of lane i
+          for (int s = 2; s > 0; s >>= 1)  // x[i] of lane q goes to x[q] of lane i
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (i & x) continue;
+              if (i & s) continue;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const bool up = quad & x;
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i][k] : w[i + x][k], x);
-                if (up) w[i][k] = got;
-                else w[i + x][k] = got;
+                const bool up = quad & s;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][k] : x[i + s][k], s);
+                if (up) x[i][k] = got;
+                else x[i + s][k] = got;
               }
             }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = r_first + i, to = tok0 + t * per_tile + r / p.G;
-            if (r >= per_tile * p.G || to >= n) continue;
-            uint16_t* dst = p.o + (row0 + to) * p.o_stride + (int64_t)(h * p.G + r % p.G) * D + c + 8 * quad;
+            const int r = r_first + i, to = w.tok0 + t * per_tile + r / p.G;
+            if (r >= per_tile * p.G || to >= w.n) continue;
+            uint16_t* dst = p.o + (w.row0 + to) * p.o_stride + (int64_t)(w.h * p.G + r % p.G) * D + c + 8 * quad;
             if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-              *reinterpret_cast<uint4*>(dst) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+              *reinterpret_cast<uint4*>(dst) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) dst[2 * k] = (uint16_t)w[i][k], dst[2 * k + 1] = (uint16_t)(w[i][k] >> 16);
+              for (int k = 0; k < 4; ++k) dst[2 * k] = (uint16_t)x[i][k], dst[2 * k + 1] = (uint16_t)(x[i][k] >> 16);
             }
           }
         }
@@ -313,41 +322,144 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
   } else {
     regs_down<kRegOther>();
     if (warp == kLoadWarp) {
-      // ---------------------------------------------------------- copies
-      if (ntile > 0 && lane == 0) {
-        const uint32_t q_bytes = (uint32_t)(per_tile * p.G * D * 2);
-        mbar_arrive_expect_tx(q_full, ntile * q_bytes);
-        for (int t = 0; t < ntile; ++t)
+      // ---------------------------------------------------------- what to work on, and copies
+      // Item x is (block of tokens, head) x of all sequences' blocks, the last ones (which see most) first.  The
+      // grid has a CTA for each; those that run take the places of those that have not begun.
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+      }
+      const int per_cta = p.ntile * per_tile, per = (p.B + 31) / 32, b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
+      auto blocks = [&](int b, int32_t* status, int& row0, int& n) {
+        return sequence(p, b, status, row0, n) ? (n + per_cta - 1) / per_cta : 0;
+      };
+      int sum = 0, row0 = 0, n = 0;  // (of the lane's sequence, where it has one)
+      for (int b = b0; b < b1; ++b) sum += blocks(b, p.status, row0, n);
+      auto scan = [&](int x) {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load(sm32 + C::kOffQ + t * C::kTile + c * (128 * 128), &map_q, 64 * c, h * p.G, row0 + tok0 + t * per_tile, q_full);
-        int done = 0;
-        for (int i = 0; i < 2 * nkt; ++i, ++done) {  // K0 V0 K1 V1 ...
-          const int slot = i % C::kSlots, use = i / C::kSlots;
-          if (use > 0 && !mbar_wait(empty + 8 * slot, (use - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(full + 8 * slot, C::kTile);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load(sm32 + C::kOffRing + slot * C::kTile + c * (128 * 128), (i & 1) ? &map_v : &map_k, 64 * c, h, row0 + kKeys * (i >> 1), full + 8 * slot);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += up;
         }
-        // nothing of these is in flight when the CTA ends
-        if (!mbar_wait(q_full, 0)) ok = false;
-        for (int i = max(0, done - C::kSlots); i < done; ++i)
-          if (!mbar_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1)) ok = false;
+        return x;
+      };
+      const int inc = scan(sum), total = __shfl_sync(0xffffffffu, inc, 31);
+      Ring at;
+      uint32_t k = 0, q_uses[2] = {0, 0}, used = 0, asked = 0;
+      int x = blockIdx.x;
+      for (bool more = true; more;) {
+        if (lane == 0) {  // the next one, while this one is worked on
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(answered, 16);
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(answer)),
+                       "r"(answered)
+                       : "memory");
+        }
+        int i = total - 1 - x / p.nkv;
+        if (i >= 0) {
+          int4 got = make_int4(0, 0, 0, x % p.nkv);
+          {
+            const int l = __ffs(__ballot_sync(0xffffffffu, i < inc)) - 1;  // the lane that holds it
+            i -= __shfl_sync(0xffffffffu, inc - sum, l);
+            if (per == 1) {
+              got.x = i * per_cta, got.y = __shfl_sync(0xffffffffu, row0, l), got.z = __shfl_sync(0xffffffffu, n, l);
+            } else {
+              for (int b = min(l * per, p.B), b_end = min(b + per, p.B); b < b_end; b += 32) {
+                int r = 0, m = 0;
+                const int nb = b + lane < b_end ? blocks(b + lane, nullptr, r, m) : 0, up = scan(nb);
+                const uint32_t hit = __ballot_sync(0xffffffffu, i < up);
+                if (hit) {
+                  const int f = __ffs(hit) - 1;
+                  got.x = (i - __shfl_sync(0xffffffffu, up - nb, f)) * per_cta;
+                  got.y = __shfl_sync(0xffffffffu, r, f), got.z = __shfl_sync(0xffffffffu, m, f);
+                  break;
+                }
+                i -= __shfl_sync(0xffffffffu, up, 31);
+              }
+            }
+          }
+          if (k >= kWorks && !all_wait(work_empty + 8 * (k % kWorks), (k / kWorks - 1) & 1)) ok = false;
+          if (ok && lane == 0) {
+            work[k % kWorks] = got;
+            mbar_arrive(work_full + 8 * (k % kWorks));
+          }
+          ++k;
+          const Item w(p, got);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || t >= w.ntile) break;
+            if (q_uses[t] > 0 && !all_wait(q_empty + 8 * t, (q_uses[t] - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ++q_uses[t];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(q_full + 8 * t, (uint32_t)(per_tile * p.G * D * 2));
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load(sm32 + C::kOffQ + t * C::kTile + c * (128 * 128), &map_q, 64 * c, w.h * p.G, w.row0 + w.tok0 + t * per_tile, q_full + 8 * t);
+            }
+          }
+          for (int j = 0; ok && j < 2 * w.nkt; ++j) {  // K0 V0 K1 V1 ...
+            if (used >= C::kSlots && !all_wait(empty + 8 * at.slot, at.parity ^ 1)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(full + 8 * at.slot, C::kTile);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load(sm32 + C::kOffRing + at.slot * C::kTile + c * (128 * 128), (j & 1) ? &map_v : &map_k, 64 * c, w.h, w.row0 + kKeys * (j >> 1),
+                         full + 8 * at.slot);
+            }
+            at.next();
+            ++used;
+          }
+        }
+        // the answer: a CTA that will not run any more, whose place is taken here, or none
+        uint32_t taken = 0, next = 0;
+        if (all_wait(answered, asked & 1)) {
+          asm volatile(
+              "{ .reg .pred p; .reg .b128 h; ld.shared.b128 h, [%2];\n"
+              "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h; selp.u32 %0, 1, 0, p; mov.u32 %1, 0;\n"
+              "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h; }"
+              : "=r"(taken), "=r"(next)
+              : "r"(smem_u32(answer))
+              : "memory");
+        } else {
+          ok = false;
+        }
+        ++asked;
+        __syncwarp();
+        x = uni((int)next);
+        more = ok && uni((int)taken) != 0;
+      }
+      if (ok && (k < kWorks || all_wait(work_empty + 8 * (k % kWorks), (k / kWorks - 1) & 1))) {
+        if (lane == 0) {
+          work[k % kWorks] = make_int4(-1, 0, 0, 0);
+          mbar_arrive(work_full + 8 * (k % kWorks));
+        }
+      } else {
+        ok = false;
+      }
+      if (!ok) {  // no copy is in flight when the CTA ends
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (q_uses[t] > 0) mbar_wait(q_full + 8 * t, (q_uses[t] - 1) & 1);
+        Ring last;
+        for (uint32_t i = 0; i < used; ++i, last.next())
+          if (i + C::kSlots >= used) mbar_wait(full + 8 * last.slot, last.parity);
       }
     } else if (warp < kLookWarp) {
       // ---------------------------------------------------------- tensor-core issue, a warp for each tile
       constexpr uint32_t id_qk = idesc_bf16(128, kKeys), id_pv = idesc_bf16(128, D) | kBMn;
-      const uint32_t lead = lane == 0 ? 1u : 0u, tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t q_lo = desc_lo(sm32 + C::kOffQ), ring = sm32 + C::kOffRing;
-      const int t = warp - kMmaWarp, mine = t == 0 ? nkt0 : nkt;
-      const uint32_t ds = tm + 128 * t, d_o = tm + C::kColO + D * t, qa = q_lo + t * (C::kTile >> 4);
+      const uint32_t lead = lane == 0 ? 1u : 0u, tm = __shfl_sync(0xffffffffu, tmem, 0), ring = sm32 + C::kOffRing;
+      const int t = warp - kMmaWarp;
+      const uint32_t ds = tm + 128 * t, d_o = tm + C::kColO + D * t, qa = desc_lo(sm32 + C::kOffQ + t * C::kTile);
       // the last products of Q K^T are issued when the other tile's turn has begun: no gap between the two
-      auto qk = [&](int j, auto&& pass) {
-        const uint32_t ka = desc_lo(ring + (2 * j) % C::kSlots * C::kTile);
+      auto qk = [&](int slot, auto&& pass) {
+        const uint32_t ka = desc_lo(ring + slot * C::kTile);
         mma_ss<false>(ds, qa, ka, id_qk, lead);
 #pragma unroll
         for (int ks = 1; ks < D / 16; ++ks) {
@@ -357,96 +469,125 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         }
         commit(s_full + 8 * t, lead);
       };
-      auto pv = [&](int j, int from, int to) {
-        const uint32_t va = desc_lo_mn(ring + (2 * j + 1) % C::kSlots * C::kTile);
+      auto pv = [&](int slot, int j, int from, int to) {
+        const uint32_t va = desc_lo_mn(ring + slot * C::kTile);
 #pragma unroll
         for (int ks = from; ks < to; ++ks) mma_ts(d_o, ds + 8 * ks, va + ((ks * 2048) >> 4), id_pv, ks > 0 ? 1u : (uint32_t)j, lead);
       };
-      auto arrived = [&](int i) { return all_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1); };
-      // (a tile that is not there, or that does not see the last positions, lets go of what it leaves out)
-      auto release = [&](int i) { commit(empty + 8 * (i % C::kSlots), lead); };
-      if (t < ntile) {
-        ok = all_wait(q_full, 0) && arrived(0);
-        if (ok) {
-          fence_after();
-          qk(0, [] {});
-        }
+      auto arrived = [&](const Ring& r) { return all_wait(full + 8 * r.slot, r.parity); };
+      auto release = [&](const Ring& r) { commit(empty + 8 * r.slot, lead); };
+      Ring at;  // K of the current tile
+      uint32_t tiles_done = 0, items_done = 0, looks_done = 0, turns_done = 0;
+      for (uint32_t k = 0; ok; ++k) {
+        const int4 got = take(k);
+        if (got.x < 0) break;
+        const Item w(p, got);
+        const int mine = t >= w.ntile ? 0 : t == 0 ? w.nkt0 : w.nkt;
         // The tiles take the tensor core by turns, tile 0 first: left alone they fall into step, both softmaxes at
         // once and then both tiles' products.
-        const bool turns = ntile == 2;
+        const bool turns = w.ntile == 2;
         auto pass = [&] {
           if (turns && lead) mbar_arrive(turn + 8 * (t ^ 1));
         };
-        for (int j = 0; ok && j < mine; ++j) {
-          release(2 * j);
-          ok = arrived(2 * j + 1) && (j < part || all_wait(looked + 8 * (j - part), 0)) && (j + 1 >= mine || arrived(2 * j + 2)) &&
-               all_wait(p_part + 8 * t, j & 1) && (!turns || (t == 0 && j == 0) || all_wait(turn + 8 * t, t == 0 ? (j - 1) & 1 : j & 1));
+        auto my_turn = [&] {
+          if (!turns) return true;
+          const uint32_t i = turns_done++;
+          return t == 0 ? i == 0 || all_wait(turn, (i - 1) & 1) : all_wait(turn + 8, i & 1);
+        };
+        if (mine > 0) {
+          ok = all_wait(q_full + 8 * t, items_done & 1) && arrived(at);
           if (!ok) break;
           fence_after();
-          pv(j, 0, 4);
-          ok = all_wait(p_part + 16 + 8 * t, j & 1);
+          qk(at.slot, [] {});
+          if (mine == 1) commit(q_empty + 8 * t, lead);
+          ++items_done;
+        }
+        for (int j = 0; ok && j < mine; ++j, ++tiles_done) {
+          release(at);
+          Ring v = at;
+          v.next();
+          at = v;
+          at.next();
+          const uint32_t look = looks_done + (j - w.part);
+          ok = arrived(v) && (j < w.part || all_wait(looked + 8 * (look % kLooks), (look / kLooks) & 1)) && (j + 1 >= mine || arrived(at)) &&
+               all_wait(p_part + 8 * t, tiles_done & 1) && my_turn();
           if (!ok) break;
           fence_after();
-          pv(j, 4, 6);
-          ok = all_wait(p_part + 32 + 8 * t, j & 1);
+          pv(v.slot, j, 0, 4);
+          ok = all_wait(p_part + 16 + 8 * t, tiles_done & 1);
           if (!ok) break;
           fence_after();
-          pv(j, 6, 8);
-          release(2 * j + 1);
+          pv(v.slot, j, 4, 6);
+          ok = all_wait(p_part + 32 + 8 * t, tiles_done & 1);
+          if (!ok) break;
+          fence_after();
+          pv(v.slot, j, 6, 8);
+          release(v);
           if (j + 1 < mine) {
-            qk(j + 1, pass);
+            qk(at.slot, pass);
+            if (j + 2 == mine) commit(q_empty + 8 * t, lead);
           } else {
             commit(o_full + 8 * t, lead);
             pass();
           }
         }
-        for (int j = mine; ok && t == 0 && j < nkt; ++j) {  // tile 1 goes on alone
-          ok = all_wait(turn, (j - 1) & 1);
+        for (int j = mine; ok && j < w.nkt; ++j) {  // what the other tile sees alone is let go of
+          for (int i = 0; ok && i < 2; ++i, at.next()) {
+            ok = arrived(at);
+            if (ok) release(at);
+          }
+          ok = ok && my_turn();
           pass();
         }
-      }
-      for (int i = t < ntile ? 2 * mine : 0; ok && i < 2 * nkt; ++i) {
-        ok = arrived(i);
-        if (ok) release(i);
+        looks_done += w.nkt - w.part;
       }
       // tensor memory is freed only when nothing issued here is in flight
       commit(drained, lead);
       if (!all_wait(drained, 0)) ok = false;
     } else {
       // ---------------------------------------------------------- V tiles that some row sees in part
-      for (int i = 0; i < 2 * nkt; ++i) {
-        if (!all_wait(full + 8 * (i % C::kSlots), (i / C::kSlots) & 1)) {
-          ok = false;
-          break;
-        }
-        const int j = i >> 1;
-        if ((i & 1) == 0 || j < part) {
-          if (lane == 0) mbar_arrive(empty + 8 * (i % C::kSlots));
-          continue;
-        }
-        uint8_t* v = sm + C::kOffRing + (i % C::kSlots) * C::kTile;
-        for (int r = lane; r < kKeys; r += 32) {
-          const int key = kKeys * j + r;
-          if (key <= tok0) continue;  // every row sees it
-          bool clear = key >= n;
-          if (!clear) {
-            uint32_t acc = 0u;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * (128 * 128) + r * 128 + (((c + lane) & 7) << 4));
-              acc = fma_bf16x2(x.x, 0u, acc), acc = fma_bf16x2(x.y, 0u, acc), acc = fma_bf16x2(x.z, 0u, acc), acc = fma_bf16x2(x.w, 0u, acc);
-            }
-            clear = (acc & 0x7FFF7FFFu) != 0u;
-            if (clear) atomicOr(&poison[j - part][r / 32], 1u << (r % 32));
+      Ring at;
+      uint32_t look = 0;
+      for (uint32_t k = 0; ok; ++k) {
+        const int4 got = take(k);
+        if (got.x < 0) break;
+        const Item w(p, got);
+        for (int i = 0; i < 2 * w.nkt; ++i, at.next()) {
+          if (!all_wait(full + 8 * at.slot, at.parity)) {
+            ok = false;
+            break;
           }
-          if (clear)
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(v + (c / 8) * (128 * 128) + r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          const int j = i >> 1;
+          if ((i & 1) && j >= w.part) {
+            uint8_t* v = sm + C::kOffRing + at.slot * C::kTile;
+            if (lane < 4) poison[look % kLooks][lane] = 0u;
+            __syncwarp();
+            for (int r = lane; r < kKeys; r += 32) {
+              const int key = kKeys * j + r;
+              if (key <= w.tok0) continue;  // every row sees it
+              bool clear = key >= w.n;
+              if (!clear) {
+                uint32_t acc[4] = {0u, 0u, 0u, 0u};  // zero unless something is infinite or NaN
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * (128 * 128) + r * 128 + (((c + lane) & 7) << 4));
+                  acc[0] = fma_bf16x2(x.x, 0u, acc[0]), acc[1] = fma_bf16x2(x.y, 0u, acc[1]);
+                  acc[2] = fma_bf16x2(x.z, 0u, acc[2]), acc[3] = fma_bf16x2(x.w, 0u, acc[3]);
+                }
+                clear = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7FFF7FFFu) != 0u;
+                if (clear) atomicOr(&poison[look % kLooks][r / 32], 1u << (r % 32));
+              }
+              if (clear)
+                for (int c = 0; c < D / 8; ++c)
+                  *reinterpret_cast<uint4*>(v + (c / 8) * (128 * 128) + r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(looked + 8 * (look % kLooks));
+            ++look;
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(empty + 8 * at.slot);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(looked + 8 * (j - part));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + 8 * (i % C::kSlots));
       }
     }
   }
@@ -490,8 +631,7 @@ static cudaError_t launch(Params& p, const CUtensorMap& q, const CUtensorMap& k,
     if (fa.numRegs < kRegLaunch) return cudaErrorInvalidConfiguration;
     allowed[dev] = 1;
   }
-  prompt_kernel<D><<<(unsigned)(blocks * p.nkv), kThreads, Cfg<D>::kSmem, st>>>(p, q, k, v);
-  return cudaGetLastError();
+  return launch_served(prompt_kernel<D>, dim3((unsigned)(blocks * p.nkv)), dim3(kThreads), Cfg<D>::kSmem, st, 1, p, q, k, v);
 }
 
 }  // namespace prompt
