@@ -1,6 +1,7 @@
 // Paged 4-bit KV cache: block tables and slot maps from request lengths, placement
 // of new K/V rows through a slot map, and reading rows back.
 #include <algorithm>
+#include <type_traits>
 
 #include "ft_paged.cuh"
 
@@ -418,8 +419,12 @@ __global__ void __launch_bounds__(kRowThreads, 9) read_paged_kernel(const PagedR
 
 // ------------------------------------------------------------------ moving entries
 // A CTA per request and KV head: every entry of the request's moves is read into shared memory before
-// any is written.  Latency: slots, entries, barrier, stores.
-constexpr int kMoveThreads = 128, kMoveMax = 256;
+// any is written.  An entry goes in pieces of d/8 bytes: four of K, eight of V (a chunk of a pair of
+// positions, of which every other halfword is this one's) and the scales.  Where both positions of a
+// pair are written by neighbouring moves, one of the two stores the whole chunk.  256 requests of up to 32
+// moves, 8 heads of 128: 7.8 us (word by word 15.8); one request's few: 3.5, the latency of slots, entries
+// and barrier.
+constexpr int kMoveThreads = 128, kMoveMax = 256, kMovePieces = 13;
 
 struct MoveParams {
   const int32_t *src, *dst;
@@ -430,40 +435,77 @@ struct MoveParams {
 };
 
 template <int D>
+struct MoveEntry {
+  static constexpr int kPiece = D / 8, kHalf = D / 16;           // bytes of a piece, and of a position's part of a V chunk
+  static constexpr int kV = 4 * kPiece, kScale = kV + 8 * kHalf, kBytes = kScale + kPiece;  // in shared memory
+};
+
+template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_paged_kernel(const MoveParams p) {
-  constexpr int NK = D / 8, NV = D / 4, NW = NK + NV + 1;  // an entry: K words, V halfwords (positions share their words), scales
-  extern __shared__ uint32_t move_smem[];
-  __shared__ int from[kMoveMax], to[kMoveMax];
+  using E = MoveEntry<D>;
+  constexpr int NJ = D / 32;
+  using Piece = typename std::conditional<D == 128, uint4, uint2>::type;
+  using Half = typename std::conditional<D == 128, uint2, uint32_t>::type;
+  extern __shared__ __align__(16) uint8_t move_smem[];
+  __shared__ int from[kMoveMax + 2], to[kMoveMax + 2];
   griddep_serve();
   const int h = blockIdx.x % p.L.nkv, b = blockIdx.x / p.L.nkv;
-  for (int i = threadIdx.x; i < p.n; i += kMoveThreads) {
-    const int a = __ldcg(p.src + (int64_t)b * p.n + i), z = __ldcg(p.dst + (int64_t)b * p.n + i);
+  for (int i = threadIdx.x; i < p.n + 2; i += kMoveThreads) {  // move i - 1, one that is none before and behind them
+    const bool in = i > 0 && i <= p.n;
+    const int a = in ? __ldcg(p.src + (int64_t)b * p.n + i - 1) : -1, z = in ? __ldcg(p.dst + (int64_t)b * p.n + i - 1) : -1;
     auto bad = [&](int s) { return s < -1 || (s >= 0 && (s >> p.L.pshift) >= p.L.npages); };
     if (h == 0 && (bad(a) || bad(z))) set_status(p.status, FT_DEV_RANGE);
-    const bool none = a < 0 || z < 0 || bad(a) || bad(z) || a == z;
+    const bool none = a < 0 || z < 0 || bad(a) || bad(z);
     from[i] = none ? -1 : a;
-    to[i] = z;
+    to[i] = none ? -1 : z;
   }
   __syncthreads();
-  auto words = [&](const int* slots, auto&& body) {  // body(word, its place in the pool): K whole words, then V halves, then scales
-    for (int i = threadIdx.x; i < p.n * NW; i += kMoveThreads) {
-      const int m = i / NW, w = i - m * NW;
-      if (from[m] < 0) continue;
-      const int slot = slots[m], pos = slot & (p.L.psize - 1);
-      uint8_t* blk = p.pages + paged_block(p.L, slot >> p.L.pshift, h);
-      if (w < NK) body(i, blk + pos * (D / 2) + 4 * w, true);
-      else if (w < NK + NV) body(i, blk + p.L.voff + paged_v_word<D>(pos, (w - NK) & 7, (w - NK) >> 3), false);
-      else body(i, blk + p.L.soff + 4 * pos, true);
+  auto place = [&](int slot) { return p.pages + paged_block(p.L, slot >> p.L.pshift, h); };
+  auto chunk = [&](uint8_t* blk, int pos, int g) { return blk + p.L.voff + (pos >> 1) * D + (g ^ paged_v_turn<D>(pos >> 1)) * E::kPiece; };
+  for (int i = threadIdx.x; i < p.n * kMovePieces; i += kMoveThreads) {
+    const int m = i / kMovePieces, w = i - m * kMovePieces, slot = from[m + 1];
+    if (slot < 0) continue;
+    const int pos = slot & (p.L.psize - 1);
+    uint8_t *blk = place(slot), *own = move_smem + m * E::kBytes;
+    if (w < 4) {
+      *reinterpret_cast<Piece*>(own + w * E::kPiece) = *reinterpret_cast<const Piece*>(blk + pos * (D / 2) + w * E::kPiece);
+    } else if (w < 12) {
+      const Piece x = *reinterpret_cast<const Piece*>(chunk(blk, pos, w - 4));
+      const uint32_t* xs = reinterpret_cast<const uint32_t*>(&x);
+      __align__(8) uint32_t y[NJ / 2];
+#pragma unroll
+      for (int k = 0; k < NJ / 2; ++k) y[k] = prmt(xs[2 * k], xs[2 * k + 1], (pos & 1) ? 0x7632u : 0x5410u);
+      *reinterpret_cast<Half*>(own + E::kV + (w - 4) * E::kHalf) = *reinterpret_cast<const Half*>(y);
+    } else {
+      *reinterpret_cast<uint32_t*>(own + E::kScale) = *reinterpret_cast<const uint32_t*>(blk + p.L.soff + 4 * pos);
     }
-  };
-  words(from, [&](int i, const uint8_t* at, bool whole) {
-    move_smem[i] = whole ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-  });
+  }
   __syncthreads();
-  words(to, [&](int i, uint8_t* at, bool whole) {
-    if (whole) *reinterpret_cast<uint32_t*>(at) = move_smem[i];
-    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)move_smem[i];
-  });
+  for (int i = threadIdx.x; i < p.n * kMovePieces; i += kMoveThreads) {
+    const int m = i / kMovePieces, w = i - m * kMovePieces, slot = to[m + 1];
+    if (slot < 0) continue;
+    const int pos = slot & (p.L.psize - 1);
+    uint8_t *blk = place(slot), *own = move_smem + m * E::kBytes;
+    if (w < 4) {
+      *reinterpret_cast<Piece*>(blk + pos * (D / 2) + w * E::kPiece) = *reinterpret_cast<const Piece*>(own + w * E::kPiece);
+    } else if (w < 12) {
+      uint8_t* at = chunk(blk, pos, w - 4);
+      const uint32_t* y = reinterpret_cast<const uint32_t*>(own + E::kV + (w - 4) * E::kHalf);
+      if (!(slot & 1) && to[m + 2] == slot + 1) {  // with its neighbour's
+        const uint32_t* z = y + E::kBytes / 4;
+        __align__(16) uint32_t x[NJ];
+#pragma unroll
+        for (int k = 0; k < NJ; ++k) x[k] = prmt(y[k / 2], z[k / 2], (k & 1) ? 0x7632u : 0x5410u);
+        *reinterpret_cast<Piece*>(at) = *reinterpret_cast<const Piece*>(x);
+      } else if (!((slot & 1) && to[m] == slot - 1)) {
+#pragma unroll
+        for (int k = 0; k < NJ; ++k)
+          *reinterpret_cast<uint16_t*>(at + 4 * k + 2 * (pos & 1)) = (uint16_t)(y[k / 2] >> (16 * (k & 1)));
+      }
+    } else {
+      *reinterpret_cast<uint32_t*>(blk + p.L.soff + 4 * pos) = *reinterpret_cast<const uint32_t*>(own + E::kScale);
+    }
+  }
 }
 
 // Grid over (rows, heads) x (K, V); 0 blocks: too many.
@@ -602,17 +644,17 @@ int ft_kv_move_paged_int4(const ft_block_cfg* c, void* pages, int n_pages, int p
   p.L = ft::paged_layout(*c, n_pages, page_size);
   p.n = n;
   p.status = dev_status;
-  const int words = c->head_dim / 8 + c->head_dim / 4 + 1;
+  const int bytes = c->head_dim == 128 ? ft::MoveEntry<128>::kBytes : ft::MoveEntry<64>::kBytes;
   const auto kernel = c->head_dim == 128 ? ft::move_paged_kernel<128> : ft::move_paged_kernel<64>;
   static int allowed[64][2] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FT_ERR_CUDA;
   int& ok = allowed[dev][c->head_dim == 128];
   if (!ok) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ft::kMoveMax * words * 4) != cudaSuccess) return FT_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ft::kMoveMax * bytes) != cudaSuccess) return FT_ERR_CUDA;
     ok = 1;
   }
-  return ft::launch_served(kernel, dim3((unsigned)(B * c->n_kv)), dim3(ft::kMoveThreads), (size_t)n * words * 4, (cudaStream_t)stream, 1,
+  return ft::launch_served(kernel, dim3((unsigned)(B * c->n_kv)), dim3(ft::kMoveThreads), (size_t)n * bytes, (cudaStream_t)stream, 1,
                            p) == cudaSuccess
              ? FT_OK
              : FT_ERR_CUDA;

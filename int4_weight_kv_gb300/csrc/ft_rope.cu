@@ -12,6 +12,8 @@ namespace ft {
 // pieces, so that the pairs of the rotation meet in one lane.  A warp holds 4 (8) consecutive tokens of one
 // head and goes through `per` heads with the same angles.
 constexpr int kRopeThreads = 128;
+// tensors whose rows are at 16-byte boundaries
+enum { kWideQ = 1, kWideK = 2, kWideV = 4, kWideQOut = 8, kWideKOut = 16 };
 
 struct RopeRows {
   const uint16_t *q, *k, *v;
@@ -21,37 +23,55 @@ struct RopeRows {
   const int32_t *pos, *slots;
   uint8_t* pages;
   PagedLayout L;
-  int total, nq, nkv, heads, per, hb;  // heads: nq q heads, then k, then (paged) v; per: those of a warp
+  int total, nq, nkv, heads, per, hb, wide;  // heads: nq q heads, then k, then (paged) v; per: those of a warp
   float norm, eps;
   int32_t* status;
   uint64_t turn[64];
 };
 
-__device__ __forceinline__ void rope_load8(const uint16_t* src, f32x2* x) {
-  if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-    const uint4 q = *reinterpret_cast<const uint4*>(src);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// A lane's two pieces of a row, as they are.  Rows at 16-byte boundaries are told apart by the host.
+template <int D>
+__device__ __forceinline__ void rope_load(const uint16_t* src, bool wide, uint4 (&raw)[2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-  } else {
+  for (int i = 0; i < 2; ++i) {
+    const uint16_t* at = src + i * (D / 2);
+    if (wide) {
+      raw[i] = *reinterpret_cast<const uint4*>(at);
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = f32x2(bf16_bits_to_f32(src[2 * i]), bf16_bits_to_f32(src[2 * i + 1]));
+      for (int k = 0; k < 4; ++k) w[k] = (uint32_t)at[2 * k] | ((uint32_t)at[2 * k + 1] << 16);
+      raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
-__device__ __forceinline__ void rope_store8(uint16_t* dst, const f32x2* x) {
-  uint32_t w[4];
+__device__ __forceinline__ void rope_values(const uint4 (&raw)[2], f32x2 (&x)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    x[i].get(a, b);
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[4 * i + k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
   }
-  if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
+}
+template <int D>
+__device__ __forceinline__ void rope_store(uint16_t* dst, bool wide, const f32x2 (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[2 * i] = (uint16_t)w[i], dst[2 * i + 1] = (uint16_t)(w[i] >> 16);
+  for (int i = 0; i < 2; ++i) {
+    uint16_t* at = dst + i * (D / 2);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a, b;
+      x[4 * i + k].get(a, b);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+      w[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    if (wide) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at[2 * k] = (uint16_t)w[k], at[2 * k + 1] = (uint16_t)(w[k] >> 16);
+    }
   }
 }
 
@@ -125,17 +145,36 @@ __device__ __forceinline__ void rope_place(const RopeRows& p, f32x2 (&x)[8], boo
   const float far = r > 0.0f || s == 0.0f ? 0.5f - 7.0f * 4.76837158203125e-07f : -1.0f;  // 7 x 2^-21
   const int mag_at = (e & 1) * 3 + (e >> 1) * 8, neg_at = 8 * (e >> 1) + (e & 1);  // the latter: places below bit 15
   uint32_t w[8];  // this lane's value of words 2 i, 2 i + 1 of group j (i < 4), and of group j + NJ / 2
+  f32x2 u[8];
+  float near = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float a, b, m0, m1, d0, d1;
+    float a, b, d0, d1;
     x[i].get(a, b);
-    const f32x2 mag(fabsf(a), fabsf(b)), u = fma2(mag, r2, magic2);
-    fma2(mag, r2, fma2(u, minus, magic2)).get(d0, d1);
-    u.get(m0, m1);
-    if (fmaxf(fabsf(d0), fabsf(d1)) >= far) {
-      if (fabsf(d0) >= far) m0 = kMagic + paged_edge(fabsf(a) * p.norm, s, m0 - kMagic);
-      if (fabsf(d1) >= far) m1 = kMagic + paged_edge(fabsf(b) * p.norm, s, m1 - kMagic);
+    const f32x2 mag(fabsf(a), fabsf(b));
+    u[i] = fma2(mag, r2, magic2);
+    fma2(mag, r2, fma2(u[i], minus, magic2)).get(d0, d1);
+    near = fmaxf(near, fmaxf(fabsf(d0), fabsf(d1)));
+  }
+  if (near >= far) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[2], m[2];
+      x[i].get(v[0], v[1]);
+      u[i].get(m[0], m[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float a = fabsf(v[k]), code = m[k] - kMagic;
+        if (fabsf(fmaf(a, r, -code)) >= far) m[k] = kMagic + paged_edge(a * p.norm, s, code);
+      }
+      u[i] = f32x2(m[0], m[1]);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b, m0, m1;
+    x[i].get(a, b);
+    u[i].get(m0, m1);
     w[i] = ((prmt(__float_as_uint(m0), __float_as_uint(m1), 0x5410u) & 0x00070007u) << mag_at) |
            ((prmt(__float_as_uint(a), __float_as_uint(b), 0x7632u) & 0x80008000u) >> neg_at);
   }
@@ -182,7 +221,7 @@ __device__ __forceinline__ void rope_place(const RopeRows& p, f32x2 (&x)[8], boo
 }
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeRows p) {
+__global__ void __launch_bounds__(kRopeThreads, PAGED ? 6 : 7) rope_rows_kernel(const __grid_constant__ RopeRows p) {
   constexpr int LV = D / 16, R = 32 / LV;
   griddep_serve();
   const int lane = threadIdx.x & 31, c = lane % LV;
@@ -192,43 +231,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   if (t - lane / LV >= p.total) return;
   const bool there = t < p.total;
   const int h0 = (int)(warp % chunks) * p.per, h1 = min(h0 + p.per, p.heads), turned = p.nq + p.nkv;
+  const int64_t row = there ? t : 0;
+  const int pos = there && h0 < turned ? p.pos[row] : 0;
   int slot = -1;
   if (PAGED) {
-    slot = there ? __ldcg(p.slots + t) : -1;
+    slot = there ? __ldcg(p.slots + row) : -1;
     if (slot != -1 && (slot < 0 || (slot >> p.L.pshift) >= p.L.npages)) {
       if (c == 0) set_status(p.status, FT_DEV_RANGE);
       slot = -1;
     }
   }
-  f32x2 cs[4], sn[4];
-  if (h0 < turned) {
-    const int pos = there ? p.pos[t] : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float c2[2], s2[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint64_t a = (uint64_t)(int64_t)pos * p.turn[8 * c + 2 * i + k];  // turns, modulo one
-        sincospif((float)(int32_t)(uint32_t)(a >> 32) * 4.656612873077393e-10f, &s2[k], &c2[k]);  // x 2^-31: half turns
-      }
-      cs[i] = f32x2(c2[0], c2[1]);
-      sn[i] = f32x2(s2[0], s2[1]);
-    }
+  // the place of head hh of this row (rows behind the last one read the first: nothing of them is stored)
+  auto source = [&](int hh, bool& wide) {
+    const bool q = hh < p.nq, k = hh < turned;
+    wide = p.wide & (q ? kWideQ : k ? kWideK : kWideV);
+    return (q ? p.q + row * p.q_stride : k ? p.k + row * p.k_stride : p.v + row * p.v_stride) + (hh - (q ? 0 : k ? p.nq : turned)) * D + 8 * c;
+  };
+  uint4 raw[2];
+  bool wide;
+  {
+    const uint16_t* src = source(h0, wide);
+    rope_load<D>(src, wide, raw);
   }
-  const f32x2 minus(-1.0f, -1.0f);
-  for (int hh = h0; hh < h1; ++hh) {
-    const int kind = hh < p.nq ? 0 : hh < turned ? 1 : 2, h = hh - (kind == 0 ? 0 : kind == 1 ? p.nq : turned);
-    const uint16_t* src = (kind == 0 ? p.q + t * p.q_stride : kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + h * D + 8 * c;
-    f32x2 x[8];
-    if (there) {
-      rope_load8(src, x);
-      rope_load8(src + D / 2, x + 4);
-    } else {
+  int hh = h0;
+  // the heads up to `end`, all of one kind, each read while the one before it is worked on
+  auto heads = [&](int end, const float* gamma, bool rotated, auto&& put) {
+    if (hh >= end) return;
+    // z_lo = lo (g_lo cos) - hi (g_hi sin), z_hi = hi (g_hi cos) + lo (g_lo sin), the gains inside the factors
+    f32x2 lc[4], ls[4], hc[4], hs[4];
+    if (rotated) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = f32x2(0.0f, 0.0f);
+      for (int i = 0; i < 4; ++i) {
+        float f[4][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint64_t a = (uint64_t)(int64_t)pos * p.turn[8 * c + 2 * i + k];  // turns, modulo one
+          float sn, cs;
+          sincospif((float)(int32_t)(uint32_t)(a >> 32) * 4.656612873077393e-10f, &sn, &cs);  // x 2^-31: half turns
+          const float lo = gamma ? gamma[8 * c + 2 * i + k] : 1.0f, hi = gamma ? gamma[D / 2 + 8 * c + 2 * i + k] : 1.0f;
+          f[0][k] = lo * cs, f[1][k] = lo * sn, f[2][k] = hi * cs, f[3][k] = -hi * sn;
+        }
+        lc[i] = f32x2(f[0][0], f[0][1]), ls[i] = f32x2(f[1][0], f[1][1]), hc[i] = f32x2(f[2][0], f[2][1]), hs[i] = f32x2(f[3][0], f[3][1]);
+      }
     }
-    if (kind < 2) {
-      const float* gamma = kind == 0 ? p.gamma_q : p.gamma_k;
+    for (; hh < end; ++hh) {
+      f32x2 x[8];
+      rope_values(raw, x);
+      if (hh + 1 < h1) {
+        const uint16_t* src = source(hh + 1, wide);
+        rope_load<D>(src, wide, raw);
+      }
       if (gamma) {
         f32x2 ss = mul2(x[0], x[0]);
 #pragma unroll
@@ -239,27 +291,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
 #pragma unroll
         for (int o = 1; o < LV; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         const float r = rsqrtf(fmaf(a, 1.0f / D, p.eps));
+        const f32x2 r2(r, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int ch = (i < 4 ? 0 : D / 2) + 8 * c + 2 * (i & 3);
-          x[i] = mul2(mul2(x[i], f32x2(r, r)), f32x2(gamma[ch], gamma[ch + 1]));
+        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], r2);
+      }
+      if (rotated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 lo = x[i], hi = x[i + 4];
+          x[i] = fma2(hi, hs[i], mul2(lo, lc[i]));
+          x[i + 4] = fma2(lo, ls[i], mul2(hi, hc[i]));
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x2 lo = x[i], hi = x[i + 4];
-        x[i] = fma2(mul2(hi, sn[i]), minus, mul2(lo, cs[i]));
-        x[i + 4] = fma2(lo, sn[i], mul2(hi, cs[i]));
-      }
+      put(x);
     }
-    if (PAGED && kind > 0) {
-      rope_place<D>(p, x, kind == 2, h, slot);
-    } else if (there) {
-      uint16_t* dst = (kind == 0 ? p.q_out + t * p.q_out_stride : p.k_out + t * p.k_out_stride) + h * D + 8 * c;
-      rope_store8(dst, x);
-      rope_store8(dst + D / 2, x + 4);
-    }
-  }
+  };
+  heads(min(h1, p.nq), p.gamma_q, true, [&](const f32x2 (&x)[8]) {
+    if (there) rope_store<D>(p.q_out + row * p.q_out_stride + hh * D + 8 * c, p.wide & kWideQOut, x);
+  });
+  heads(min(h1, turned), p.gamma_k, true, [&](f32x2 (&x)[8]) {
+    if constexpr (PAGED) rope_place<D>(p, x, false, hh - p.nq, slot);
+    else if (there) rope_store<D>(p.k_out + row * p.k_out_stride + (hh - p.nq) * D + 8 * c, p.wide & kWideKOut, x);
+  });
+  if constexpr (PAGED) heads(h1, nullptr, false, [&](f32x2 (&x)[8]) { rope_place<D>(p, x, true, hh - turned, slot); });
 }
 
 static int launch_rope(const ft_block_cfg& c, RopeRows& p, bool paged, cudaStream_t st) {
@@ -267,6 +321,9 @@ static int launch_rope(const ft_block_cfg& c, RopeRows& p, bool paged, cudaStrea
   p.nkv = p.k ? c.n_kv : 0;
   p.heads = p.nq + p.nkv * (paged ? 2 : 1);
   p.eps = c.rms_eps;
+  auto wide = [](const void* at, int64_t stride, int bit) { return ft_host::aligned16(at) && stride % 8 == 0 ? bit : 0; };
+  p.wide = wide(p.q, p.q_stride, kWideQ) | wide(p.k, p.k_stride, kWideK) | wide(p.v, p.v_stride, kWideV) |
+           wide(p.q_out, p.q_out_stride, kWideQOut) | wide(p.k_out, p.k_out_stride, kWideKOut);
   rope_turns(c.rope_base, c.head_dim, p.turn);
   const int rows = 512 / c.head_dim;
   const int64_t groups = ((int64_t)p.total + rows - 1) / rows;
