@@ -448,7 +448,10 @@ static int few_ctas(int nt) {
   if (sms <= 0) sms = 152;
   return sms * (nt == 1 ? 4 : 2);
 }
-// 8-column tiles for max_q tokens of a group of G heads; 0: too many rows for this kernel.
+// 8-column tiles for max_q tokens of a group of G heads; 0: too many rows for this kernel.  The same for trees, whose
+// many rows have a kernel of their own (ft_attn_tree.cu).  Measured there, this kernel against that (us): 32 requests of up
+// to 4096 positions, 32 heads over 8, trees of 4 / 8 tokens (16 / 32 rows) 36 / 63 and 58 / 67; one of 32768, 64 heads
+// over 8, trees of 2 / 4 tokens 22 / 34 and 33 / 34.
 static int few_tiles(int max_q, int G) {
   const int64_t rows = (int64_t)max_q * G;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0;
@@ -496,9 +499,10 @@ static cudaError_t launch_few_any(const AttnPagedParams& p, int head_dim, int nt
   return nt == 1 ? launch_few<64, 1, TREE>(p, ws, st) : nt == 2 ? launch_few<64, 2, TREE>(p, ws, st) : launch_few<64, 4, TREE>(p, ws, st);
 }
 
-static size_t attn_ws(const ft_block_cfg* c, int B, int total_q, int max_q) {
+static size_t attn_ws(const ft_block_cfg* c, int B, int total_q, int max_q, bool tree) {
   if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > kApMaxB || total_q < 0 || max_q < 1) return 0;
   const int nt = few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
+  if (nt == 0 && tree) return attn_tree_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   if (nt == 0) return attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   return align_up((size_t)(B + 1) * 4, 256) + (size_t)few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
 }
@@ -524,7 +528,7 @@ static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int 
   // to eight a request and head) are counted in 32 bits
   static_assert(1 + kSegUnits <= 8, "units of work");
   if (((int64_t)table_stride * page_size / kUnit + 8) * c->n_kv > INT32_MAX / B) return FT_ERR_UNSUPPORTED;
-  if (ws_bytes < attn_ws(c, B, total_q, max_q)) return FT_ERR_WORKSPACE;
+  if (ws_bytes < attn_ws(c, B, total_q, max_q, tree)) return FT_ERR_WORKSPACE;
   AttnPagedParams p = {};
   p.pages = static_cast<const uint8_t*>(pages);
   p.L = paged_layout(*c, n_pages, page_size);
@@ -551,6 +555,10 @@ static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int 
     const cudaError_t e = tree ? launch_few_any<true>(p, c->head_dim, nt, workspace, stream) : launch_few_any<false>(p, c->head_dim, nt, workspace, stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
   }
+  if (tree) {
+    if (!attn_tree_fits(p)) return FT_ERR_UNSUPPORTED;
+    return launch_attn_tree(p, c->head_dim, workspace, stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  }
   if (attn_tiles_ctas(p) > INT32_MAX) return FT_ERR_UNSUPPORTED;
   return launch_attn_tiles(p, c->head_dim, workspace, stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
@@ -559,8 +567,8 @@ static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int 
 
 extern "C" {
 
-size_t ft_attn_paged_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q); }
-size_t ft_attn_tree_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q); }
+size_t ft_attn_paged_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q, false); }
+size_t ft_attn_tree_workspace_bytes(const ft_block_cfg* c, int B, int total_q, int max_q) { return ft::attn_ws(c, B, total_q, max_q, true); }
 
 int ft_attn_paged_int4(const ft_block_cfg* c, const void* pages, int n_pages, int page_size, const uint16_t* q_bf16,
                        int64_t q_stride, const int32_t* cu_seqlens, const int32_t* kv_len, const int32_t* block_table,

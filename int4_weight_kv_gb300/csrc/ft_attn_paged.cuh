@@ -162,6 +162,10 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
 // Requests with many rows (ft_attn_tiles.cu); a workspace of attn_tiles_ws bytes.
 size_t attn_tiles_ws(int nkv, int G, int head_dim, int B, int total_q);
 int64_t attn_tiles_ctas(const AttnPagedParams& p);
-cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);  // p.mask: a tree's
+cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
+// Draft trees with more rows than the kernel for few rows takes (ft_attn_tree.cu).
+size_t attn_tree_ws(int nkv, int G, int head_dim, int B, int total_q);
+bool attn_tree_fits(const AttnPagedParams& p);
+cudaError_t launch_attn_tree(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
 
 }  // namespace ft

@@ -85,7 +85,7 @@ struct TilesSplit {
   float* part;
 };
 
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPagedParams p, const TilesSplit sp) {
   using C = Cfg<D>;
   constexpr int NJ = D / 32;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
   }
   const int nrow = (int)min((int64_t)n * p.G - r0, (int64_t)sp.rows);  // rows of this CTA
   const int ntile = nrow > 128 ? 2 : 1;
-  const int last = TREE ? kv - 1 : kv - n + (r0 + nrow - 1) / p.G;  // last visible position of any row
+  const int last = kv - n + (r0 + nrow - 1) / p.G;               // last visible position of any row
   const int all_kt = last >= 0 ? last / kKeys + 1 : 0;
   const int parts = min(sp.parts, max(1, (all_kt + kPartTiles - 1) / kPartTiles)), per_part = parts == 1 ? all_kt : (all_kt + parts - 1) / parts;
   const int j0 = part * per_part, nkt = max(0, min(all_kt - j0, per_part));  // this CTA's tiles: j0, j0 + 1, ...
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
     if (t < ntile) {
       const int tok = min(r / p.G, n - 1);
       const int lim = kv - n + tok;  // last position this row sees
-      const int lim_all = TREE ? kv - n - 1 : kv - n + (r0 + 128 * t + 32 * (warp & 3)) / p.G;  // and that every row of the warp sees
+      const int lim_all = kv - n + (r0 + 128 * t + 32 * (warp & 3)) / p.G;  // and that every row of the warp sees
       // the rotated query row as the FP16 operand
       if (nkt > 0 && !all_wait(rot_full + 8 * t, 0)) ok = false;
       if (ok && nkt > 0) {
@@ -318,19 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnPaged
         wait_ld();
         // a tile that some row of the warp sees in part, or with positions on a page outside the pool
         if (kKeys * (j0 + j) + kKeys - 1 > lim_all || (mask4.x & mask4.y & mask4.z & mask4.w) != 0xFFFFFFFFu) {
-          uint32_t mask[4] = {mask4.x, mask4.y, mask4.z, mask4.w};
-          if constexpr (TREE) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int at = kKeys * (j0 + j) + 32 * g - (kv - n);  // first position of the group among the new tokens
-              uint32_t bits = tree_bits(p.mask + (row0 + tok) * p.mask_stride, at, n);
-              if (at < 0) bits |= at <= -32 ? 0xFFFFFFFFu : (1u << -at) - 1u;  // the history
-              mask[g] &= bits;
-            }
-          }
+          const uint32_t mask[4] = {mask4.x, mask4.y, mask4.z, mask4.w};
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
-            s[c] = (TREE || kKeys * (j0 + j) + c <= lim) && ((mask[c / 32] >> (c % 32)) & 1u) ? s[c] : 0xFF800000u;
+            s[c] = kKeys * (j0 + j) + c <= lim && ((mask[c / 32] >> (c % 32)) & 1u) ? s[c] : 0xFF800000u;
         }
         float mx = -INFINITY;
 #pragma unroll
@@ -783,18 +774,18 @@ int64_t attn_tiles_ctas(const AttnPagedParams& p) {
   return blocks * p.L.nkv * parts;
 }
 
-template <int D, bool TREE>
+template <int D>
 static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cudaStream_t st) {
   static int allowed[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!allowed[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(attn_tiles_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+        cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     // the roles' register shares add up to 128 a thread: a build with fewer would wait for them forever
     cudaFuncAttributes fa = {};
-    if (cudaFuncGetAttributes(&fa, attn_tiles_kernel<D, TREE>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
+    if (cudaFuncGetAttributes(&fa, attn_tiles_kernel<D>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
     if (fa.numRegs < kRegCommon) return cudaErrorInvalidConfiguration;
     allowed[dev] = 1;
   }
@@ -803,7 +794,7 @@ static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cud
   tiles_shape(p.L.nkv, p.G, p.B, p.total_q, sp.rows, sp.parts, blocks);
   sp.meta = static_cast<int4*>(workspace);
   sp.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up((size_t)blocks * 16, 256));
-  attn_tiles_kernel<D, TREE><<<(unsigned)(blocks * p.L.nkv * sp.parts), kThreads, Cfg<D>::kSmem, st>>>(p, sp);
+  attn_tiles_kernel<D><<<(unsigned)(blocks * p.L.nkv * sp.parts), kThreads, Cfg<D>::kSmem, st>>>(p, sp);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || sp.parts == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -819,8 +810,7 @@ static cudaError_t launch_tiles_d(const AttnPagedParams& p, void* workspace, cud
 }
 
 cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st) {
-  if (p.mask) return head_dim == 128 ? launch_tiles_d<128, true>(p, workspace, st) : launch_tiles_d<64, true>(p, workspace, st);
-  return head_dim == 128 ? launch_tiles_d<128, false>(p, workspace, st) : launch_tiles_d<64, false>(p, workspace, st);
+  return head_dim == 128 ? launch_tiles_d<128>(p, workspace, st) : launch_tiles_d<64>(p, workspace, st);
 }
 
 }  // namespace ft

@@ -291,19 +291,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
                   __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
               x[i][k] = *reinterpret_cast<const uint32_t*>(&v);
             }
-#pragma unroll
-          for (int s = 2; s > 0; s >>= 1)  // x[i] of lane q goes to x[q] of lane i
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i & s) continue;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const bool up = quad & s;
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][k] : x[i + s][k], s);
-                if (up) x[i][k] = got;
-                else x[i + s][k] = got;
-              }
-            }
+          quad_transpose(x, quad);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = r_first + i, to = w.tok0 + t * per_tile + r / p.G;

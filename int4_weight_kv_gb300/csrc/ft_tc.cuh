@@ -37,6 +37,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* d) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7]), "=r"(d[8]),
+        "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]), "=r"(d[14]), "=r"(d[15])
+      : "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -105,6 +113,24 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Piece i of lane q of each four lanes goes to piece q of lane i: rows that a lane each holds become runs of
+// four pieces that the four lanes store together.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][4], int quad) {
+#pragma unroll
+  for (int s = 2; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool up = quad & s;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][k] : x[i + s][k], s);
+        if (up) x[i][k] = got;
+        else x[i + s][k] = got;
+      }
+    }
 }
 
 // A wait of a whole warp with one outcome: its accesses to tensor memory are warp-wide.
