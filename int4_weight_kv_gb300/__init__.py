@@ -209,6 +209,28 @@ def _rows(t, inner: int, kind: int, dev: int) -> tuple[int, int]:
     return t.data_ptr(), step[0] if shape[0] > 1 else max(step[0], inner)
 
 
+def _rows_of(t, n: int, inner: int, kind: int, dev: int) -> tuple[int, int]:
+    """_rows of a tensor of at least n rows; the common case, [rows, heads, d] with any stride between rows, in one look."""
+    shape, step = t.shape, t.stride()
+    if (len(shape) == 3 and shape[0] >= n and shape[0] > 1 and step[2] == 1 and step[1] == shape[2] and shape[1] * shape[2] == inner
+            and t.dtype in _torch[kind] and t.get_device() == dev):
+        return t.data_ptr(), step[0]
+    if shape[0] < n:
+        raise ValueError(f"{shape[0]} of {n} rows")
+    return _rows(t, inner, kind, dev)
+
+
+def _plain_of(t, n: int, kind: int, dev: int):
+    """_plain of a tensor of at least n elements (or None, or a raw pointer)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype in _torch[kind] and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    if t.numel() < n:
+        raise ValueError(f"an argument holds {t.numel()} of {n} elements")
+    return _plain(t, kind, dev)
+
+
 def make_cfg(hidden, n_q, n_kv, head_dim, inter, had_block=0, kv_group=0, rms_eps=1e-5, rope_base=500000.0,
              w_group=128, weight_format=0) -> BlockCfg:
     hb = had_block or head_dim
@@ -372,20 +394,17 @@ def ft_attn_tree_paged_int4(cfg, pages, n_pages, page_size, q, cu_seqlens, kv_le
     """As ft_attn_paged_int4; tree_mask: int32 [>= total_q, >= max_q / 32] (bit j: sees the request's new token j)."""
     dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
-    if min(q.shape[0], o.shape[0], tree_mask.shape[0]) < total_q or \
-            min(cu_seqlens.numel() - 1, kv_len.numel(), block_table.shape[0]) < B:
-        raise ValueError(f"fewer than {total_q} rows or {B} requests")
-    if 32 * tree_mask.shape[1] < min(max_q, total_q):
-        raise ValueError(f"masks of {tree_mask.shape[1]} words for up to {max_q} tokens")
-    row = cfg.n_q * cfg.head_dim
-    qp, qs = _rows(q, row, _B16, dev)
-    op, os_ = _rows(o, row, _B16, dev)
-    table, stride = _rows(block_table, block_table.shape[1], _I32, dev)
-    mask, words = _rows(tree_mask, tree_mask.shape[1], _I32, dev)
+    row, width, words = cfg.n_q * cfg.head_dim, block_table.shape[1], tree_mask.shape[1]
+    if 32 * words < min(max_q, total_q):
+        raise ValueError(f"masks of {words} words for up to {max_q} tokens")
+    qp, qs = _rows_of(q, total_q, row, _B16, dev)
+    op, os_ = _rows_of(o, total_q, row, _B16, dev)
+    table, stride = _rows_of(block_table, B, width, _I32, dev)
+    mask, words = _rows_of(tree_mask, total_q, words, _I32, dev)
     return lib().ft_attn_tree_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size, qp, qs,
-                                         _plain(cu_seqlens, _I32, dev), _plain(kv_len, _I32, dev), table, stride, mask,
-                                         words, B, total_q, max_q, scale, op, os_, _plain(workspace, _ANY, dev),
-                                         workspace.numel() * workspace.element_size(),
+                                         _plain_of(cu_seqlens, B + 1, _I32, dev), _plain_of(kv_len, B, _I32, dev), table,
+                                         stride, mask, words, B, total_q, max_q, scale, op, os_,
+                                         _plain(workspace, _ANY, dev), workspace.numel() * workspace.element_size(),
                                          _plain(dev_status, _I32, dev), here if stream is None else _stream(stream))
 
 
@@ -393,42 +412,35 @@ def ft_kv_move_paged_int4(cfg, pages, n_pages, page_size, src_slots, dst_slots, 
     """src_slots, dst_slots: int32 [B, n]."""
     dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
-    if src_slots.dim() != 2 or src_slots.shape != dst_slots.shape:
-        raise ValueError(f"slots of shapes {tuple(src_slots.shape)} and {tuple(dst_slots.shape)}: need [B, n] twice")
+    shape = src_slots.shape
+    if len(shape) != 2 or shape != dst_slots.shape:
+        raise ValueError(f"slots of shapes {tuple(shape)} and {tuple(dst_slots.shape)}: need [B, n] twice")
     return lib().ft_kv_move_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size,
-                                       _plain(src_slots, _I32, dev), _plain(dst_slots, _I32, dev), src_slots.shape[0],
-                                       src_slots.shape[1], _plain(dev_status, _I32, dev),
-                                       here if stream is None else _stream(stream))
-
-
-def _gain(t, cfg, dev: int):
-    if t is not None and not isinstance(t, int) and t.numel() < cfg.head_dim:
-        raise ValueError(f"a gain of {t.numel()} of {cfg.head_dim} elements")
-    return _plain(t, _F32, dev)
-
-
-def _opt_rows(t, out, total: int, heads: int, cfg, dev: int) -> tuple:
-    """(pointer, stride) of rows [>= total, heads, d] and of the rows that they go to; (None, 0) twice where both are None."""
-    if t is None and out is None:
-        return None, 0, None, 0
-    if t is None or out is None:
-        raise ValueError("rows without an output, or an output without rows")
-    if min(t.shape[0], out.shape[0]) < total:
-        raise ValueError(f"fewer than {total} rows")
-    return *_rows(t, heads * cfg.head_dim, _B16, dev), *_rows(out, heads * cfg.head_dim, _B16, dev)
+                                       _plain(src_slots, _I32, dev), _plain(dst_slots, _I32, dev), shape[0], shape[1],
+                                       _plain(dev_status, _I32, dev), here if stream is None else _stream(stream))
 
 
 def ft_qk_norm_rope_bf16(cfg, q, k, gamma_q, gamma_k, positions, total, q_out, k_out, stream=None) -> int:
     """q, q_out: BF16 [>= total, n_q, d], k, k_out: BF16 [>= total, n_kv, d], rows at any stride, either pair or None;
     gamma_q, gamma_k: FP32 [d] or None; positions: int32 [>= total]."""
     dev, here = _current()
-    if positions.numel() < total:
-        raise ValueError(f"{positions.numel()} of {total} positions")
-    qp, qs, qo, qos = _opt_rows(q, q_out, total, cfg.n_q, cfg, dev)
-    kp, ks, ko, kos = _opt_rows(k, k_out, total, cfg.n_kv, cfg, dev)
-    return lib().ft_qk_norm_rope_bf16(ctypes.byref(cfg), qp, qs, kp, ks, _gain(gamma_q, cfg, dev), _gain(gamma_k, cfg, dev),
-                                      _plain(positions, _I32, dev), total, qo, qos, ko, kos,
-                                      here if stream is None else _stream(stream))
+    d = cfg.head_dim
+    qp = qs = qo = qos = kp = ks = ko = kos = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q without q_out, or q_out without q")
+        row = cfg.n_q * d
+        qp, qs = _rows_of(q, total, row, _B16, dev)
+        qo, qos = _rows_of(q_out, total, row, _B16, dev)
+    if k is not None or k_out is not None:
+        if k is None or k_out is None:
+            raise ValueError("k without k_out, or k_out without k")
+        row = cfg.n_kv * d
+        kp, ks = _rows_of(k, total, row, _B16, dev)
+        ko, kos = _rows_of(k_out, total, row, _B16, dev)
+    return lib().ft_qk_norm_rope_bf16(ctypes.byref(cfg), qp, qs, kp, ks, _plain_of(gamma_q, d, _F32, dev),
+                                      _plain_of(gamma_k, d, _F32, dev), _plain_of(positions, total, _I32, dev), total, qo, qos,
+                                      ko, kos, here if stream is None else _stream(stream))
 
 
 def ft_kv_append_rope_paged_int4(cfg, pages, n_pages, page_size, k, v, gamma_k, positions, slots, total, q=None, gamma_q=None,
@@ -437,30 +449,35 @@ def ft_kv_append_rope_paged_int4(cfg, pages, n_pages, page_size, k, v, gamma_k, 
     FP32 [d] or None; positions, slots: int32 [>= total]."""
     dev, here = _current()
     _check_pool(cfg, pages, n_pages, page_size)
-    if min(k.shape[0], v.shape[0], slots.numel(), positions.numel()) < total:
-        raise ValueError(f"fewer than {total} rows, positions or slots")
-    row = cfg.n_kv * cfg.head_dim
-    kp, ks = _rows(k, row, _B16, dev)
-    vp, vs = _rows(v, row, _B16, dev)
-    qp, qs, qo, qos = _opt_rows(q, q_out, total, cfg.n_q, cfg, dev)
+    d = cfg.head_dim
+    row = cfg.n_kv * d
+    kp, ks = _rows_of(k, total, row, _B16, dev)
+    vp, vs = _rows_of(v, total, row, _B16, dev)
+    qp = qs = qo = qos = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q without q_out, or q_out without q")
+        row = cfg.n_q * d
+        qp, qs = _rows_of(q, total, row, _B16, dev)
+        qo, qos = _rows_of(q_out, total, row, _B16, dev)
     return lib().ft_kv_append_rope_paged_int4(ctypes.byref(cfg), _plain(pages, _U8, dev), n_pages, page_size, kp, ks, vp, vs,
-                                              _gain(gamma_k, cfg, dev), _plain(positions, _I32, dev),
-                                              _plain(slots, _I32, dev), total, qp, qs, _gain(gamma_q, cfg, dev), qo, qos,
-                                              _plain(dev_status, _I32, dev), here if stream is None else _stream(stream))
+                                              _plain_of(gamma_k, d, _F32, dev), _plain_of(positions, total, _I32, dev),
+                                              _plain_of(slots, total, _I32, dev), total, qp, qs,
+                                              _plain_of(gamma_q, d, _F32, dev), qo, qos, _plain(dev_status, _I32, dev),
+                                              here if stream is None else _stream(stream))
 
 
 def ft_attn_prompt_bf16(cfg, q, k, v, cu_seqlens, B, total, max_len, scale, o, dev_status=None, stream=None) -> int:
-    """q, o: BF16 [>= total, n_q, d], k, v: BF16 [>= total, n_kv, d], rows at any stride (k, v: a multiple of 8);
+    """q, o: BF16 [>= total, n_q, d], k, v: BF16 [>= total, n_kv, d], rows at any stride (q, k, v: a multiple of 8);
     cu_seqlens: int32 [>= B + 1]."""
     dev, here = _current()
-    if min(q.shape[0], k.shape[0], v.shape[0], o.shape[0]) < total or cu_seqlens.numel() <= B:
-        raise ValueError(f"fewer than {total} rows or {B} sequences")
-    row, kv_row = cfg.n_q * cfg.head_dim, cfg.n_kv * cfg.head_dim
-    qp, qs = _rows(q, row, _B16, dev)
-    kp, ks = _rows(k, kv_row, _B16, dev)
-    vp, vs = _rows(v, kv_row, _B16, dev)
-    op, os_ = _rows(o, row, _B16, dev)
-    return lib().ft_attn_prompt_bf16(ctypes.byref(cfg), qp, qs, kp, ks, vp, vs, _plain(cu_seqlens, _I32, dev), B, total,
+    d = cfg.head_dim
+    row, kv_row = cfg.n_q * d, cfg.n_kv * d
+    qp, qs = _rows_of(q, total, row, _B16, dev)
+    kp, ks = _rows_of(k, total, kv_row, _B16, dev)
+    vp, vs = _rows_of(v, total, kv_row, _B16, dev)
+    op, os_ = _rows_of(o, total, row, _B16, dev)
+    return lib().ft_attn_prompt_bf16(ctypes.byref(cfg), qp, qs, kp, ks, vp, vs, _plain_of(cu_seqlens, B + 1, _I32, dev), B, total,
                                      max_len, scale, op, os_, _plain(dev_status, _I32, dev),
                                      here if stream is None else _stream(stream))
 
