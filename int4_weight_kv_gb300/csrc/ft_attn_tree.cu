@@ -64,7 +64,7 @@ struct Cfg {
   static constexpr int kOffSums = kOffScale + kScaleRing * 64, kOffBar = kOffSums + 2 * 128 * 8;
   static constexpr int kBars = 512, kSmem = kOffBar + kBars + 1024;  // 1024: alignment slack
   static constexpr int kColO = 256;                                  // tensor memory: S0, S1, then O0, O1
-  static constexpr int kPW = D + 4;                                  // a partial: max, sum, 2 unused, accumulator
+  static constexpr int kPW = D + 8;                                  // a partial: 4 unused, max, sum, 2 unused, accumulator (at 32 bytes)
 };
 
 // Partials: of a segment that begins its (request, block, head), by the row's place in q; of one that goes on with it, by CTA.
@@ -422,45 +422,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
           L = fmaf(f[0], x.y, f[1] * y.y);
         }
         fence_after();
-        const int quad = lane & 3, c0 = both ? D / 2 * t : 0, c1 = both ? c0 + D / 2 : D;
+        const int c0 = both ? D / 2 * t : 0, c1 = both ? c0 + D / 2 : D;
         if (ok && !idle) {
-          const int rb = first_row + row;  // row of the block
-          auto place = [&](int i) {
-            if (w.j0 > 0) return sp.more + ((int64_t)blockIdx.x * kRows + i) * C::kPW;
-            const int rr = w.r0 + i, to = rr / p.G;
-            return sp.first + ((int64_t)(w.row0 + to) * (p.L.nkv * p.G) + w.h * p.G + (rr - to * p.G)) * C::kPW;
-          };
-          float* dst[4];  // of the rows that this lane and its three neighbours hold
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = (rb & ~3) + i < w.nrow ? place((rb & ~3) + i) : nullptr;
-          if (there && c0 == 0) {
-            float* own = dst[0];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) own = quad == i ? dst[i] : own;
-            *reinterpret_cast<float2*>(own) = make_float2(M, L);
-          }
+          const int rb = first_row + row, to = r / p.G;  // row of the block
+          float* dst = w.j0 > 0 ? sp.more + ((int64_t)blockIdx.x * kRows + rb) * C::kPW
+                                : sp.first + ((int64_t)(w.row0 + to) * (p.L.nkv * p.G) + w.h * p.G + (r - to * p.G)) * C::kPW;
+          if (there && c0 == 0) *reinterpret_cast<float2*>(dst + 4) = make_float2(M, L);
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
-            uint32_t o[4][4];
-            {
-              uint32_t a[16];
-              tmem_ld16(tmem + lane_base + C::kColO + (both ? 0 : D * t) + c, a);
-              if (both) {
-                uint32_t b[16];
-                tmem_ld16(tmem + lane_base + C::kColO + D + c, b);
-                wait_ld();
+            uint32_t a[16];
+            tmem_ld16(tmem + lane_base + C::kColO + (both ? 0 : D * t) + c, a);
+            if (both) {
+              uint32_t b[16];
+              tmem_ld16(tmem + lane_base + C::kColO + D + c, b);
+              wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) a[i] = __float_as_uint(fmaf(__uint_as_float(a[i]), f[0], __uint_as_float(b[i]) * f[1]));
-              } else {
-                wait_ld();
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i / 4][i % 4] = a[i];
+              for (int i = 0; i < 16; ++i) a[i] = __float_as_uint(fmaf(__uint_as_float(a[i]), f[0], __uint_as_float(b[i]) * f[1]));
+            } else {
+              wait_ld();
             }
-            quad_transpose(o, quad);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 4 + c + 4 * quad) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+            if (there) {
+              st_global_v8(dst + 8 + c, a);
+              st_global_v8(dst + 8 + c + 8, a + 8);
             }
           }
         }
@@ -880,7 +863,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const AttnPagedParams p,
   const int c0 = share_of(units, shares, u0), c1 = share_of(units, shares, u0 + (int64_t)x.weight(block) * (x.keys - 1));
   const int tok = r / p.G, hh = h * p.G + (r - tok * p.G);
   const int64_t at = (int64_t)(row0 + tok) * (p.L.nkv * p.G) + hh;
-  const float *first = sp.first + at * PW, *more = sp.more + ((int64_t)(c0 + 1) * kRows + (r - block * kRows)) * PW;
+  const float *first = sp.first + at * PW + 4, *more = sp.more + ((int64_t)(c0 + 1) * kRows + (r - block * kRows)) * PW + 4;
   join_row<D, W>(p, c1 - c0 + 1, [&](int i) { return i == 0 ? first : more + (int64_t)(i - 1) * kRows * PW; }, kOScale,
                  p.o + (row0 + tok) * p.o_stride + (int64_t)hh * D);
 }
@@ -906,12 +889,12 @@ static cudaError_t launch(const AttnPagedParams& p, void* workspace, cudaStream_
   }
   const int ctas = num_ctas();
   Split sp;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);  // (given at 16 bytes)
   sp.pref = reinterpret_cast<int64_t*>(ws);
   ws += align_up((size_t)(p.B + 1) * 8, 256);
   sp.q = reinterpret_cast<uint16_t*>(ws);
   const int64_t q_rows = (int64_t)p.total_q * p.L.nkv * p.G;
-  ws += (size_t)q_rows * D * 2;
+  ws += (size_t)q_rows * D * 2;  // (a multiple of 128)
   sp.more = reinterpret_cast<float*>(ws);
   sp.first = sp.more + (size_t)ctas * kRows * Cfg<D>::kPW;
   const int per = kPrepThreads / 32 * (32 / (D / 32));
@@ -930,8 +913,8 @@ static cudaError_t launch(const AttnPagedParams& p, void* workspace, cudaStream_
 }  // namespace tree
 
 size_t attn_tree_ws(int nkv, int G, int head_dim, int B, int total_q) {
-  return align_up((size_t)(B + 1) * 8, 256) + ((size_t)tree::num_ctas() * tree::kRows + (size_t)total_q * nkv * G) * (head_dim + 4) * 4 +
-         (size_t)total_q * nkv * G * head_dim * 2;
+  return align_up((size_t)(B + 1) * 8, 256) + ((size_t)tree::num_ctas() * tree::kRows + (size_t)total_q * nkv * G) * (head_dim + 8) * 4 +
+         (size_t)total_q * nkv * G * head_dim * 2 + 16;
 }
 
 bool attn_tree_fits(const AttnPagedParams& p) {

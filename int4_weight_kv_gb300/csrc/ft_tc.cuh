@@ -115,22 +115,11 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Piece i of lane q of each four lanes goes to piece q of lane i: rows that a lane each holds become runs of
-// four pieces that the four lanes store together.
-__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][4], int quad) {
-#pragma unroll
-  for (int s = 2; s > 0; s >>= 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & s) continue;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool up = quad & s;
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][k] : x[i + s][k], s);
-        if (up) x[i][k] = got;
-        else x[i + s][k] = got;
-      }
-    }
+// 32 bytes at a 32-byte boundary.
+__device__ __forceinline__ void st_global_v8(void* at, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+               "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 // A wait of a whole warp with one outcome: its accesses to tensor memory are warp-wide.

@@ -328,6 +328,19 @@ def test_tree_bounds_strides_and_place(i):
     a.check(o)
 
 
+@pytest.mark.parametrize("i", [1, 6, 12])
+def test_tree_workspace_at_16_bytes(i):
+    """A workspace at an odd multiple of 16 bytes, of just the size asked for."""
+    a = _tree(i)
+    want, _ = a.run()
+    size = ft.ft_attn_tree_workspace_bytes(a.cfg, a.B, a.total, max(a.qlens))
+    buf = torch.full((size + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    at = 16 + (-buf.data_ptr()) % 32
+    o, st = a.run(ws=buf[at:at + size])
+    assert st == 0 and torch.equal(o, want)
+    assert (buf[:at] == 0xFF).all() and (buf[at + size:] == 0xFF).all()
+
+
 @pytest.mark.parametrize("heads,qlens,kvlens", [(64, [64], [20000]), (32, [7] * 3, [9000, 33000, 40]), (32, [24, 24], [12000, 5000])])
 def test_tree_long(heads, qlens, kvlens):
     a = Tree(heads, 8, 128, 64, qlens, kvlens)
