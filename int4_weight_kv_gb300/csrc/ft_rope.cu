@@ -9,9 +9,9 @@
 namespace ft {
 
 // D / 16 lanes per row: lane c owns channels 8 c .. 8 c + 7 and d/2 + 8 c .. d/2 + 8 c + 7, two 16-byte
-// pieces, so that the pairs of the rotation meet in one lane.  A warp holds 4 (8) consecutive tokens of one
-// head and goes through `per` heads with the same angles.
-constexpr int kRopeThreads = 128;
+// pieces, so that the pairs of the rotation meet in one lane.  A CTA has 4 (8) consecutive tokens, their angles in
+// shared memory, and a warp of its four goes through `per` heads of them.
+constexpr int kRopeThreads = 128, kRopeHeads = 12;
 // tensors whose rows are at 16-byte boundaries
 enum { kWideQ = 1, kWideK = 2, kWideV = 4, kWideQOut = 8, kWideKOut = 16 };
 
@@ -222,17 +222,37 @@ __device__ __forceinline__ void rope_place(const RopeRows& p, f32x2 (&x)[8], boo
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kRopeThreads, PAGED ? 6 : 7) rope_rows_kernel(const __grid_constant__ RopeRows p) {
-  constexpr int LV = D / 16, R = 32 / LV;
+  constexpr int LV = D / 16, R = 32 / LV, W = kRopeThreads / 32;
+  __shared__ __align__(16) float2 angles[R][D / 2 + 2];  // (cos, sin) of the CTA's tokens, each warp's share of them made by it
   griddep_serve();
-  const int lane = threadIdx.x & 31, c = lane % LV;
-  const int chunks = (p.heads + p.per - 1) / p.per;
-  const int64_t warp = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = warp / chunks * R + lane / LV;
-  if (t - lane / LV >= p.total) return;
+  const int lane = threadIdx.x & 31, c = lane % LV, warp = threadIdx.x >> 5;
+  const int chunks = (p.heads + W * p.per - 1) / (W * p.per), chunk = blockIdx.x % chunks;
+  const int64_t t = (int64_t)(blockIdx.x / chunks) * R + lane / LV;
   const bool there = t < p.total;
-  const int h0 = (int)(warp % chunks) * p.per, h1 = min(h0 + p.per, p.heads), turned = p.nq + p.nkv;
-  const int64_t row = there ? t : 0;
-  const int pos = there && h0 < turned ? p.pos[row] : 0;
+  const int h0 = min((chunk * W + warp) * p.per, p.heads), h1 = min(h0 + p.per, p.heads), turned = p.nq + p.nkv;
+  const int64_t row = there ? t : 0;  // (rows behind the last one read the first: nothing of them is stored)
+  // the first head of each kind that this warp has, and the next one's bytes on their way
+  auto source = [&](int hh) {
+    return (hh < p.nq ? p.q + row * p.q_stride + hh * D
+            : hh < turned ? p.k + row * p.k_stride + (hh - p.nq) * D
+                          : p.v + row * p.v_stride + (hh - turned) * D) + 8 * c;
+  };
+  auto wide_of = [&](int hh) { return (p.wide & (hh < p.nq ? kWideQ : hh < turned ? kWideK : kWideV)) != 0; };
+  uint4 raw[2];
+  const uint16_t* src = source(h0 < p.heads ? h0 : 0);
+  rope_load<D>(src, wide_of(h0 < p.heads ? h0 : 0), raw);
+  if (chunk * W * p.per < turned) {
+    const int pos = p.pos[row];
+    float2* to = &angles[lane / LV][8 * c + 8 / W * warp];
+#pragma unroll
+    for (int k = 0; k < 8 / W; ++k) {
+      const uint64_t a = (uint64_t)(int64_t)pos * p.turn[8 * c + 8 / W * warp + k];  // turns, modulo one
+      float sn, cs;
+      sincospif((float)(int32_t)(uint32_t)(a >> 32) * 4.656612873077393e-10f, &sn, &cs);  // x 2^-31: half turns
+      to[k] = make_float2(cs, sn);
+    }
+    __syncthreads();
+  }
   int slot = -1;
   if (PAGED) {
     slot = there ? __ldcg(p.slots + row) : -1;
@@ -241,52 +261,42 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? 6 : 7) rope_rows_kernel(
       slot = -1;
     }
   }
-  // the place of head hh of this row (rows behind the last one read the first: nothing of them is stored)
-  auto source = [&](int hh, bool& wide) {
-    const bool q = hh < p.nq, k = hh < turned;
-    wide = p.wide & (q ? kWideQ : k ? kWideK : kWideV);
-    return (q ? p.q + row * p.q_stride : k ? p.k + row * p.k_stride : p.v + row * p.v_stride) + (hh - (q ? 0 : k ? p.nq : turned)) * D + 8 * c;
-  };
-  uint4 raw[2];
-  bool wide;
-  {
-    const uint16_t* src = source(h0, wide);
-    rope_load<D>(src, wide, raw);
-  }
   int hh = h0;
   // the heads up to `end`, all of one kind, each read while the one before it is worked on
-  auto heads = [&](int end, const float* gamma, bool rotated, auto&& put) {
+  auto heads = [&](int end, const float* gamma, bool rotated, bool wide, auto&& put) {
     if (hh >= end) return;
     // z_lo = lo (g_lo cos) - hi (g_hi sin), z_hi = hi (g_hi cos) + lo (g_lo sin), the gains inside the factors
     f32x2 lc[4], ls[4], hc[4], hs[4];
     if (rotated) {
+      const float4* from = reinterpret_cast<const float4*>(&angles[lane / LV][8 * c]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float f[4][2];
+        const float4 a = from[i];  // cos, sin; cos, sin
+        float lo[2] = {1.0f, 1.0f}, hi[2] = {1.0f, 1.0f};
+        if (gamma) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint64_t a = (uint64_t)(int64_t)pos * p.turn[8 * c + 2 * i + k];  // turns, modulo one
-          float sn, cs;
-          sincospif((float)(int32_t)(uint32_t)(a >> 32) * 4.656612873077393e-10f, &sn, &cs);  // x 2^-31: half turns
-          const float lo = gamma ? gamma[8 * c + 2 * i + k] : 1.0f, hi = gamma ? gamma[D / 2 + 8 * c + 2 * i + k] : 1.0f;
-          f[0][k] = lo * cs, f[1][k] = lo * sn, f[2][k] = hi * cs, f[3][k] = -hi * sn;
+          for (int k = 0; k < 2; ++k) lo[k] = gamma[8 * c + 2 * i + k], hi[k] = gamma[D / 2 + 8 * c + 2 * i + k];
         }
-        lc[i] = f32x2(f[0][0], f[0][1]), ls[i] = f32x2(f[1][0], f[1][1]), hc[i] = f32x2(f[2][0], f[2][1]), hs[i] = f32x2(f[3][0], f[3][1]);
+        lc[i] = f32x2(lo[0] * a.x, lo[1] * a.z), ls[i] = f32x2(lo[0] * a.y, lo[1] * a.w);
+        hc[i] = f32x2(hi[0] * a.x, hi[1] * a.z), hs[i] = f32x2(-hi[0] * a.y, -hi[1] * a.w);
       }
     }
     for (; hh < end; ++hh) {
       f32x2 x[8];
       rope_values(raw, x);
-      if (hh + 1 < h1) {
-        const uint16_t* src = source(hh + 1, wide);
+      if (hh + 1 < end) {
+        src += D;
         rope_load<D>(src, wide, raw);
+      } else if (hh + 1 < h1) {
+        src = source(hh + 1);
+        rope_load<D>(src, wide_of(hh + 1), raw);
       }
       if (gamma) {
-        f32x2 ss = mul2(x[0], x[0]);
+        f32x2 ss[2] = {mul2(x[0], x[0]), mul2(x[4], x[4])};
 #pragma unroll
-        for (int i = 1; i < 8; ++i) ss = fma2(x[i], x[i], ss);
+        for (int i = 1; i < 4; ++i) ss[0] = fma2(x[i], x[i], ss[0]), ss[1] = fma2(x[4 + i], x[4 + i], ss[1]);
         float a, b;
-        ss.get(a, b);
+        add2(ss[0], ss[1]).get(a, b);
         a += b;
 #pragma unroll
         for (int o = 1; o < LV; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -306,14 +316,19 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? 6 : 7) rope_rows_kernel(
       put(x);
     }
   };
-  heads(min(h1, p.nq), p.gamma_q, true, [&](const f32x2 (&x)[8]) {
-    if (there) rope_store<D>(p.q_out + row * p.q_out_stride + hh * D + 8 * c, p.wide & kWideQOut, x);
-  });
-  heads(min(h1, turned), p.gamma_k, true, [&](f32x2 (&x)[8]) {
-    if constexpr (PAGED) rope_place<D>(p, x, false, hh - p.nq, slot);
-    else if (there) rope_store<D>(p.k_out + row * p.k_out_stride + (hh - p.nq) * D + 8 * c, p.wide & kWideKOut, x);
-  });
-  if constexpr (PAGED) heads(h1, nullptr, false, [&](f32x2 (&x)[8]) { rope_place<D>(p, x, true, hh - turned, slot); });
+  auto out = [&](uint16_t* base, int64_t stride, int first, int bit) {  // puts rows to BF16 rows, from this warp's first head on
+    return [=, to = base + row * stride + (int64_t)(max(h0, first) - first) * D + 8 * c, wide = (p.wide & bit) != 0](const f32x2 (&x)[8]) mutable {
+      if (there) rope_store<D>(to, wide, x);
+      to += D;
+    };
+  };
+  heads(min(h1, p.nq), p.gamma_q, true, (p.wide & kWideQ) != 0, out(p.q_out, p.q_out_stride, 0, kWideQOut));
+  if constexpr (PAGED) {
+    heads(min(h1, turned), p.gamma_k, true, (p.wide & kWideK) != 0, [&](f32x2 (&x)[8]) { rope_place<D>(p, x, false, hh - p.nq, slot); });
+    heads(h1, nullptr, false, (p.wide & kWideV) != 0, [&](f32x2 (&x)[8]) { rope_place<D>(p, x, true, hh - turned, slot); });
+  } else {
+    heads(min(h1, turned), p.gamma_k, true, (p.wide & kWideK) != 0, out(p.k_out, p.k_out_stride, p.nq, kWideKOut));
+  }
 }
 
 static int launch_rope(const ft_block_cfg& c, RopeRows& p, bool paged, cudaStream_t st) {
@@ -327,8 +342,12 @@ static int launch_rope(const ft_block_cfg& c, RopeRows& p, bool paged, cudaStrea
   rope_turns(c.rope_base, c.head_dim, p.turn);
   const int rows = 512 / c.head_dim;
   const int64_t groups = ((int64_t)p.total + rows - 1) / rows;
-  p.per = (int)std::min<int64_t>(8, std::max<int64_t>(1, groups * p.heads / (152 * 48)));
-  const int64_t warps = groups * ((p.heads + p.per - 1) / p.per), blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  constexpr int W = kRopeThreads / 32;
+  // heads of a warp: as many as leave every SM some warps, the warps' shares equal
+  const int most = (int)std::min<int64_t>(kRopeHeads, std::max<int64_t>(1, groups * p.heads / (152 * 48)));
+  const int chunks = (p.heads + W * most - 1) / (W * most);
+  p.per = (p.heads + W * chunks - 1) / (W * chunks);
+  const int64_t blocks = groups * ((p.heads + W * p.per - 1) / (W * p.per));
   if (blocks > INT32_MAX) return FT_ERR_UNSUPPORTED;
   const auto kernel = c.head_dim == 128 ? (paged ? rope_rows_kernel<128, true> : rope_rows_kernel<128, false>)
                                         : (paged ? rope_rows_kernel<64, true> : rope_rows_kernel<64, false>);
