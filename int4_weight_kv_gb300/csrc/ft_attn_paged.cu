@@ -502,7 +502,8 @@ static cudaError_t launch_few_any(const AttnPagedParams& p, int head_dim, int nt
 static size_t attn_ws(const ft_block_cfg* c, int B, int total_q, int max_q, bool tree) {
   if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > kApMaxB || total_q < 0 || max_q < 1) return 0;
   const int nt = few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
-  if (nt == 0 && tree) return attn_tree_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
+  if (tree && nt != 1)
+    return nt == 0 ? attn_tree_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q) : attn_tree_few_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   if (nt == 0) return attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   return align_up((size_t)(B + 1) * 4, 256) + (size_t)few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
 }
@@ -551,13 +552,14 @@ static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int 
   p.mask = tree ? mask : nullptr;
   p.mask_stride = mask_stride;
   const int nt = few_tiles(p.max_q, p.G);
+  if (tree && nt != 1) {
+    if (!attn_tree_fits(p)) return FT_ERR_UNSUPPORTED;
+    const cudaError_t e = nt == 0 ? launch_attn_tree(p, c->head_dim, workspace, stream) : launch_attn_tree_few(p, c->head_dim, workspace, stream);
+    return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
+  }
   if (nt > 0) {
     const cudaError_t e = tree ? launch_few_any<true>(p, c->head_dim, nt, workspace, stream) : launch_few_any<false>(p, c->head_dim, nt, workspace, stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
-  }
-  if (tree) {
-    if (!attn_tree_fits(p)) return FT_ERR_UNSUPPORTED;
-    return launch_attn_tree(p, c->head_dim, workspace, stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;
   }
   if (attn_tiles_ctas(p) > INT32_MAX) return FT_ERR_UNSUPPORTED;
   return launch_attn_tiles(p, c->head_dim, workspace, stream) == cudaSuccess ? FT_OK : FT_ERR_CUDA;

@@ -167,5 +167,8 @@ cudaError_t launch_attn_tiles(const AttnPagedParams& p, int head_dim, void* work
 size_t attn_tree_ws(int nkv, int G, int head_dim, int B, int total_q);
 bool attn_tree_fits(const AttnPagedParams& p);
 cudaError_t launch_attn_tree(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
+// Those of up to 32 rows (ft_attn_tree_few.cu).
+size_t attn_tree_few_ws(int nkv, int G, int head_dim, int B, int total_q);
+cudaError_t launch_attn_tree_few(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st);
 
 }  // namespace ft

@@ -2,11 +2,7 @@
 //
 // The formulas are at the top of ft_attn_paged.cuh; which of the new tokens a token sees is in its mask's bits.
 //
-// The work is the list of (request, block of up to 256 rows, head, 128 positions) in this order; a CTA per SM takes
-// an equal, contiguous share of it whatever the lengths are.  A share's segment is its part of one (request, block,
-// head); it costs about as much beside its positions as kSegUnits units of them do, so each counts that many more,
-// ahead of its first.  Every segment leaves (max, sum, accumulator) partials, which a second kernel joins in the
-// order of the shares, rotates back and stores.
+// How the work is shared out over the CTAs, one an SM, and joined: ft_attn_tree.cuh.
 //
 // Inside a CTA two tiles of products run against each other, the tensor core working for one while the other's
 // softmax runs: where a block has more than 128 rows, its two halves over the same positions, else the same rows
@@ -34,19 +30,15 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ft_attn_paged.cuh"
-#include "ft_tc.cuh"
+#include "ft_attn_tree.cuh"
 
 namespace ft {
 
 namespace tree {
 
-using namespace tiles;
-
-constexpr int kThreads = 640, kRows = 256, kKeys = 128;
+constexpr int kThreads = 640;
 constexpr int kAheadWarp = 16, kMmaWarp = 18;  // (the first schedulers have the softmax's warps of few rows)
 constexpr int kSegUnits = 8;  // a segment's cost beside its positions, in units of 128 rows x 128 positions
-constexpr int kMinShare = 6;
 constexpr int kWorks = 4;     // segments known ahead: decoding looks up to two beyond its own, never behind the query rows'
 constexpr float kOScale = 512.0f;  // the operands hold V's values x 2^-9
 constexpr uint32_t kWide = 0x5C005C00u;  // 2^8 in both halves: the factor of a group with a wide range of scales
@@ -64,44 +56,8 @@ struct Cfg {
   static constexpr int kOffSums = kOffScale + kScaleRing * 64, kOffBar = kOffSums + 2 * 128 * 8;
   static constexpr int kBars = 512, kSmem = kOffBar + kBars + 1024;  // 1024: alignment slack
   static constexpr int kColO = 256;                                  // tensor memory: S0, S1, then O0, O1
-  static constexpr int kPW = D + 8;                                  // a partial: 4 unused, max, sum, 2 unused, accumulator (at 32 bytes)
+  static constexpr int kPW = D + kPartHead;                          // a partial
 };
-
-// Partials: of a segment that begins its (request, block, head), by the row's place in q; of one that goes on with it, by CTA.
-struct Split {
-  int64_t* pref;  // [B + 1] prefix sums of the requests' units
-  uint16_t* q;    // the rotated queries as FP16 operand rows, [total_q][n_q][D], channels in the order of the cache's words
-  float *first, *more;
-};
-
-// Units of a request: blocks of kRows rows, each head of each kSegUnits and one for each 128 positions and 128 rows.
-struct Units {
-  int rows, keys, full;       // rows and position tiles of the request, blocks of kRows rows
-  int64_t pair, last, total;  // units of one head of a full block, and of the last block if it is not full; all
-  __device__ __forceinline__ Units(const AttnPagedParams& p, int n, int kv) {
-    rows = n * p.G;
-    keys = max(1, (kv + kKeys - 1) / kKeys);
-    full = rows / kRows;
-    pair = kSegUnits + 2 * (int64_t)keys;
-    const int rest = rows % kRows;
-    last = rest == 0 ? 0 : kSegUnits + (rest > 128 ? 2 : 1) * (int64_t)keys;
-    total = p.L.nkv * (full * pair + last);
-  }
-  __device__ __forceinline__ int weight(int block) const { return block < full || rows % kRows > 128 ? 2 : 1; }
-  // first tile of positions at or behind unit `at` of its (block, head)
-  __device__ __forceinline__ int tile(int block, int64_t at) const {
-    const int w = weight(block);
-    return at <= kSegUnits ? 0 : (int)min((at - kSegUnits + w - 1) / w, (int64_t)keys);
-  }
-};
-// Shares of `units` on `ctas` CTAs: as many as there are CTAs, none of fewer than kMinShare units but the only one
-// (of two at least, so that each holds the beginning of a 256-row tile).
-__device__ __forceinline__ int shares_of(int64_t units, int ctas) { return (int)max(min(units / kMinShare, (int64_t)ctas), (int64_t)1); }
-__device__ __forceinline__ int64_t share_begin(int64_t units, int ctas, int c) { return c * (units / ctas) + min((int64_t)c, units % ctas); }
-__device__ __forceinline__ int share_of(int64_t units, int ctas, int64_t u) {
-  const int64_t per = units / ctas, rem = units % ctas, cut = rem * (per + 1);
-  return (int)(u < cut ? u / (per + 1) : rem + (u - cut) / max(per, (int64_t)1));
-}
 
 // A segment: rows r0 .. r0 + nrow - 1 (tokens x heads of a group) of request b for head h over position tiles j0 .. j1 - 1.
 struct Segment {
@@ -118,81 +74,6 @@ struct Cursor {
     if (++slot == N) slot = 0, parity ^= 1;
   }
 };
-
-// The prefix sums (the first CTA), and the query rows rotated and rounded to FP16 (the others): D / 32 lanes a row, 32
-// channels a lane.
-constexpr int kPrepThreads = 128;
-template <int D>
-__global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPagedParams p, const Split sp) {
-  constexpr int LV = D / 32, R = 32 / LV, NJ = D / 32;
-  griddep_serve();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x == 0) {
-    __shared__ int64_t sums[kPrepThreads / 32];
-    const int per = (p.B + kPrepThreads - 1) / kPrepThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    auto units_of = [&](int b, int32_t* status) {
-      int row0, n, kv;
-      if (!attn_request(p, b, status, row0, n, kv) || n == 0) return (int64_t)0;
-      return Units(p, n, kv).total;
-    };
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += units_of(b, p.status);
-    int64_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    int64_t at = inc - sum;
-    for (int w = 0; w < warp; ++w) at += sums[w];
-    for (int b = b0; b < b1; ++b) {
-      sp.pref[b] = at;
-      at += units_of(b, nullptr);
-    }
-    if (b1 == p.B && b0 < b1) sp.pref[p.B] = at;
-    return;
-  }
-  const int nq = p.L.nkv * p.G;
-  const int64_t row = ((int64_t)(blockIdx.x - 1) * (kPrepThreads / 32) + warp) * R + lane / LV, rows = (int64_t)p.total_q * nq;
-  const bool in = row < rows;
-  const int64_t tok = in ? row / nq : 0;
-  const int h = in ? (int)(row - tok * nq) : 0, j = lane % LV;
-  const uint16_t* src = p.q + tok * p.q_stride + (int64_t)h * D + 32 * j;
-  f32x2 v[16];
-  if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(src)[i];
-      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[4 * i + c] = f32x2(__uint_as_float(y[c] << 16), __uint_as_float(y[c] & 0xFFFF0000u));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = f32x2(bf16_bits_to_f32(src[2 * i]), bf16_bits_to_f32(src[2 * i + 1]));
-  }
-  paged_fwht<D>(v, p.hb);
-  if (!in) return;
-  const float f0 = p.qscale * p.norm;
-  uint32_t over = 0u;  // stays zero unless a value is infinite or NaN in FP16
-  uint4* to = reinterpret_cast<uint4*>(sp.q + row * D);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a, c;
-      v[q + 4 * e].get(a, c);
-      const __half2 hv = __floats2half2_rn(a * f0, c * f0);
-      o[e] = *reinterpret_cast<const uint32_t*>(&hv);
-      over = hfma2(o[e], 0u, over);
-    }
-    to[j + NJ * q] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if ((over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams p, const Split sp) {
@@ -786,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
             if (!attn_request(p, b, nullptr, row0, n, kv)) n = 0;
             fresh = false;
           }
-          const Units x(p, n, kv);
+          const Units x(p, n, kv, sp.seg);
           if (n == 0 || off >= x.total) {
             ++b, off = 0, fresh = true;
             continue;
@@ -846,33 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-// Joins the parts of each row, W = 1 or 4 warps a row.
-template <int D, int W>
-__global__ void __launch_bounds__(128) tree_join_kernel(const AttnPagedParams p, const Split sp, int ctas, int groups) {
-  constexpr int PW = Cfg<D>::kPW;
-  const int g = blockIdx.x % groups, bh = blockIdx.x / groups, h = bh % p.L.nkv, b = bh / p.L.nkv;
-  const int r = W == 1 ? 4 * g + (threadIdx.x >> 5) : g;
-  int row0, n, kv;
-  griddep_serve();
-  if (!attn_request(p, b, nullptr, row0, n, kv) || r >= n * p.G) return;
-  const Units x(p, n, kv);
-  const int64_t units = __ldcg(sp.pref + p.B);
-  const int shares = shares_of(units, ctas);
-  const int block = r / kRows;
-  const int64_t u0 = __ldcg(sp.pref + b) + block * p.L.nkv * x.pair + h * (block < x.full ? x.pair : x.last) + kSegUnits;
-  const int c0 = share_of(units, shares, u0), c1 = share_of(units, shares, u0 + (int64_t)x.weight(block) * (x.keys - 1));
-  const int tok = r / p.G, hh = h * p.G + (r - tok * p.G);
-  const int64_t at = (int64_t)(row0 + tok) * (p.L.nkv * p.G) + hh;
-  const float *first = sp.first + at * PW + 4, *more = sp.more + ((int64_t)(c0 + 1) * kRows + (r - block * kRows)) * PW + 4;
-  join_row<D, W>(p, c1 - c0 + 1, [&](int i) { return i == 0 ? first : more + (int64_t)(i - 1) * kRows * PW; }, kOScale,
-                 p.o + (row0 + tok) * p.o_stride + (int64_t)hh * D);
-}
-
-static int num_ctas() {
-  const int sms = ft_host::num_sms();
-  return sms > 0 ? sms : 152;
-}
-
 template <int D>
 static cudaError_t launch(const AttnPagedParams& p, void* workspace, cudaStream_t st) {
   static int allowed[64] = {0};
@@ -887,34 +741,19 @@ static cudaError_t launch(const AttnPagedParams& p, void* workspace, cudaStream_
     if (fa.numRegs < kRegLaunch) return cudaErrorInvalidConfiguration;
     allowed[dev] = 1;
   }
-  const int ctas = num_ctas();
-  Split sp;
-  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);  // (given at 16 bytes)
-  sp.pref = reinterpret_cast<int64_t*>(ws);
-  ws += align_up((size_t)(p.B + 1) * 8, 256);
-  sp.q = reinterpret_cast<uint16_t*>(ws);
-  const int64_t q_rows = (int64_t)p.total_q * p.L.nkv * p.G;
-  ws += (size_t)q_rows * D * 2;  // (a multiple of 128)
-  sp.more = reinterpret_cast<float*>(ws);
-  sp.first = sp.more + (size_t)ctas * kRows * Cfg<D>::kPW;
-  const int per = kPrepThreads / 32 * (32 / (D / 32));
-  cudaError_t e = launch_served(tree_prepare_kernel<D>, dim3((unsigned)(1 + (q_rows + per - 1) / per)), dim3(kPrepThreads), 0, st, 1, p, sp);
+  Split sp = split_of(workspace, p.B, (int64_t)p.total_q * p.L.nkv * p.G, D, num_sms(), kRows);
+  sp.seg = kSegUnits;
+  sp.odd = 1.0f, sp.up = kOScale;
+  cudaError_t e = launch_prepare<D>(p, sp, st);
   if (e != cudaSuccess) return e;
-  e = launch_served(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::kSmem, st, 1, p, sp);
-  if (e != cudaSuccess) return e;
-  // four warps a row where a row may have more than twelve partials (a warp loads eight at once)
-  const int rows = p.max_q * p.G;
-  const bool wide = ((int64_t)p.total_q * p.G / kRows + std::min(p.B, p.total_q)) * p.L.nkv * 12 < ctas;
-  const int groups = wide ? rows : (rows + 3) / 4;
-  return launch_served(wide ? tree_join_kernel<D, 4> : tree_join_kernel<D, 1>, dim3((unsigned)(p.B * p.L.nkv * groups)), dim3(128), 0, st, 1, p,
-                       sp, ctas, groups);
+  e = launch_served(tree_kernel<D>, dim3((unsigned)sp.ctas), dim3(kThreads), Cfg<D>::kSmem, st, 1, p, sp);
+  return e != cudaSuccess ? e : launch_join<D>(p, sp, st);
 }
 
 }  // namespace tree
 
 size_t attn_tree_ws(int nkv, int G, int head_dim, int B, int total_q) {
-  return align_up((size_t)(B + 1) * 8, 256) + ((size_t)tree::num_ctas() * tree::kRows + (size_t)total_q * nkv * G) * (head_dim + 8) * 4 +
-         (size_t)total_q * nkv * G * head_dim * 2 + 16;
+  return tree::split_bytes(B, (int64_t)total_q * nkv * G, head_dim, tree::num_sms(), tree::kRows);
 }
 
 bool attn_tree_fits(const AttnPagedParams& p) {
