@@ -93,8 +93,11 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
   constexpr int CH = D / 32, kBatch = 8;  // channels CH lane .. + CH - 1 of each lane
   const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(row(i)));
-  M = warp_max(M);
+  const bool one = n <= kBatch && W == 1;  // all at once: the maxima come with the rest
+  if (!one) {
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(row(i)));
+    M = warp_max(M);
+  }
   float lt = 0.0f, o[CH] = {};
   for (int c = kBatch * warp; c < n; c += kBatch * W) {
     float2 ml[kBatch];
@@ -111,6 +114,11 @@ __device__ __forceinline__ void join_row(const AttnPagedParams& p, int n, Row ro
         const float2 f = __ldcg(reinterpret_cast<const float2*>(q + 4) + lane);
         x[i][0] = f.x, x[i][1] = f.y;
       }
+    }
+    if (one) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i < n) M = fmaxf(M, ml[i].x);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {

@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
         fence_after();
         const int c0 = both ? D / 2 * t : 0, c1 = both ? c0 + D / 2 : D;
         if (ok && !idle) {
-          const int rb = first_row + row, to = r / p.G;  // row of the block
+          const int rb = first_row + row;  // row of the block
           float* dst = w.j0 > 0 ? sp.more + ((int64_t)blockIdx.x * kRows + rb) * C::kPW
-                                : sp.first + ((int64_t)(w.row0 + to) * (p.L.nkv * p.G) + w.h * p.G + (r - to * p.G)) * C::kPW;
+                                : sp.first + ((int64_t)(w.h * p.total_q + w.row0) * p.G + r) * C::kPW;
           if (there && c0 == 0) *reinterpret_cast<float2*>(dst + 4) = make_float2(M, L);
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
@@ -644,44 +644,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
       if (!all_wait(drained, 0)) ok = false;
     } else if (warp == kAheadWarp) {
       // ---------------------------------------------------------- segments
-      const int64_t units = __ldcg(sp.pref + p.B);
-      const int shares = shares_of(units, gridDim.x), c = min((int)blockIdx.x, shares);
-      const int64_t u = share_begin(units, shares, c);
-      int64_t off = 0, left = share_begin(units, shares, min(c + 1, shares)) - u;  // place in the request's units, units of the share left
-      int b = -1, row0 = 0, n = 0, kv = 0;
-      bool fresh = true;
-      if (left > 0) {
-        // the last request whose prefix sum is <= u, by up to three steps of 32 candidates
-        b = 0;
-        for (int st = p.B > 1024 ? 1024 : p.B > 32 ? 32 : 1; st; st >>= 5) {
-          const int i = b + (lane + 1) * st;
-          b += st * __popc(__ballot_sync(0xffffffffu, i < p.B && __ldcg(sp.pref + min(i, p.B)) <= u));
-        }
-        off = u - __ldcg(sp.pref + b);
-      }
-      Segment w = {};
+      Share share;
+      share.begin(p, sp, lane);
       for (uint32_t k = 0; ok; ++k) {
+        Segment w = {};
+        int block = 0;
         w.b = -1;
-        while (b >= 0 && b < p.B && left > 0 && w.b < 0) {
-          if (fresh) {
-            if (!attn_request(p, b, nullptr, row0, n, kv)) n = 0;
-            fresh = false;
-          }
-          const Units x(p, n, kv, sp.seg);
-          if (n == 0 || off >= x.total) {
-            ++b, off = 0, fresh = true;
-            continue;
-          }
-          const int64_t span = p.L.nkv * x.pair;
-          const int block = (int)min(off / span, (int64_t)x.full);
-          const int64_t in = off - block * span, len = block < x.full ? x.pair : x.last;
-          const int h = (int)(in / len);
-          const int64_t at = in - h * len, go = min(left, len - at);
-          w.j0 = x.tile(block, at), w.j1 = x.tile(block, at + go);
-          off += go, left -= go;
-          if (w.j0 == w.j1) continue;  // the share ends in what the segment costs beside its positions
-          w.b = b, w.row0 = row0, w.n = n, w.kv = kv, w.h = h;
-          w.r0 = block * kRows, w.nrow = min(x.rows - w.r0, kRows);
+        if (share.next(p, sp, block, w.h, w.j0, w.j1)) {
+          w.b = share.b, w.row0 = share.req.y, w.n = share.req.z, w.kv = share.req.w;
+          w.r0 = block * kRows, w.nrow = min(w.n * p.G - w.r0, kRows);
         }
         if (k >= kWorks && !all_wait(work_empty + 8 * (k % kWorks), (k / kWorks - 1) & 1)) ok = false;
         if (ok && lane == 0) {
@@ -708,11 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
           }
           const uint32_t to = sm32 + C::kOffQ + q_at.slot * C::kTile;
           const int rows = min(128, w.nrow - 128 * t), c = lane % kChunks;
+          const uint16_t* from = sp.q + ((int64_t)(w.h * p.total_q + w.row0) * p.G + w.r0 + 128 * t) * D + 8 * c;
 #pragma unroll 4
-          for (int r = lane / kChunks; r < rows; r += 32 / kChunks) {
-            const int rr = w.r0 + 128 * t + r, tok = rr / p.G;
-            cp_async16(to + chunk_at(128, r, c), sp.q + ((int64_t)(w.row0 + tok) * (p.L.nkv * p.G) + w.h * p.G + (rr - tok * p.G)) * D + 8 * c);
-          }
+          for (int r = lane / kChunks; r < rows; r += 32 / kChunks) cp_async16(to + chunk_at(128, r, c), from + (int64_t)r * D);
           cp_async_wait_all();
           fence_proxy_async_smem();
           arrive(q_full + 8 * q_at.slot);
@@ -757,7 +726,7 @@ size_t attn_tree_ws(int nkv, int G, int head_dim, int B, int total_q) {
 }
 
 bool attn_tree_fits(const AttnPagedParams& p) {
-  return (int64_t)p.B * p.L.nkv <= INT32_MAX / std::max<int64_t>(1, (int64_t)p.max_q * p.G) && (int64_t)p.total_q * p.L.nkv * p.G < (int64_t)INT32_MAX * 8;
+  return tree::units_fit(p);
 }
 
 cudaError_t launch_attn_tree(const AttnPagedParams& p, int head_dim, void* workspace, cudaStream_t st) {
