@@ -448,10 +448,11 @@ static int few_ctas(int nt) {
   if (sms <= 0) sms = 152;
   return sms * (nt == 1 ? 4 : 2);
 }
-// 8-column tiles for max_q tokens of a group of G heads; 0: too many rows for this kernel.  The same for trees, whose
-// many rows have a kernel of their own (ft_attn_tree.cu).  Measured there, this kernel against that (us): 32 requests of up
-// to 4096 positions, 32 heads over 8, trees of 4 / 8 tokens (16 / 32 rows) 36 / 63 and 58 / 67; one of 32768, 64 heads
-// over 8, trees of 2 / 4 tokens 22 / 34 and 33 / 34.
+// 8-column tiles for max_q tokens of a group of G heads; 0: too many rows for this kernel.
+// Trees of more than 16 rows have kernels of their own, ft_attn_tree_few.cu up to 32 and ft_attn_tree.cu above.  Measured,
+// this kernel against that of up to 32 rows (us): 32 requests of up to 4096 positions, 32 heads over 8, trees of 4 / 8
+// tokens (16 / 32 rows) 36 / 42 and 58 / 45; one of 32768, 64 heads over 8, trees of 2 / 4 tokens 22 / 30 and 33 / 32;
+// and that one against the one of more rows, 32 requests of 7 tokens (28 rows) 45 / 61.
 static int few_tiles(int max_q, int G) {
   const int64_t rows = (int64_t)max_q * G;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0;
@@ -494,15 +495,17 @@ static cudaError_t launch_few(const AttnPagedParams& p, void* workspace, cudaStr
 
 template <bool TREE>
 static cudaError_t launch_few_any(const AttnPagedParams& p, int head_dim, int nt, void* ws, cudaStream_t st) {
-  if (head_dim == 128)
-    return nt == 1 ? launch_few<128, 1, TREE>(p, ws, st) : nt == 2 ? launch_few<128, 2, TREE>(p, ws, st) : launch_few<128, 4, TREE>(p, ws, st);
-  return nt == 1 ? launch_few<64, 1, TREE>(p, ws, st) : nt == 2 ? launch_few<64, 2, TREE>(p, ws, st) : launch_few<64, 4, TREE>(p, ws, st);
+  if constexpr (!TREE) {
+    if (nt == 4) return head_dim == 128 ? launch_few<128, 4, false>(p, ws, st) : launch_few<64, 4, false>(p, ws, st);
+  }
+  if (head_dim == 128) return nt == 1 ? launch_few<128, 1, TREE>(p, ws, st) : launch_few<128, 2, TREE>(p, ws, st);
+  return nt == 1 ? launch_few<64, 1, TREE>(p, ws, st) : launch_few<64, 2, TREE>(p, ws, st);
 }
 
 static size_t attn_ws(const ft_block_cfg* c, int B, int total_q, int max_q, bool tree) {
   if (ft_host::check_cfg(c) != FT_OK || B < 1 || B > kApMaxB || total_q < 0 || max_q < 1) return 0;
   const int nt = few_tiles(std::min(max_q, std::max(total_q, 1)), c->n_q / c->n_kv);
-  if (tree && nt != 1)
+  if (tree && (nt == 0 || nt == 4))
     return nt == 0 ? attn_tree_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q) : attn_tree_few_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   if (nt == 0) return attn_tiles_ws(c->n_kv, c->n_q / c->n_kv, c->head_dim, B, total_q);
   return align_up((size_t)(B + 1) * 4, 256) + (size_t)few_ctas(nt) * 2 * (8 * nt) * (c->head_dim + 4) * 4;
@@ -552,7 +555,7 @@ static int attn_call(const ft_block_cfg* c, const void* pages, int n_pages, int 
   p.mask = tree ? mask : nullptr;
   p.mask_stride = mask_stride;
   const int nt = few_tiles(p.max_q, p.G);
-  if (tree && nt != 1) {
+  if (tree && (nt == 0 || nt == 4)) {
     if (!attn_tree_fits(p)) return FT_ERR_UNSUPPORTED;
     const cudaError_t e = nt == 0 ? launch_attn_tree(p, c->head_dim, workspace, stream) : launch_attn_tree_few(p, c->head_dim, workspace, stream);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;

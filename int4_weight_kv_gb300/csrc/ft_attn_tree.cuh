@@ -63,14 +63,14 @@ __device__ __forceinline__ int share_of(int units, int ctas, int u) {
 struct Share {
   int b, off, left;  // request (behind the last one or < 0: no more), place in its units, units left
   int4 req;          // its record
-  // (all lanes; the records of up to 31 requests and the sum in one load)
+  // (all lanes; the records of up to 32 requests are loaded together with the sum)
   __device__ __forceinline__ void begin(const AttnPagedParams& p, const Split& sp, int lane) {
-    int4 r = __ldcg(sp.req + min(lane, p.B));
-    const int units = p.B < 32 ? __shfl_sync(0xffffffffu, r.x, p.B) : __ldcg(sp.req + p.B).x;
+    int4 r = __ldcg(sp.req + min(lane, p.B - 1));
+    const int units = __ldcg(&sp.req[p.B].x);
     const int shares = shares_of(units, gridDim.x), c = min((int)blockIdx.x, shares), u = share_begin(units, shares, c);
     left = share_begin(units, shares, min(c + 1, shares)) - u;
     b = 0;  // the last request whose units begin at or before u
-    if (p.B < 32) {
+    if (p.B <= 32) {
       b = __popc(__ballot_sync(0xffffffffu, lane > 0 && lane < p.B && r.x <= u));
     } else {  // by steps of 32 candidates
       int st = 1;
@@ -83,7 +83,7 @@ struct Share {
         }
       r = __ldcg(sp.req + b);
     }
-    const int from = p.B < 32 ? b : 0;
+    const int from = p.B <= 32 ? b : 0;
     req.x = __shfl_sync(0xffffffffu, r.x, from), req.y = __shfl_sync(0xffffffffu, r.y, from);
     req.z = __shfl_sync(0xffffffffu, r.z, from), req.w = __shfl_sync(0xffffffffu, r.w, from);
     off = u - req.x;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const AttnPagedParams p,
   const int g = blockIdx.x % groups, bh = blockIdx.x / groups, h = bh % p.L.nkv, b = bh / p.L.nkv;
   const int r = W == 1 ? 4 * g + (threadIdx.x >> 5) : g;
   griddep_serve();
-  const int units = __ldcg(sp.req + p.B).x;
+  const int units = __ldcg(&sp.req[p.B].x);
   const int4 req = __ldcg(sp.req + b);
   if (r >= req.z * p.G) return;
   const Units x(p, req.z, req.w, sp.seg);
