@@ -291,7 +291,9 @@ int ft_attn_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, 
  * (a token that sees itself and its ancestors; all of a block; none): a row that sees nothing gets zeros.
  * A token whose entry would be at a negative position has none; bits that name it are ignored.  The position
  * that a token is rotated to (its depth in the tree) need not be that of its entry: see
- * ft_kv_append_rope_paged_int4.  Everything else (limits, arithmetic, device conditions, workspace) is as there. */
+ * ft_kv_append_rope_paged_int4.  Everything else (arithmetic, device conditions, workspace) is as there, and so are the
+ * limits; with R = min(max_q, total_q) n_q / n_kv > 16 also B n_kv ceil(R / 256) (table_stride page_size / 64 + 18),
+ * B n_kv R and total_q n_q stay below 2^31 - 128, else FT_ERR_UNSUPPORTED. */
 size_t ft_attn_tree_workspace_bytes(const ft_block_cfg *cfg, int B, int total_q, int max_q);
 int ft_attn_tree_paged_int4(const ft_block_cfg *cfg, const void *pages, int n_pages, int page_size,
                             const uint16_t *q_bf16, int64_t q_stride, const int32_t *cu_seqlens, const int32_t *kv_len,

@@ -34,6 +34,7 @@ constexpr float kLazy = 8.0f;
 constexpr int kWorks = 2;  // items known ahead
 constexpr int kLooks = 8;  // partly visible tiles of V looked through ahead: more than the ring holds, and one item's, together
 constexpr int kPassLeft = 1;  // products of a batch issued behind the end of its turn (1, 2, 3, 5: 344, 349, 360, 371 us for 8192 tokens)
+static_assert(kPassLeft > 0 && kPassLeft < 64 / 16, "the turn is passed on in every batch");
 // Registers of a thread: softmax twice, the others; the sum over the three warpgroups is what the block is
 // launched with, kThreads x kRegLaunch.
 constexpr int kRegSoftmax = 208, kRegOther = 88, kRegLaunch = 168;

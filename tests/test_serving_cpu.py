@@ -103,6 +103,10 @@ def test_tree_refusals(ft):
     assert call(total=0) == ft.FT_OK and call(wsb=size - 1) == ft.FT_ERR_WORKSPACE and call(ps=40) == ft.FT_ERR_UNSUPPORTED
     for big in (dict(total=2 ** 29), dict(stride=2 ** 28), dict(B=8193)):
         assert call(wsb=2 ** 60, **big) == ft.FT_ERR_UNSUPPORTED, big
+    # what grows with the rows: blocks of 256, rows of the batch, rows of the call
+    for big in (dict(B=4096, stride=2048, max_q=2000, total=2000, ms=63), dict(B=8192, stride=1, max_q=2 ** 15, total=2 ** 15, ms=1024),
+                dict(B=1, stride=1, total=2 ** 26, max_q=100, ms=4)):
+        assert call(wsb=2 ** 60, **big) == ft.FT_ERR_UNSUPPORTED, big
     for bad in (dict(pages=None), dict(q=None), dict(o=None), dict(cu=None), dict(kv=None), dict(table=None), dict(ws=None),
                 dict(ws=FAKE + 4), dict(B=0), dict(total=-1), dict(max_q=0), dict(stride=0), dict(qs=4095), dict(os=1),
                 dict(scale=0.0), dict(scale=float("nan")), dict(mask=None), dict(mask=FAKE + 2), dict(ms=1), dict(ms=0)):

@@ -349,7 +349,7 @@ def test_tree_long(heads, qlens, kvlens):
     a.check(o, heads=[0, heads // 2 + 1, heads - 1])
 
 
-@pytest.mark.parametrize("qlens", [[3, 2, 4], [40, 2, 60]])
+@pytest.mark.parametrize("qlens", [[3, 2, 4], [6, 2, 7], [40, 2, 60]])
 def test_tree_bad_requests(qlens):
     a = Tree(8, 2, 128, 16, qlens, [50, 70, 90])
     want, _ = a.run()
@@ -373,7 +373,7 @@ def test_tree_bad_requests(qlens):
 
 
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), 2.0 ** 13])
-@pytest.mark.parametrize("n,d", [(5, 128), (100, 128), (100, 64)])
+@pytest.mark.parametrize("n,d", [(5, 128), (5, 64), (3, 128), (100, 128), (100, 64)])
 def test_tree_entries_that_a_row_does_not_see(n, d, what):
     """A new token's entry with scales that are not finite, or far above its neighbours', is not there for rows whose masks
     leave it out."""
@@ -389,6 +389,78 @@ def test_tree_entries_that_a_row_does_not_see(n, d, what):
     a.set_scales(0, [60 + bad], k=0.5, v=0.5)                                           # the oracle's: any finite one
     a.check(o, floor=2.0 ** -27)
     assert k is not None
+
+
+@pytest.mark.parametrize("n", [3, 7, 24])
+@pytest.mark.parametrize("B", [31, 32, 33, 1024, 1100])
+def test_tree_many_requests(B, n):
+    """Trees of every size up to n, none in many: the shares find their requests however many there are."""
+    g = np.random.default_rng(B + n)
+    qlens = np.where(g.random(B) < 0.4, 0, g.integers(0, n + 1, B))
+    qlens[-1] = n
+    a = Tree(8, 2, 64, 16, qlens.tolist(), (qlens + g.integers(0, 40, B)).tolist())
+    o, st = a.run()
+    assert st == 0
+    a.check(o, reqs=sorted({*range(0, B, max(B // 20, 1)), B - 2, B - 1}))
+
+
+@pytest.mark.parametrize("n,d", [(3, 128), (7, 128), (7, 64), (40, 128), (40, 64)])
+@pytest.mark.parametrize("down", [False, True])
+def test_tree_scores_that_rise(n, d, down):
+    """Each 64 positions' scores 1.3 times those before (behind) them: the running maximum moves at every tile, or at none."""
+    a = Tree(8, 2, d, 64, [n, n], [1500, 900])
+    for b, kv in enumerate(a.kvlens):
+        for i in range(0, kv, 64):
+            a.set_scales(b, range(i, min(i + 64, kv)), k=0.02 * 1.3 ** ((kv - i if down else i) // 64))
+    o, st = a.run()
+    assert st == 0
+    a.check(o)
+
+
+@pytest.mark.parametrize("n", [1, 4, 7, 40])
+def test_tree_rows_anywhere(n):
+    """q and o at odd addresses and strides, nothing written between o's rows."""
+    a = Tree(8, 2, 128, 16, [n, 2], [n + 150, 70])
+    want, _ = a.run()
+    a.q = a.q.contiguous()
+    buf = torch.full((a.total * (8 * 128 + 5) + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
+    src = torch.zeros_like(buf)
+    q, o = (t[3:].as_strided((a.total, 8, 128), (8 * 128 + 5, 128, 1)) for t in (src, buf))
+    q.copy_(a.q[:a.total])
+    _, st = a.run(q=q, o=o)
+    assert st == 0 and torch.equal(o, want[:a.total])
+    o.fill_(7.0)
+    assert (buf == 7.0).all()
+
+
+def test_pool_beyond_4_gib():
+    """Rows placed, moved and attended to on pages more than 2^32 bytes into the pool: as on its first pages."""
+    cfg, ps, n_pages, few = _cfg(8, 2, 128), 64, 2 ** 32 // (2 * 64 * 132) + 40, 20
+    big = torch.empty(ft.ft_kv_pages_bytes(cfg, n_pages, ps), dtype=torch.uint8, device="cuda").view(n_pages, -1)
+    g, base = np.random.default_rng(2), n_pages - few
+    assert base * big.shape[1] > 2 ** 32
+    x, _ = _bf16(g, 1000, 4, 128)
+    slots = g.permutation(few * ps)[:1000]
+    small = torch.zeros((few, big.shape[1]), dtype=torch.uint8, device="cuda")
+    big[base:] = 0
+    src, dst = slots[:100].reshape(2, 50), np.setdiff1d(np.arange(few * ps), slots)[:100].reshape(2, 50)
+    for pool, pages, at in ((small, few, 0), (big, n_pages, base)):
+        st = _status()
+        ft.check(ft.ft_kv_append_rope_paged_int4(cfg, pool.view(-1), pages, ps, x[:, :2], x[:, 2:], None, _i32(np.arange(1000)), _i32(slots + at * ps), 1000,
+                                                 dev_status=st))
+        ft.check(ft.ft_kv_move_paged_int4(cfg, pool.view(-1), pages, ps, _i32(src + at * ps), _i32(dst + at * ps), st))
+        assert ft.ft_read_device_status(st) == 0
+    assert torch.equal(big[base:], small) and small.any()
+    for n in (2, 7, 40):
+        a = Tree(8, 2, 128, ps, [n, n], [600, 500])
+        a.table = np.arange(20).reshape(2, 10)
+        out = []
+        for a.pool, a.n_pages, at in ((small.view(-1), few, 0), (big.view(-1), n_pages, base)):
+            a.table = np.arange(20).reshape(2, 10) + at
+            o, st = a.run()
+            assert st == 0
+            out.append(o)
+        assert torch.equal(*out) and out[0][:a.total].any()
 
 
 # ---------------------------------------------------------------- prompts
@@ -433,6 +505,7 @@ class Prompt:
 PROMPTS = [
     (8, 2, 64, [1]), (32, 8, 128, [2]), (32, 8, 128, [31, 32, 33]), (4, 4, 128, [127, 128, 129, 1]), (4, 4, 64, [255, 256, 257]),
     (64, 8, 128, [1, 0, 16, 17]), (42, 6, 64, [100, 37]), (7, 1, 128, [259, 5]), (12, 4, 128, [0, 85, 86, 0]), (10, 2, 64, [1] * 70),
+    (8, 2, 64, [70, 1, 300] + [9] * 29), (8, 2, 128, [70, 1, 700] + [9] * 30),
     (32, 8, 128, [300, 1, 511, 512, 513, 77]), (8, 8, 128, [700]), (6, 2, 128, [1025, 640]), (16, 2, 64, [900, 1111]),
 ]
 
@@ -479,6 +552,20 @@ def test_prompt_in_place():
     buf = a.q.clone()
     o, st = a.run(o=buf, q=buf)
     assert st == 0 and torch.equal(o[:a.total], want[:a.total])
+
+
+@pytest.mark.parametrize("off", [1, 2, 8])
+def test_prompt_rows_anywhere(off):
+    """o at any address and stride, q, k and v at strides of their own; nothing written between o's rows."""
+    a = Prompt(8, 2, 128, [300, 40, 129])
+    want, _ = a.run()
+    a.k, a.v = a.k.contiguous(), torch.nn.functional.pad(a.v, (0, 0, 0, 3))[:, :2]
+    buf = torch.full((a.total * (8 * 128 + off) + 2 * off,), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = buf[off:].as_strided((a.total, 8, 128), (8 * 128 + off, 128, 1))
+    _, st = a.run(o=o)
+    assert st == 0 and torch.equal(o, want[:a.total])
+    o.fill_(7.0)
+    assert (buf == 7.0).all()
 
 
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
@@ -648,6 +735,26 @@ def test_on_another_stream():
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     assert torch.equal(a.run(stream=side)[0], want_p) and torch.equal(t.run(stream=side)[0], want_t)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, leave each other's results alone."""
+    trees = [Tree(8, 2, 128, 16, [9, 3], [2000, 300], seed=1), Tree(32, 8, 128, 64, [7] * 6, [900] * 6), Tree(8, 2, 64, 16, [100, 70], [3000, 500])]
+    prompts = [Prompt(8, 2, 128, [900, 40]), Prompt(8, 2, 64, [33] * 20)]
+    want = [a.run()[0] for a in trees + prompts]
+    got = [torch.full_like(w, 7.0) for w in want]
+    ws = [torch.empty(ft.ft_attn_tree_workspace_bytes(a.cfg, a.B, a.total, max(a.qlens)), dtype=torch.uint8, device="cuda") for a in trees]
+    ints = [[_i32(x) for x in ((a.cu, a.kvlens, a.table) if a in trees else (a.cu,))] for a in trees + prompts]
+    streams = [torch.cuda.Stream() for _ in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (a, s, o, n) in enumerate(zip(trees + prompts, streams, got, ints)):
+            if i < len(trees):
+                ft.check(ft.ft_attn_tree_paged_int4(a.cfg, a.pool, a.n_pages, a.ps, a.q, *n, a.mask, a.B, a.total, max(a.qlens), a.scale, o, ws[i], None, s))
+            else:
+                ft.check(ft.ft_attn_prompt_bf16(a.cfg, a.q, a.k, a.v, n[0], a.B, a.total, max(a.lens), a.scale, o, None, s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_arguments_of_the_wrong_kind():
