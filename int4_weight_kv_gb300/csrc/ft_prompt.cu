@@ -16,6 +16,10 @@
 // finite (0 x infinity would reach the rows before them), which are noted for the rows that see them.
 // The running max moves only when a score passes it by 2^8 (P is BF16, sums are FP32), so O is rarely rescaled.
 // Every wait is bounded; a timeout sets FT_DEV_TIMEOUT and the CTA winds down.
+//
+// Measured, 32 heads over 8 of 128: 8192 tokens 317 us (1735 TFLOP/s of the causal half), 8 prompts of up to 2048 83 us
+// (1130), 100 tokens 7.5.  Bound by the tensor core, 2570 cycles a pair of tiles of which it works 2048, and by about
+// 6500 cycles a block beside its tiles: query rows in, first S, last P V, rows out, which only half overlap.
 #include <cuda.h>
 
 #include <algorithm>
@@ -378,35 +382,34 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
           }
           ++k;
           const Item w(p, got);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || t >= w.ntile) break;
-            if (q_uses[t] > 0 && !all_wait(q_empty + 8 * t, (q_uses[t] - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            ++q_uses[t];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(q_full + 8 * t, (uint32_t)(per_tile * p.G * D * 2));
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load(sm32 + C::kOffQ + t * C::kTile + c * (128 * 128), &map_q, 64 * c, w.h * p.G, w.row0 + w.tok0 + t * per_tile, q_full + 8 * t);
-            }
-          }
-          for (int j = 0; ok && j < 2 * w.nkt; ++j) {  // K0 V0 K1 V1 ...
-            if (used >= C::kSlots && !all_wait(empty + 8 * at.slot, at.parity ^ 1)) {
+          // K0, the query rows, V0 K1 V1 ...: the first tile's slot is free before the query rows' places are (8192 tokens:
+          // 324 -> 318 us).  One loop, as what runs once comes from a cold instruction cache.
+#pragma unroll 1
+          for (int step = 0; ok && step < 2 * w.nkt + 2; ++step) {
+            const int t = step - 1, j = step == 0 ? 0 : step - 2;  // query rows of tile t, or K / V tile j
+            const bool rows = t == 0 || t == 1;
+            if (t == 1 && w.ntile == 1) continue;
+            const uint32_t to = rows ? q_full + 8 * t : full + 8 * at.slot, free_at = rows ? q_empty + 8 * t : empty + 8 * at.slot;
+            const uint32_t before = rows ? (t == 0 ? q_uses[0] : q_uses[1]) : used >= C::kSlots ? 1u : 0u;
+            if (before > 0 && !all_wait(free_at, rows ? (before - 1) & 1 : at.parity ^ 1)) {
               ok = false;
               break;
             }
             if (lane == 0) {
-              mbar_arrive_expect_tx(full + 8 * at.slot, C::kTile);
+              mbar_arrive_expect_tx(to, rows ? (uint32_t)(per_tile * p.G * D * 2) : (uint32_t)C::kTile);
+              const CUtensorMap* map = rows ? &map_q : (j & 1) ? &map_v : &map_k;
+              const uint32_t dst = sm32 + (rows ? C::kOffQ + t * C::kTile : C::kOffRing + at.slot * C::kTile);
+              const int head = rows ? w.h * p.G : w.h, first = w.row0 + (rows ? w.tok0 + t * per_tile : kKeys * (j >> 1));
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load(sm32 + C::kOffRing + at.slot * C::kTile + c * (128 * 128), (j & 1) ? &map_v : &map_k, 64 * c, w.h, w.row0 + kKeys * (j >> 1),
-                         full + 8 * at.slot);
+              for (int c = 0; c < D / 64; ++c) tma_load(dst + c * (128 * 128), map, 64 * c, head, first, to);
             }
-            at.next();
-            ++used;
+            if (rows) {
+              if (t == 0) ++q_uses[0];
+              else ++q_uses[1];
+            } else {
+              at.next();
+              ++used;
+            }
           }
         }
         // the answer: a CTA that will not run any more, whose place is taken here, or none
