@@ -728,6 +728,38 @@ def test_drafted_steps_captured_and_without_overlap():
             ft.ft_set_pdl(was)
 
 
+@pytest.mark.parametrize("n", [2, 7, 40])
+def test_captured_with_other_lengths(n):
+    """A captured call reads its lengths, tables and masks when it is replayed."""
+    a, p = Tree(8, 2, 128, 16, [n, n], [300, 90]), Prompt(8, 2, 128, [200, 60, 40])
+    cu, kv, table, pcu = _i32(a.cu), _i32(a.kvlens), _i32(a.table), _i32(p.cu)
+    o, po = torch.zeros((a.total, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((p.total, 8, 128), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ft.ft_attn_tree_workspace_bytes(a.cfg, 2, a.total, n), dtype=torch.uint8, device="cuda")
+
+    def call():
+        ft.check(ft.ft_attn_tree_paged_int4(a.cfg, a.pool, a.n_pages, a.ps, a.q, cu, kv, table, a.mask, 2, a.total, n, a.scale, o, ws))
+        ft.check(ft.ft_attn_prompt_bf16(p.cfg, p.q, p.k, p.v, pcu, 3, p.total, 300, p.scale, po))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    a.kvlens, p.lens, p.cu = [n + 1, 64], [5, 295, 0], np.array([0, 5, 300, 300])
+    kv.copy_(_i32(a.kvlens))
+    pcu.copy_(_i32(p.cu))
+    a.table[0, :8] = a.table[0, 7::-1].copy()
+    table.copy_(_i32(a.table))
+    for m in (a.mask, o, po):
+        m.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = o.clone()
+    want, _ = a.run(max_q=n)
+    assert torch.equal(got, want[:a.total])
+    want, _ = p.run(max_len=300)
+    assert torch.equal(po, want[:p.total])
+
+
 def test_on_another_stream():
     """The calls take the stream that they are given: nothing waits for the current one."""
     a, t = Prompt(8, 2, 128, [300, 40]), Tree(8, 2, 128, 16, [9, 3], [200, 30])
