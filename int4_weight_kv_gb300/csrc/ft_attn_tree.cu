@@ -21,8 +21,8 @@
 // Bound by the chain from S over P to the next S: 4400 cycles a pair of tiles, of which the tensor core works for 2048,
 // while decoding keeps up (2 x 1250).  Leaving out the weights' 2^x, the decoding's stores or most of the products makes
 // 5 to 8% each.  Where products and decoding meet at shared memory (a product of two operands in it takes all of its 128
-// bytes a cycle) both wait.  Measured: one tree of 64 tokens over 32768 positions, 64 heads over 8 of 128, 90 us (758
-// TFLOP/s; with the kernel for prompts and chunks, masked, 124); a segment takes about as long as eight units beside its
+// bytes a cycle) both wait.  Measured: one tree of 64 tokens over 32768 positions, 64 heads over 8 of 128, 85 us of the
+// three kernels (804 TFLOP/s; with the kernel for prompts and chunks, masked, 124); a segment takes about as long as eight units beside its
 // positions (4: 80 us where 8 takes 70, 32 requests of up to 4096; 12 and 18: 70 and 74).
 // Slower: all of S kept in registers by the softmax (a warpgroup less for decoding, 136 us), code unrolled (see below),
 // P handed over as a whole (93 us) or from its first half on (135: the turn is then held while the rest is made).

@@ -113,6 +113,15 @@ def test_tree_refusals(ft):
         assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
 
 
+def test_tree_workspace_grows(ft):
+    """A workspace for the longest trees is enough for shorter ones, whichever kernel takes them."""
+    for n_q, n_kv, d in ((32, 8, 128), (8, 8, 64), (56, 7, 128)):
+        c = ft.make_cfg(n_q * d, n_q, n_kv, d, 1024)
+        for B, total in ((1, 600), (40, 900)):
+            sizes = [ft.ft_attn_tree_workspace_bytes(c, B, total, q) for q in range(1, 600)]
+            assert sizes == sorted(sizes) and sizes[-1] <= ft.ft_attn_tree_workspace_bytes(c, B + 1, total + 1, 600)
+
+
 def test_prompt_refusals(ft):
     c = ft.cfg_from_shape(synth.L8B)
     ok = dict(q=FAKE, qs=4096, k=FAKE, ks=1024, v=FAKE, vs=1024, cu=FAKE, B=4, total=100, max_len=40, scale=0.1, o=FAKE, os=4096)
