@@ -3,8 +3,8 @@
 //
 //   y = gamma x / sqrt(mean x^2 + eps),   z_i = y_i cos a - y_(i+d/2) sin a,  z_(i+d/2) = y_(i+d/2) cos a + y_i sin a
 //
-// Every byte is moved once.  Measured, 32 heads over 8 of 128: norm and rotation of 32k rows 62 us, 83% of the copy rate
-// (bound by HBM), of 32 rows 3.1; placement of 16k rows of k and v, with q's on the way and norms, 56 us (bound by
+// Every byte is moved once.  Measured, 32 heads over 8 of 128: norm and rotation of 17k tokens 62 us, 83% of the copy rate
+// (bound by HBM), of 32 tokens 3.1; placement of 9k tokens' k and v, with q's on the way and norms, 56 us (bound by
 // instructions: the exact quantiser and the shuffles of the rotation by H).
 #include <algorithm>
 
