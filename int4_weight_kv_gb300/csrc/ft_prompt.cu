@@ -24,6 +24,7 @@
 
 #include <algorithm>
 
+#include "ft_prompt_items.h"
 #include "ft_tc.cuh"
 
 namespace ft {
@@ -335,7 +336,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         return x;
       };
       const int inc = scan(sum), total = __shfl_sync(0xffffffffu, inc, 31);
-      int level = __reduce_max_sync(0xffffffffu, sum) - 1, above = 0;  // (a sequence a lane) blocks at places above `level`
+      ItemWalk walk(__reduce_max_sync(0xffffffffu, sum) - 1);  // (a sequence a lane)
       Ring at;
       uint32_t k = 0, q_uses[2] = {0, 0}, used = 0, asked = 0;
       int x = blockIdx.x;
@@ -351,13 +352,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
         if (i < total) {
           int4 got = make_int4(0, 0, 0, x % p.nkv);
           if (per == 1) {
-            uint32_t some = __ballot_sync(0xffffffffu, sum > level);
-            while (i - above >= __popc(some)) {  // (items come in ascending order)
-              above += __popc(some);
-              some = __ballot_sync(0xffffffffu, sum > --level);
-            }
-            const int l = __fns(some, 0, i - above + 1);
-            got.x = level * per_cta, got.y = __shfl_sync(0xffffffffu, row0, l), got.z = __shfl_sync(0xffffffffu, n, l);
+            const uint32_t some =
+                walk.find(i, [&](int level) { return __ballot_sync(0xffffffffu, sum > level); }, [](uint32_t bits) { return __popc(bits); });
+            const int l = __fns(some, 0, i - walk.above + 1);
+            got.x = walk.level * per_cta, got.y = __shfl_sync(0xffffffffu, row0, l), got.z = __shfl_sync(0xffffffffu, n, l);
           } else {
             i = total - 1 - i;
             const int l = __ffs(__ballot_sync(0xffffffffu, i < inc)) - 1;  // the lane that holds it

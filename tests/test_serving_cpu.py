@@ -1,6 +1,9 @@
 """Rows of the fused projection, draft trees, moved entries and prompt attention without a GPU: the
 oracle's pins and the refusals of the entry points (every call here returns before a launch)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -133,3 +136,57 @@ def test_prompt_refusals(ft):
                 dict(v=FAKE + 2), dict(ks=1028), dict(vs=1025), dict(q=FAKE + 2), dict(qs=4100)):
         assert call(**bad) == ft.FT_ERR_INVALID_ARG, bad
     assert call(ks=2 ** 40) == ft.FT_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------- what an item of prompt attention is
+WALK = r"""
+#include "ft_prompt_items.h"
+// blocks[n] of each sequence, items[k] in any order -> (sequence, place) of each; -1: none
+extern "C" void walk(const int* blocks, int n, const int* items, int k, int* out) {
+  int top = -1;
+  for (int b = 0; b < n; ++b) top = blocks[b] - 1 > top ? blocks[b] - 1 : top;
+  ft::ItemWalk w(top);
+  auto have = [&](int level) {
+    uint32_t bits = 0;
+    for (int b = 0; b < n; ++b) bits |= (uint32_t)(blocks[b] > level) << b;
+    return bits;
+  };
+  for (int i = 0; i < k; ++i) {
+    const uint32_t some = w.find(items[i], have, [](uint32_t bits) { return __builtin_popcount(bits); });
+    int at = items[i] - w.above, b = at < 0 ? n : 0;
+    for (; b < n; ++b)
+      if ((some >> b & 1) && at-- == 0) break;
+    out[2 * i] = b < n ? b : -1, out[2 * i + 1] = w.level;
+  }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def item_walk(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no host compiler")
+    at = tmp_path_factory.mktemp("walk")
+    (at / "walk.cpp").write_text(WALK)
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "int4_weight_kv_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, "-o", str(at / "walk.so"), str(at / "walk.cpp")], check=True)
+    fn = ctypes.CDLL(str(at / "walk.so")).walk
+
+    def run(blocks, items):
+        out = np.full((len(items), 2), -9, np.int32)
+        ptr = lambda a: a.ctypes.data_as(ctypes.POINTER(ctypes.c_int))  # noqa: E731
+        b, i = (np.ascontiguousarray(x, np.int32) for x in (blocks, items))
+        fn(ptr(b), len(b), ptr(i), len(i), ptr(out))
+        return [tuple(x) for x in out.tolist()]
+    return run
+
+
+@pytest.mark.parametrize("blocks", [[1], [4], [3, 1, 0, 5, 5], [0, 0, 2], [1] * 32, list(range(32)), [40, 1, 39, 2]])
+def test_prompt_items_in_any_order(item_walk, blocks):
+    """An item is the same block whatever items came before it: ascending, descending, shuffled, the same one again."""
+    want = [(b, level) for level in range(max(blocks) - 1, -1, -1) for b, n in enumerate(blocks) if n > level]
+    n, g = len(want), np.random.default_rng(len(blocks))
+    up = np.arange(n)
+    for items in (up, up[::-1], up[::2], g.permutation(n), g.integers(0, n, 200), np.repeat(up, 2)):
+        assert item_walk(blocks, items) == [want[i] for i in items]
