@@ -159,6 +159,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
   const int row = ((int)(blockIdx.x - 1) * (kPrepThreads / 32) + warp) * R + lane / LV, rows = p.total_q * nq;
   const bool in = row < rows;
   const int tok = in ? row / nq : 0, h = in ? row - tok * nq : 0, j = lane % LV, kvh = h / p.G;
+  // Rows before the first request's and behind the last one's (a call padded to a fixed number of rows) may hold anything:
+  // they are rotated as the others are, read by nobody, and not reported.  (Where the requests do not ascend from the one
+  // end to the other, that is reported, with the same condition.)
+  const bool owned = tok >= __ldcg(p.cu) && tok < __ldcg(p.cu + p.B);
   const uint16_t* src = p.q + tok * p.q_stride + (int64_t)h * D + 32 * j;
   f32x2 v[16];
   if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPa
     }
     to[j + NJ * q] = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  if ((over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
+  if (owned && (over & 0x7FFF7FFFu) != 0u) set_status(p.status, FT_DEV_RANGE);
 }
 
 // Joins the parts of each row, W = 1 or 4 warps a row.

@@ -391,6 +391,27 @@ def test_tree_entries_that_a_row_does_not_see(n, d, what):
     assert k is not None
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("n", [1, 4, 7, 40])
+def test_tree_rows_of_no_request(n, what):
+    """Rows before the first request's and behind the last one's (a call padded to a fixed number of rows) may hold
+    anything: nothing is reported and nothing written.  The same in a request's row is reported."""
+    a = Tree(8, 2, 128, 16, [n, n], [n + 150, n + 20])
+    want, st = a.run()
+    assert st == 0
+    rows, front, end = a.total, 3, 4
+    pad = lambda t, x, top, low: torch.cat([torch.full((top, *t.shape[1:]), x, dtype=t.dtype, device="cuda"), t,  # noqa: E731
+                                            torch.full((low, *t.shape[1:]), x, dtype=t.dtype, device="cuda")])
+    a.total, a.cu = rows + front + end, a.cu + front
+    a.q, a.mask = pad(a.q[:rows], what, front, end), pad(a.mask, -1, front, end)
+    o, st = a.run(max_q=n)
+    assert st == 0
+    assert torch.equal(o[front:front + rows], want[:rows]) and (o[:front] == 7.0).all() and (o[front + rows:] == 7.0).all()
+    a.q[front + rows - 1, 3] = what
+    o, st = a.run(max_q=n)
+    assert st == ft.FT_DEV_RANGE and torch.equal(o[front:front + n], want[:n])
+
+
 @pytest.mark.parametrize("n", [3, 7, 24])
 @pytest.mark.parametrize("B", [31, 32, 33, 1024, 1100])
 def test_tree_many_requests(B, n):
