@@ -340,10 +340,12 @@ int ft_kv_append_rope_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pag
  *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,   query head h reads KV head h / G.
  * q, o: [total, n_q, d], k, v: [total, n_kv, d] at their strides (elements); q, k and v at 16-byte
  * boundaries with strides of a multiple of 8, else FT_ERR_INVALID_ARG; o may be q where the strides are equal.  Rows that no
- * sequence owns are left as they are.  max_len: an upper bound of the lengths; it sizes the launch.
+ * sequence owns are left as they are.  max_len: an upper bound of the lengths, which are checked against it.
  * Arithmetic: BF16 products, FP32 sums, maxima and statistics, weights rounded to BF16 below the second
- * product (2^-8 each).  A row that sees a k or v which is not finite is not finite in the channels
- * concerned (it may be NaN in all of them); rows that do not see it, and other sequences, are not touched.
+ * product (2^-8 each).  A row that sees a v which is not finite is not finite in the channels concerned (it
+ * may be NaN in all of them).  A row with a score that is NaN or +infinity is NaN; a score of -infinity (an
+ * infinite value in k, q of the other sign) is a weight of 0.  Rows that do not see such a k or v, and other
+ * sequences, are not touched.
  * Device conditions: cu_seqlens not ascending within [0, total], or a length above max_len: FT_DEV_RANGE, that
  * sequence's rows are not written.  B <= 8192, total n_q / n_kv < 2^31, strides below 2^39, else
  * FT_ERR_UNSUPPORTED. */

@@ -617,6 +617,38 @@ def test_prompt_rows_that_are_not_finite(d, at, what):
     assert torch.equal(o[:a.total][same], want[:a.total][same])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [0, 60, 127, 128, 299])
+def test_prompt_infinite_keys(d, at):
+    """An infinite value of a k: rows whose q has its sign there (a score of +infinity) are NaN, those of the other sign (a
+    score of -infinity) have no weight for it."""
+    a = Prompt(8, 2, d, [50, 300, 129])
+    first, n = int(a.cu[1]), 300
+    a.k[first + at, 1, 5] = float("inf")
+    a.q[:, 4:, 5] = torch.where(torch.arange(len(a.q), device="cuda") % 2 == 0, 1.0, -1.0).to(torch.bfloat16)[:, None]
+    o, st = a.run()
+    assert st == 0
+    a.check(o, seqs=[0, 2])
+    a.check(o, seqs=[1], heads=[0, 3])
+    t = torch.arange(n, device="cuda")
+    up = a.q[first:first + n, 4, 5] > 0
+    sees = t >= at
+    alone = sees & (t == 0)                                                             # a row that sees that k only: 0 / 0
+    got = o[first:first + n, 4:].double()
+    assert torch.isnan(got[(sees & up) | alone]).all()
+    rows = ~((sees & up) | alone)
+    hidden = (t[None, :] > t[:, None]) | (t == at)[None, :] & sees[:, None]
+    k, v = (x[first:first + n, 1].double() for x in (a.k, a.v))
+    k[at] = 0
+    for h in range(4):
+        q = a.q[first:first + n, 4 + h].double()
+        w = torch.softmax((q @ k.T * a.scale).masked_fill(hidden, -torch.inf), -1)
+        o64, vn = w @ v, w @ v.norm(dim=-1)
+        dn = a.scale * (q.abs() @ k.abs().T).masked_fill(hidden, 0).amax(-1)
+        tol = (2.0 ** -16 * dn + 2.0 ** -8 + 2.0 ** -15) * vn + 2.0 ** -8 * o64.norm(dim=-1)
+        assert ((got[:, h] - o64).norm(dim=-1) <= tol)[rows].all()
+
+
 def test_prompt_bad_sequences():
     a = Prompt(8, 2, 128, [50, 300, 129])
     want, _ = a.run()
