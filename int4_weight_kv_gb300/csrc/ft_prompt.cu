@@ -8,12 +8,13 @@
 //   O += P V    A = P from tensor memory (over S's columns), B = V from shared memory (as it lies there: MN-major)
 // with BF16 operands and FP32 accumulators in tensor memory (S 2 x 128 columns, O 2 x d).
 //
-// Roles: two warpgroups of softmax (one row per thread, a tile each); a warp of which one thread issues the
-// TMA copies of Q, K and V; a warp of which one issues the products, for the tiles by turns
+// Roles: two warpgroups of softmax (one row per thread, a tile each); a warp that works out the items and of which one
+// thread issues the TMA copies of Q, K and V; two that issue the products, one for each tile, which take the tensor core
+// by turns
 //   PV0(j) QK0(j+1) PV1(j) QK1(j+1) ...
-// so that the tensor core works for one while the other's softmax runs; and two warps that look through the V
-// tiles which some row sees in part: rows behind the sequence's end become zeros, and so do rows that are not
-// finite (0 x infinity would reach the rows before them), which are noted for the rows that see them.
+// so that it works for one while the other's softmax runs; and one that looks through the V tiles which some row sees
+// in part: rows behind the sequence's end become zeros, and so do rows that are not finite (0 x infinity would reach
+// the rows before them), which are noted for the rows that see them.
 // The running max moves only when a score passes it by 2^8 (P is BF16, sums are FP32), so O is rarely rescaled.
 // Every wait is bounded; a timeout sets FT_DEV_TIMEOUT and the CTA winds down.
 //
@@ -55,7 +56,6 @@ struct Cfg {
 };
 
 struct Params {
-  const uint16_t* q;
   uint16_t* o;
   int64_t o_stride;
   const int32_t* cu;
@@ -666,7 +666,6 @@ int ft_attn_prompt_bf16(const ft_block_cfg* c, const uint16_t* q_bf16, int64_t q
   if (!ft::prompt::make_map(&q, q_bf16, D, c->n_q, total, q_stride, G, per_tile) ||
       !ft::prompt::make_map(&k, k_bf16, D, c->n_kv, total, k_stride, 1, 128) || !ft::prompt::make_map(&v, v_bf16, D, c->n_kv, total, v_stride, 1, 128))
     return FT_ERR_CUDA;
-  p.q = q_bf16;
   p.o = o_bf16;
   p.o_stride = o_stride;
   p.cu = cu_seqlens;
