@@ -86,6 +86,19 @@ def test_norm_rope_odd_address_and_negative_positions():
     assert np.all(np.abs(o.float().cpu().numpy() - z) <= tol + 2.0 ** -8 * np.abs(z))
 
 
+@pytest.mark.parametrize("base", [0.25, 2.0 ** -7, 1.0])
+def test_norm_rope_bases_below_one(base):
+    """Frequencies that grow along the channels, past a turn a position."""
+    cfg, g, total = _cfg(4, 2, 64), np.random.default_rng(11), 40
+    cfg.rope_base = base
+    x, xf = _bf16(g, total, 6, 64)
+    pos = _positions(g, total, 2 ** 16)
+    out = torch.empty((total, 6, 64), dtype=torch.bfloat16, device="cuda")
+    ft.check(ft.ft_qk_norm_rope_bf16(cfg, x[:, :4], x[:, 4:], None, None, _i32(pos), total, out[:, :4], out[:, 4:]))
+    z, tol = _turned(xf, None, pos, cfg)
+    assert np.all(np.abs(out.float().cpu().numpy() - z) <= tol + 2.0 ** -8 * np.abs(z))
+
+
 # ---------------------------------------------------------------- placement on the way
 def _pool(cfg, n_pages, ps, fill=0xA5):
     return torch.full((ft.ft_kv_pages_bytes(cfg, n_pages, ps),), fill, dtype=torch.uint8, device="cuda")
@@ -391,6 +404,31 @@ def test_tree_entries_that_a_row_does_not_see(n, d, what):
     assert k is not None
 
 
+@pytest.mark.parametrize("k,v", [(float("nan"), 0.5), (0.5, float("nan")), (float("inf"), 0.5), (0.5, float("inf")), (2.0 ** 111, 0.5), (0.5, 2.0 ** 111),
+                                 (float("nan"), float("inf"))])
+@pytest.mark.parametrize("n,d", [(3, 128), (3, 64), (5, 128), (5, 64), (100, 128), (100, 64)])
+def test_tree_entries_that_some_rows_see(n, d, k, v):
+    """A new token's entry with a scale that is not finite, or 2^110 and more: the rows whose masks name it are NaN, those
+    beside them are as they would be with any other entry there, and the status says nothing."""
+    a = Tree(32, 8, d, 64, [n, n], [n + 60, n + 60])
+    bad, sees = n // 2, np.arange(n) % 2 == 1
+    for s in a.see:
+        s[:, bad] = sees
+    words = a.mask.shape[1]
+    a.mask = torch.from_numpy(np.concatenate([paged.mask_words(s, words) for s in a.see])).cuda()
+    a.set_scales(0, [60 + bad], k=0.5, v=0.5)
+    fine, st = a.run()
+    assert st == 0
+    a.set_scales(0, [60 + bad], k=k, v=v)
+    o, st = a.run()
+    assert st == 0
+    rows = torch.from_numpy(np.nonzero(sees)[0]).cuda()
+    assert torch.isnan(o[rows].float()).all()
+    a.set_scales(0, [60 + bad], k=0.5, v=0.5)                                           # the oracle's
+    o[rows] = fine[rows]
+    a.check(o)
+
+
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), 3e38])
 @pytest.mark.parametrize("n", [1, 4, 7, 40])
 def test_tree_rows_of_no_request(n, what):
@@ -410,6 +448,18 @@ def test_tree_rows_of_no_request(n, what):
     a.q[front + rows - 1, 3] = what
     o, st = a.run(max_q=n)
     assert st == ft.FT_DEV_RANGE and torch.equal(o[front:front + n], want[:n])
+
+
+@pytest.mark.parametrize("B", [40, 300])
+def test_tree_many_requests_of_many_rows(B):
+    """Batches of trees of 33 rows and more with d = 128, some without tokens."""
+    g = np.random.default_rng(B)
+    qlens = np.where(g.random(B) < 0.2, 0, g.integers(1, 25, B))
+    qlens[-1] = 24
+    a = Tree(32, 8, 128, 64, qlens.tolist(), (qlens + g.integers(0, 300, B)).tolist())
+    o, st = a.run()
+    assert st == 0
+    a.check(o, reqs=sorted({*range(0, B, max(B // 20, 1)), B - 2, B - 1}), heads=[0, 13, 31])
 
 
 @pytest.mark.parametrize("n", [3, 7, 24])
@@ -647,6 +697,17 @@ def test_prompt_infinite_keys(d, at):
         dn = a.scale * (q.abs() @ k.abs().T).masked_fill(hidden, 0).amax(-1)
         tol = (2.0 ** -16 * dn + 2.0 ** -8 + 2.0 ** -15) * vn + 2.0 ** -8 * o64.norm(dim=-1)
         assert ((got[:, h] - o64).norm(dim=-1) <= tol)[rows].all()
+
+
+def test_prompt_many_blocks_of_many_sequences():
+    """More than 32 prompts whose blocks are several a CTA, with d = 128."""
+    g = np.random.default_rng(9)
+    lens = np.where(g.random(70) < 0.1, 0, g.integers(1, 500, 70))
+    lens[-1] = 499
+    a = Prompt(32, 8, 128, lens.tolist())
+    o, st = a.run()
+    assert st == 0
+    a.check(o, heads=[0, 17, 31])
 
 
 def test_prompt_bad_sequences():
