@@ -316,7 +316,9 @@ int ft_kv_move_paged_int4(const ft_block_cfg *cfg, void *pages, int n_pages, int
  *   y = gamma * x / sqrt(mean x^2 + cfg->rms_eps) per head (gamma: FP32 [d]; NULL: y = x),
  *   z_i = y_i cos a - y_(i+d/2) sin a,  z_(i+d/2) = y_(i+d/2) cos a + y_i sin a,  i < d/2,
  *   a = positions[t] cfg->rope_base^(-2i/d),
- * the pairing, the frequencies and the exact reduction of the angles being the decode block's.
+ * the pairing, the frequencies and the reduction of the angles being the decode block's: a turn's fraction a
+ * position, computed in FP64, times the position, modulo one turn without a loss.  The angle's error is that of
+ * the fraction, |position| 2^-54 max(1, 1 / rope_base) turns (2^-23 at position 2^31), and FP32's below.
  * positions: int32 [total], any values (tokens of a tree share them).  With a norm, |x| < 2^60. */
 
 /* q_out, k_out: z rounded once to BF16, rows at their own strides; an output may be its input where the
