@@ -119,6 +119,11 @@ inline bool units_fit(const AttnPagedParams& p) {
 
 // The prefix sums (the first CTA), and the query rows rotated and rounded to FP16 (the others): D / 32 lanes a row, 32
 // channels a lane.
+//
+// The kernel behind this one reads tables, masks and pages as constants (__ldg, ld.global.nc), which a kernel that lives
+// beside its predecessor must not do.  It may here: this kernel lets it begin only behind its own wait, when all that came
+// before the call is complete, and writes nothing of them itself.  What it does write (records, queries) is read by L2
+// loads.  A kernel for attention that began beside the caller's kernels would have to read all of it by ordinary loads.
 constexpr int kPrepThreads = 128;  // (four warps)
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const AttnPagedParams p, const Split sp) {
