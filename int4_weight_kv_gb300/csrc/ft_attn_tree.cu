@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const AttnPagedParams
     int page_next = -1, page = 0;
     bool there = false, there_next = false;
     uint32_t sc = 0u, sc_next = 0u;
+    // (tables, masks and pages as constants: see tree_prepare_kernel)
     auto look_up = [&] {  // the pages of the tile behind `next` (raw entries; positions behind the end, and no tile: -1)
       step();
       const int pos = kKeys * ahead.j + 32 * w4 + lane;

@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) tree_few_kernel(const AttnPa
       if (tid < kMaxRows) row_m[tid] = -INFINITY, row_u[tid] = kPBias;
       // The bytes of tile i, K by one half, V by the other, 16 threads for each 16 positions, which are on one page: K entries
       // (chunks turned so that 8 lanes' reads meet 8 banks), V as it is; pages outside the pool and behind the end are page 0
-      // (no scale, and hidden).  Pages are looked up a tile further ahead.
+      // (no scale, and hidden).  Pages are looked up a tile further ahead.  (Tables and pages as constants: see
+      // tree_prepare_kernel.)
       const int grp = t >> 4, in = t & 15;
       const uint32_t ring = sm32 + C::kOffRing + grp * (16 * D / 2) + half * (kKeys * D / 2);
       const uint32_t even = ring + (D == 128 && half == 0 ? (in >> 2) * 64 + (((in & 3) ^ (in >> 3)) << 4) : 16 * in);

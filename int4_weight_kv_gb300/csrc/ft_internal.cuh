@@ -45,7 +45,8 @@ __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.
 // complete, and what comes next may take its places (it waits here in its turn).  Such a kernel lives
 // while its predecessor still writes, so whatever that may have produced (lengths, slots, pages, rows,
 // logits) is not constant to it: ordinary or __ldcg loads, which stay behind this wait and see all that
-// was written before it, never __ldg or ld.global.nc.
+// was written before it, never __ldg or ld.global.nc (but for what was complete when its predecessor passed
+// its own wait: ft_attn_tree.cuh).
 __device__ __forceinline__ void griddep_serve() {
   griddep_wait();
   griddep_launch();
