@@ -18,6 +18,10 @@ namespace tree {
 using namespace tiles;
 
 constexpr int kRows = 256, kKeys = 128;
+// Units that a share has at least.  2 / 3 / 6 / 12 / 24 (us): one tree of 7 tokens over 64 positions 11.5 / 11.4 / 15.3 / 23.0 /
+// 38.9, over 4096 14.8 / 15.7 / 19.7 / 26.2 / 41.8, 32 of up to 7 over up to 200 18.5 / 18.5 / 23.6 / 27.4 / 39.5, over up to 4096
+// 44.5 but for 24 (58.3); one of 64 tokens over 300 17.4 / 19.7 / 22.2 / 25.8 / 34.1, over 32768 85.5 for all.  So 2 or 3
+// would do better by small trees and worse by none of these.
 constexpr int kMinShare = 6;
 constexpr int kPartHead = 8;  // a partial: 4 unused, max, sum, 2 unused, accumulator (at a 32-byte boundary)
 
@@ -250,7 +254,9 @@ cudaError_t launch_prepare(const AttnPagedParams& p, const Split& sp, cudaStream
 }
 template <int D>
 cudaError_t launch_join(const AttnPagedParams& p, const Split& sp, cudaStream_t st) {
-  // four warps a row where a row may have more than twelve partials (a warp loads eight at once)
+  // Four warps a row where a row may have more than twelve partials (a warp loads eight at once).  One warp / this rule /
+  // four (us): one tree of 4 tokens, 64 heads over 8, over 32768 positions 35.1 / 32.1 / 32.1, of 64 85.4 / 85.5 / 93.8; 32 of
+  // up to 7 over up to 4096 44.6 / 44.6 / 54.6.  From 6 partials on: 93.8 for the tree of 64; from 24 on: as from 12.
   const int rows = p.max_q * p.G;
   const bool wide = ((int64_t)p.total_q * p.G / kRows + std::min(p.B, p.total_q)) * p.L.nkv * 12 < sp.ctas;
   const int groups = wide ? rows : (rows + 3) / 4;

@@ -17,8 +17,10 @@
 // Every wait is bounded; a timeout sets FT_DEV_TIMEOUT and the CTA winds down.
 //
 // Measured, 32 requests of up to 4096 positions, 7 tokens (28 rows) of 32 heads over 8: 45 us of the call's three kernels
-// (65 MB, 1459 GB/s), of which 5 are the kernel before and 8 the joining one; lengths of 64: 23.  Bound by instructions:
-// 535 a warp and tile (44% of the issue slots), of them a third decode.  With four working warps it was 52 and 60.
+// (65 MB, 1459 GB/s), of which 5 are the kernel before and 8 the joining one; lengths of 64: 23.  Neither the issue slots
+// (45%) nor HBM (22%) are at their end: what bounds it is the chain of a tile, 535 instructions a warp of which a third
+// decode, with two CTAs an SM to cover it (26% of the warps resident; 96 registers, 40 bytes of them spilled).  With four
+// working warps it was 52 and 60.
 #include "ft_attn_tree.cuh"
 
 namespace ft {

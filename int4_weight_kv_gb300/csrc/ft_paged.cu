@@ -422,8 +422,9 @@ __global__ void __launch_bounds__(kRowThreads, 9) read_paged_kernel(const PagedR
 // any is written.  An entry goes in pieces of d/8 bytes: four of K, eight of V (a chunk of a pair of
 // positions, of which every other halfword is this one's) and the scales.  Where both positions of a
 // pair are written by neighbouring moves, one of the two stores the whole chunk.  256 requests of up to 32
-// moves, 8 heads of 128: 7.8 us (word by word 15.8); one request's few: 3.5, the latency of slots, entries
-// and barrier.
+// moves, 8 heads of 128: 7.8 us (word by word 15.8): a thread has up to four pieces (416 of 128 threads), each a
+// load that is waited for before the next, and as many stores behind the barrier; one request's few: 3.5, the
+// latency of slots, entries and barrier.
 constexpr int kMoveThreads = 128, kMoveMax = 256, kMovePieces = 13;
 
 struct MoveParams {

@@ -312,7 +312,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap map_q, const _
     regs_down<kRegOther>();
     if (warp == kLoadWarp) {
       // ---------------------------------------------------------- what to work on, and copies
-      // Item x is (block of tokens, head) x of all sequences' blocks.  With up to 32 sequences the blocks that see most
+      // Item x is (block of tokens, head) x of all sequences' blocks.  With up to 32 sequences (a lane each) the blocks that see most
       // come first: those of the same place in their sequences together, from the last place on (8 prompts of up to 2048:
       // 92 -> 85 us); else each sequence's last ones first.  The grid has a CTA for each; those that run take the places
       // of those that have not begun.

@@ -4,8 +4,9 @@
 //   y = gamma x / sqrt(mean x^2 + eps),   z_i = y_i cos a - y_(i+d/2) sin a,  z_(i+d/2) = y_(i+d/2) cos a + y_i sin a
 //
 // Every byte is moved once.  Measured, 32 heads over 8 of 128: norm and rotation of 17k tokens 62 us, 83% of the copy rate
-// (bound by HBM), of 32 tokens 3.1; placement of 9k tokens' k and v, with q's on the way and norms, 56 us (bound by
-// instructions: the exact quantiser and the shuffles of the rotation by H).
+// (bound by HBM), of 32 tokens 3.1; placement of 9k tokens' k and v, with q's on the way and norms, 56 us, 1.9 times what
+// the bytes take: neither the issue slots (50%) nor HBM (39%) are at their end, there is too little in flight (27% of the
+// warps resident, for their 80 registers, of which 88 bytes are spilled; 2.5 waves of CTAs).
 #include <algorithm>
 
 #include "ft_paged.cuh"
@@ -15,6 +16,8 @@ namespace ft {
 // D / 16 lanes per row: lane c owns channels 8 c .. 8 c + 7 and d/2 + 8 c .. d/2 + 8 c + 7, two 16-byte
 // pieces, so that the pairs of the rotation meet in one lane.  A CTA has 4 (8) consecutive tokens, their angles in
 // shared memory, and a warp of its four goes through `per` heads of them.
+// Heads at most, 4 / 8 / 12 / 16 (us): rows of 17k tokens 67.6 / 63.2 / 61.3 / 61.3, placement of 9k with reading back
+// 73.1 / 71.5 / 69.9 / 69.9.
 constexpr int kRopeThreads = 128, kRopeHeads = 12;
 // tensors whose rows are at 16-byte boundaries
 enum { kWideQ = 1, kWideK = 2, kWideV = 4, kWideQOut = 8, kWideKOut = 16 };
@@ -224,6 +227,7 @@ __device__ __forceinline__ void rope_place(const RopeRows& p, f32x2 (&x)[8], boo
   if (slot >= 0 && c == 0) *reinterpret_cast<uint16_t*>(blk + p.L.soff + 4 * pos + (is_v ? 2 : 0)) = sb;
 }
 
+// CTAs an SM, rows 6 / 7 / 8: 63.9 / 61.3 / 65.7 us for 17k tokens; placement 5 / 6 / 7: 75.5 / 69.9 / 75.0 for 9k.
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kRopeThreads, PAGED ? 6 : 7) rope_rows_kernel(const __grid_constant__ RopeRows p) {
   constexpr int LV = D / 16, R = 32 / LV, W = kRopeThreads / 32;
@@ -347,8 +351,11 @@ static int launch_rope(const ft_block_cfg& c, RopeRows& p, bool paged, cudaStrea
   const int rows = 512 / c.head_dim;
   const int64_t groups = ((int64_t)p.total + rows - 1) / rows;
   constexpr int W = kRopeThreads / 32;
-  // heads of a warp: as many as leave every SM some warps, the warps' shares equal
-  const int most = (int)std::min<int64_t>(kRopeHeads, std::max<int64_t>(1, groups * p.heads / (152 * 48)));
+  // Heads of a warp: as many as leave every SM 48 warps, the warps' shares equal.  24 / 48 / 96 warps (us): 2048 tokens'
+  // rows 10.3 / 12.6 / 17.7, placement with reading back 24.8 / 23.7 / 29.6; 17k and 9k tokens alike.
+  int sms = ft_host::num_sms();
+  if (sms <= 0) sms = 152;
+  const int most = (int)std::min<int64_t>(kRopeHeads, std::max<int64_t>(1, groups * p.heads / ((int64_t)sms * 48)));
   const int chunks = (p.heads + W * most - 1) / (W * most);
   p.per = (p.heads + W * chunks - 1) / (W * chunks);
   const int64_t blocks = groups * ((p.heads + W * p.per - 1) / (W * p.per));
